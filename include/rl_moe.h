@@ -71,6 +71,14 @@ typedef enum rl_status {
     RL_ERR_TIMEOUT = 4      /* reserved for host-visible bounded-wait expiry */
 } rl_status;
 
+/* element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_logprobs) */
+typedef enum rl_dtype {
+    RL_F32 = 0,
+    RL_F16 = 1,
+    RL_BF16 = 2,
+    RL_F8_E4M3 = 3 /* 8-bit floats (4 exponent, 3 mantissa bits, largest 448) with f32 group scales */
+} rl_dtype;
+
 #define RL_NO_EARLY_OUT 0x7fffffff
 #define RL_ABI_VERSION 1
 
@@ -357,6 +365,100 @@ rl_status moe_prefill_chunk_f32(const rl_moe_shape *shp, int32_t layer, int32_t 
                                 const uint64_t *slots, const float *weights, const int8_t *codebook,
                                 float *y, int32_t accumulate, int32_t *ctrl, void *ws,
                                 size_t ws_bytes, void *stream);
+
+/*
+ * moe_decode_tokens - one whole layer (router, experts, combine) for a FEW tokens, T <= 32, in
+ * ONE launch: drafted tokens verified together, or sequences decoded side by side.  For every
+ * token t the work of rl_route and moe_decode,
+ *   logits[t] = w_router xn_t (+ bias),  ids/weights/slots[t] as rl_route,
+ *   y[t][h] = (accumulate ? y[t][h] : 0) + sum_{k in order} weights[t][k] * o_{t,k}[h],
+ *   xn = x (norm_eps < 0) or RMSNorm(x) with unit gain and that eps (norm_eps >= 0),
+ * reading each distinct selected expert once however many tokens share it ("Red Lite dev21 -
+ * GPU-routed decode", "What changed": router and experts of a decode step with no host round
+ * trip; "Red Lite dev20", "What changed", item 3: pairs sorted by expert, sums in selection
+ * order).  Arithmetic at f32 accuracy: the router's dots in f32, the experts on the tensor cores
+ * with every activation as an exact sum of three bf16 values and f32 accumulation.
+ * Misses: if any token selects an absent expert, ids, weights and slots of all tokens are
+ * written, miss[layer] += the number of such selections, ctrl[0] = min(ctrl[0], layer), and y is
+ * left as it was; after a fill and rl_resolve_slots the experts run through the same call with
+ * w_router = NULL.  Does nothing when ctrl[0] < layer.
+ * w_router = NULL: ids, weights and slots are inputs and only the experts run (as moe_decode:
+ * does nothing when ctrl[0] <= layer; a zero slot sets RL_DEVERR_MISSING, an id outside
+ * [0, n_experts) RL_DEVERR_BAD_ID, and y is left as it was; equal ids have equal slots).
+ * x [T][H] f32; w_router [E][H] f32 or NULL; bias [E] f32 or NULL; residency uint64
+ * [n_layers][E]; codebook int8 [256][8]; ids int32, weights f32, slots uint64: [T][K]; miss
+ * uint32 [n_layers]; logits_out f32 [T][E] or NULL; y [T][H] f32 (may be x).  x, w_router and ws
+ * 16-byte aligned.  residency and miss may be NULL when w_router is.  T = 0 does nothing.
+ * ws: moe_decode_tokens_workspace_bytes(shp, T) bytes, zero-filled before its first use (a
+ * grid-barrier counter that grows across calls; calls with any T may share a workspace large
+ * enough for the largest, but must not overlap on the GPU); after RL_DEVERR_WAIT_TIMEOUT it must
+ * be zero-filled again.  Bytes 64..71 are test knobs as in moe_decode_stack (a poll limit; a CTA
+ * n - 1 that leaves before its first arrival), zero in normal use.  Cooperative launch, one CTA per
+ * SM; it may be captured in a CUDA graph.
+ */
+#define RL_MAX_DECODE_TOKENS 32
+size_t moe_decode_tokens_workspace_bytes(const rl_moe_shape *shp, int32_t T);
+rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, int32_t T, const float *x, float norm_eps,
+                            const float *w_router, const float *bias, const uint64_t *residency,
+                            const int8_t *codebook, int32_t *ids, float *weights, uint64_t *slots, uint32_t *miss,
+                            int32_t *ctrl, float *logits_out, float *y, int32_t accumulate, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/*
+ * rl_add_rmsnorm - residual addition and RMSNorm of T rows of width H, with an 8-bit copy:
+ *   s = x + res (res NULL: s = x), rounded to the row type;  x_out = s
+ *   v = s / sqrt(mean(s^2) + eps) * gain (gain NULL: 1), in f32;  xn = v rounded to the row type
+ *   per group of `group` consecutive values: scale = max|v| / 448,  q = e4m3(v * (448 / max|v|)),
+ *   round to nearest even (q = 0 and scale = 0 for a group of zeros; a group that holds an
+ *   infinity or a NaN gets scale NaN and q = 0).
+ * Unlike rl_rmsnorm the squares are summed in plain f32 (rescaled when they leave its range), for
+ * any magnitude of x.  x, res, x_out, xn: [T][H] of `dtype` (RL_F32, RL_F16, RL_BF16); gain f32
+ * [H]; q e4m3 bytes [T][H]; scale f32 [T][H / group]; group 32, 64 or 128.  x_out, xn and the pair
+ * (q, scale) may each be NULL, not all; x_out or xn may be x or res itself, but not each other.
+ * All 16-byte aligned (scale: 4).  H a multiple of 8 (of `group` with q), at most 16384; T >= 0.
+ */
+rl_status rl_add_rmsnorm(const void *x, const void *res, const float *gain, int32_t dtype, int32_t T, int32_t H,
+                         float eps, void *x_out, void *xn, uint8_t *q, float *scale, int32_t group, void *stream);
+
+/*
+ * rl_q4_matvec - products of an N x K matrix of 4-bit weights with T activation rows (shared-expert
+ * projections, an output head):
+ *   y[t][n] = (accumulate ? y[t][n] : 0) + sum_k (q[n][k] - 8) * w_scale[n][k / group] * x[t][k].
+ * w: uint8 [N][K / 2], byte i of a row holds q[2i] in its low and q[2i + 1] in its high four bits;
+ * w_scale IEEE half [N][K / group]; group 32, 64 or 128, K a multiple of it, K <= 8192, N <= 2^26.
+ * x [T][K] of x_dtype: RL_F32, RL_F16, RL_BF16, or RL_F8_E4M3 with x_scale f32 [T][K / group] (else
+ * NULL), as rl_add_rmsnorm writes them with the same group.  y [T][N] of y_dtype (not
+ * RL_F8_E4M3), rounded once.  f32 accumulation; f32 activations carry at least 22 bits relative to
+ * the largest of their group.  An infinity or a NaN in x reaches its own token's outputs only.
+ * Any T >= 0; weights are read once per 32 (or, with f32 x or a small matrix, 16 or 8) columns.
+ * w, w_scale, x 16-byte aligned; y must not overlap an input.
+ */
+rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t N, int32_t K, int32_t group, const void *x,
+                       int32_t x_dtype, const float *x_scale, int32_t T, void *y, int32_t y_dtype, int32_t accumulate,
+                       void *stream);
+
+/*
+ * rl_logprobs - log probability of given tokens, entropy and most probable tokens of T rows of V
+ * logits, in one pass:
+ *   lse = log sum_v e^logits[t][v];  logprob[t] = logits[t][targets[t]] - lse
+ *   entropy[t] = lse - sum_v p_v logits[t][v],  p_v = e^(logits[t][v] - lse)
+ *   top_ids[t][0..top_n-1]: the largest logits in descending order, equal values (-0.0 == +0.0) to
+ *   the lower index;  top_logprob = their logit - lse.
+ * A logit of -infinity has probability 0.  A row of -infinities only has no distribution: its log
+ * probabilities are -infinity, its entropy 0, its top_ids the lowest indices.  A NaN or +infinity
+ * makes the row's log probabilities and entropy NaN (in top_ids NaN ranks below every number).  A
+ * target outside [0, V) is not looked up: logprob NaN.
+ * logits [T][V] of `dtype` (RL_F32, RL_F16, RL_BF16), aligned to their element; targets int32 [T]
+ * with logprob f32 [T], or both NULL; entropy f32 [T] or NULL; 0 <= top_n <= min(32, V), top_ids
+ * int32 and top_logprob f32 [T][top_n] (NULL with top_n = 0).  V <= 2^30, T >= 0.
+ * ws: rl_logprobs_workspace_bytes(T, V, top_n) bytes, 16-byte aligned, zero-filled before its first
+ * use (every call leaves its completion counters at zero, so calls of any sizes may share a
+ * workspace large enough for the largest, but must not overlap on the GPU).
+ */
+size_t rl_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t top_n);
+rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, int32_t V, const int32_t *targets, float *logprob,
+                      float *entropy, int32_t top_n, int32_t *top_ids, float *top_logprob, void *ws, size_t ws_bytes,
+                      void *stream);
 
 #ifdef __cplusplus
 }

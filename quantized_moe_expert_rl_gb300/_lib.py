@@ -24,7 +24,11 @@ EXPORTS = ("rl_abi_version", "rl_last_error", "rl_record_bytes", "rl_rmsnorm", "
            "rl_build_pairs_workspace_bytes", "rl_build_pairs", "moe_prefill_workspace_bytes",
            "moe_prefill_chunk", "moe_prefill_chunk_f32", "moe_decode_static", "moe_decode_stack_workspace_bytes",
            "moe_decode_stack", "rl_fill_workspace_bytes", "rl_fill_missing", "rl_host_device_pointer",
-           "moe_decode_stack_fill", "moe_decode_layer")
+           "moe_decode_stack_fill", "moe_decode_layer", "moe_decode_tokens_workspace_bytes", "moe_decode_tokens",
+           "rl_add_rmsnorm", "rl_q4_matvec", "rl_logprobs_workspace_bytes", "rl_logprobs")
+
+RL_F32, RL_F16, RL_BF16, RL_F8_E4M3 = 0, 1, 2, 3
+RL_MAX_DECODE_TOKENS = 32
 
 
 class RlShape(ctypes.Structure):
@@ -78,6 +82,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "moe_decode_stack_fill": (i32, [shp, i32, i32, vp, f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                         vp, vp, sz, vp]),
         "moe_decode_layer": (i32, [shp, i32, vp, f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_decode_tokens_workspace_bytes": (sz, [shp, i32]),
+        "moe_decode_tokens": (i32, [shp, i32, i32, vp, f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz,
+                                    vp]),
+        "rl_add_rmsnorm": (i32, [vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, i32, vp]),
+        "rl_q4_matvec": (i32, [vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, i32, i32, vp]),
+        "rl_logprobs_workspace_bytes": (sz, [i32, i32, i32]),
+        "rl_logprobs": (i32, [vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
         "rl_fill_workspace_bytes": (sz, [shp]),
         "rl_fill_missing": (i32, [shp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "rl_host_device_pointer": (i32, [vp, ctypes.POINTER(ctypes.c_uint64)]),
@@ -208,6 +219,88 @@ def moe_decode_layer(shape, layer, x, norm_eps, w_router, bias, residency, codeb
         ctypes.byref(shape), layer, ptr(x), float(norm_eps), ptr(w_router), ptr(bias), ptr(residency), ptr(codebook),
         ptr(ids), ptr(weights), ptr(slots), ptr(miss), ptr(ctrl), ptr(logits_out), ptr(y), ptr(ws), ws_bytes,
         _stream(stream)))
+
+
+def moe_decode_tokens_workspace_bytes(shape, T) -> int:
+    return load().moe_decode_tokens_workspace_bytes(ctypes.byref(shape), T)
+
+
+def moe_decode_tokens(shape, layer, T, x, norm_eps, w_router, bias, residency, codebook, ids, weights, slots, miss,
+                      ctrl, logits_out, y, accumulate, ws, ws_bytes, stream=None):
+    _check("moe_decode_tokens", load().moe_decode_tokens(
+        ctypes.byref(shape), layer, T, ptr(x), float(norm_eps), ptr(w_router), ptr(bias), ptr(residency),
+        ptr(codebook), ptr(ids), ptr(weights), ptr(slots), ptr(miss), ptr(ctrl), ptr(logits_out), ptr(y),
+        int(accumulate), ptr(ws), ws_bytes, _stream(stream)))
+
+
+_dtypes = None
+
+
+def _typed(what: str, t, allowed, numel: int | None = None) -> int:
+    """RL_* code of a tensor's type; refuses other types than `allowed` and, with `numel`, other
+    sizes (the library only sees an address)."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: RL_F32, torch.float16: RL_F16, torch.bfloat16: RL_BF16,
+                   torch.float8_e4m3fn: RL_F8_E4M3}
+    code = _dtypes.get(t.dtype, -1)
+    if code not in allowed:
+        raise ValueError(f"{what}: a tensor of type {t.dtype} is not supported here")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{what}: {numel} values expected, got shape {tuple(t.shape)}")
+    return code
+
+
+def _sized(what: str, t, itemsize: int, numel: int) -> None:
+    if t is not None and (t.element_size() != itemsize or t.numel() != numel):
+        raise ValueError(f"{what}: {numel} items of {itemsize} bytes expected, got {t.dtype} {tuple(t.shape)}")
+
+
+_ROW = (RL_F32, RL_F16, RL_BF16)
+
+
+def rl_add_rmsnorm(x, T, H, eps, res=None, gain=None, x_out=None, xn=None, q=None, scale=None, group=128, stream=None):
+    """x (+ res) -> x_out, RMSNorm (* gain) -> xn and, in 8 bits with group scales, (q, scale); any output
+    may be None.  The row type is x's."""
+    dt = _typed("x", x, _ROW, T * H)
+    for what, t in (("res", res), ("x_out", x_out), ("xn", xn)):
+        if t is not None and _typed(what, t, _ROW, T * H) != dt:
+            raise ValueError(f"{what}: type {t.dtype} differs from x's {x.dtype}")
+    if gain is not None:
+        _typed("gain", gain, (RL_F32,), H)
+    if q is not None:
+        _sized("q", q, 1, T * H)
+    if scale is not None and group > 0:
+        _typed("scale", scale, (RL_F32,), T * (H // group))
+    _check("rl_add_rmsnorm", load().rl_add_rmsnorm(ptr(x), ptr(res), ptr(gain), dt, T, H, eps, ptr(x_out), ptr(xn),
+                                                   ptr(q), ptr(scale), group, _stream(stream)))
+
+
+def rl_q4_matvec(w, w_scale, x, y, T, N, K, group, x_scale=None, accumulate=0, stream=None):
+    """y [T][N] (+)= x [T][K] times the 4-bit matrix (w, w_scale) transposed; types from the tensors, x in
+    e4m3 with x_scale [T][K / group]."""
+    xdt, ydt = _typed("x", x, (*_ROW, RL_F8_E4M3), T * K), _typed("y", y, _ROW, T * N)
+    _sized("w", w, 1, N * K // 2)
+    if group > 0:
+        _typed("w_scale", w_scale, (RL_F16,), N * (K // group))
+        if x_scale is not None:
+            _typed("x_scale", x_scale, (RL_F32,), T * (K // group))
+    _check("rl_q4_matvec", load().rl_q4_matvec(ptr(w), ptr(w_scale), N, K, group, ptr(x), xdt, ptr(x_scale), T, ptr(y),
+                                               ydt, accumulate, _stream(stream)))
+
+
+def rl_logprobs_workspace_bytes(T, V, top_n) -> int:
+    return load().rl_logprobs_workspace_bytes(T, V, top_n)
+
+
+def rl_logprobs(logits, T, V, targets, logprob, entropy, top_n, top_ids, top_logprob, ws, ws_bytes, stream=None):
+    dt = _typed("logits", logits, _ROW, T * V)
+    for what, t, n in (("targets", targets, T), ("logprob", logprob, T), ("entropy", entropy, T),
+                       ("top_ids", top_ids, T * top_n), ("top_logprob", top_logprob, T * top_n)):
+        _sized(what, t, 4, n)
+    _check("rl_logprobs", load().rl_logprobs(ptr(logits), dt, T, V, ptr(targets), ptr(logprob), ptr(entropy), top_n,
+                                             ptr(top_ids), ptr(top_logprob), ptr(ws), ws_bytes, _stream(stream)))
 
 
 def rl_build_pairs_workspace_bytes(shape, T) -> int:

@@ -1,0 +1,188 @@
+// add_norm.cu - rl_add_rmsnorm: residual addition, RMSNorm and an e4m3 copy with group scales, one
+// pass over the row.
+//
+//   s = x + res (rounded to the row type: the residual stream as it is kept)
+//   v = s / sqrt(mean(s^2) + eps) * gain,  xn = round(v)
+//   scale_g = max_{h in g} |v_h| / 448,  q_h = e4m3(v_h * (448 / max_g))
+//
+// A row is read once and stays in registers: a thread owns NC runs of 8 consecutive values (one
+// 16-byte load of a 16-bit row), so that a group of 32 / 64 / 128 values is 4 / 8 / 16 neighbouring
+// lanes and its maximum takes 2 to 4 shuffles; the sum of squares takes one CTA barrier.  Rows of
+// fewer than 256 threads share a CTA of about 256 threads.
+#include "qdot.cuh"
+#include "row_types.cuh"
+
+using namespace rl;
+
+namespace {
+
+constexpr int kNormMaxH = 16384;
+
+struct NormArgs {
+    const void *x, *res;
+    const float *gain;
+    void *x_out, *xn;
+    uint8_t *q;
+    float *scale;
+    float eps;
+    int T, H, tpr, rows, group;  // threads per row (a multiple of 32), rows per CTA
+};
+
+// sum (or maximum) of v over the threads of a row: warps of the row through shared memory
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float *part, int warp0, int nwarps) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(kFull, v, o);
+        v = MAX ? fmaxf(v, w) : v + w;
+    }
+    if (nwarps == 1) return v;
+    __syncthreads();  // an earlier reduction's values have been read
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = part[warp0];
+    for (int i = 1; i < nwarps; ++i) r = MAX ? fmaxf(r, part[warp0 + i]) : r + part[warp0 + i];
+    return r;
+}
+
+template <typename E, int NC>
+__global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
+    __shared__ float part[32];
+    const int rowi = threadIdx.x / a.tpr, tr = threadIdx.x - rowi * a.tpr;
+    const int row = blockIdx.x * a.rows + rowi, nw = a.tpr >> 5, w0 = rowi * nw;
+    const int lane = threadIdx.x & 31;
+    const size_t base = (size_t)row * a.H;
+    const bool live = row < a.T;
+    pdl_wait();
+    pdl_trigger();
+    float s[NC][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int h = 8 * (c * a.tpr + tr);
+        const bool in = live && h < a.H;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[c][j] = 0.f;
+        if (in) {
+            load8(static_cast<const E *>(a.x) + base + h, s[c]);
+            if (a.res) {
+                float r[8];
+                load8(static_cast<const E *>(a.res) + base + h, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[c][j] = to_float(from_float<E>(s[c][j] + r[j]));
+            }
+            if (a.x_out) store8(static_cast<E *>(a.x_out) + base + h, s[c]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(s[c][j], s[c][j], ss);
+    }
+    ss = row_reduce<false>(ss, part, w0, nw);
+    float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    // Squares outside the f32 range (values beyond about 1e18, or all below about 1e-15): the sum is
+    // taken again over values scaled by a power of two.  The vote makes the branch uniform.
+    const bool odd = live && !(ss < 1e37f && ss > 1e-30f * (float)a.H);
+    if (__syncthreads_or(odd)) {
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[c][j]));
+        m = row_reduce<true>(m, part, w0, nw);
+        int ex = 0;
+        const bool fin = m > 0.f && m < __int_as_float(0x7f800000);
+        if (fin) frexpf(m, &ex);
+        float s2 = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = ldexpf(s[c][j], -ex);
+                s2 = fmaf(v, v, s2);
+            }
+        s2 = row_reduce<false>(s2, part, w0, nw);
+        if (odd && fin && s2 == s2)
+            r = (float)(1.0 / sqrt(ldexp((double)s2 / a.H, 2 * ex) + (double)a.eps));
+    }
+    const int gl = a.group >> 3;  // lanes per group
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int h = 8 * (c * a.tpr + tr);
+        const bool in = live && h < a.H;
+        float v[8];
+        if (a.gain && in) {
+            load8(a.gain + h, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= s[c][j] * r;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s[c][j] * r;
+        }
+        if (a.xn && in) store8(static_cast<E *>(a.xn) + base + h, v);
+        if (!a.q) continue;
+        // largest magnitude as an integer: a NaN or infinity ranks above every number and stays visible
+        uint32_t mb = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[j]) & 0x7fffffffu);
+        for (int o = 1; o < gl; o <<= 1) mb = max(mb, __shfl_xor_sync(kFull, mb, o));
+        if (!in) continue;
+        float m = __uint_as_float(mb), up = 1.f;
+        float sc = m / 448.0f, inv = 0.f;
+        if (mb >= 0x7f800000u) {  // a group holding an infinity or a NaN: scale NaN, q 0
+            sc = __int_as_float(0x7fffffff);
+        } else if (m > 0.f) {
+            if (m < 1e-30f) up = 18446744073709551616.0f, m *= up;  // 448 / m must stay finite
+            inv = 448.0f / m;
+        }
+        uint2 o8 = make_uint2(0u, 0u);
+        if (inv > 0.f) {
+            o8.x = pack4_e4m3(v[0] * up * inv, v[1] * up * inv, v[2] * up * inv, v[3] * up * inv);
+            o8.y = pack4_e4m3(v[4] * up * inv, v[5] * up * inv, v[6] * up * inv, v[7] * up * inv);
+        }
+        *reinterpret_cast<uint2 *>(a.q + base + h) = o8;
+        if ((lane & (gl - 1)) == 0) a.scale[(size_t)row * (a.H / a.group) + h / a.group] = sc;
+    }
+}
+
+template <typename E>
+rl_status launch_norm(NormArgs &a, cudaStream_t s) {
+    const int oct = a.H / 8;
+    const int nc = oct > 1024 ? 2 : 1;
+    a.tpr = (int)align_up((size_t)(oct + nc - 1) / nc, 32);
+    a.rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
+    if (a.rows > a.T) a.rows = a.T;
+    const dim3 grid((a.T + a.rows - 1) / a.rows), block(a.tpr * a.rows);
+    return nc == 2 ? launch_pdl(add_norm_kernel<E, 2>, grid, block, 0, s, "rl_add_rmsnorm", a)
+                   : launch_pdl(add_norm_kernel<E, 1>, grid, block, 0, s, "rl_add_rmsnorm", a);
+}
+
+}  // namespace
+
+extern "C" rl_status rl_add_rmsnorm(const void *x, const void *res, const float *gain, int32_t dtype, int32_t T,
+                                    int32_t H, float eps, void *x_out, void *xn, uint8_t *q, float *scale,
+                                    int32_t group, void *stream) {
+    if (dtype != RL_F32 && dtype != RL_F16 && dtype != RL_BF16)
+        return fail(RL_ERR_INVALID, "rl_add_rmsnorm: dtype %d is none of RL_F32, RL_F16, RL_BF16", dtype);
+    if (T < 0 || H <= 0 || !(eps >= 0.f)) return fail(RL_ERR_INVALID, "rl_add_rmsnorm: T=%d H=%d eps=%g", T, H, eps);
+    if (H % 8 != 0 || H > kNormMaxH)
+        return fail(RL_ERR_UNSUPPORTED, "rl_add_rmsnorm: H=%d is not a multiple of 8 up to %d", H, kNormMaxH);
+    if (q && !(group == 32 || group == 64 || group == 128))
+        return fail(RL_ERR_UNSUPPORTED, "rl_add_rmsnorm: group=%d: supported 32, 64, 128", group);
+    if (q && H % group != 0)
+        return fail(RL_ERR_INVALID, "rl_add_rmsnorm: H=%d is not a multiple of group=%d", H, group);
+    if (T == 0) return RL_OK;
+    if (!x) return fail(RL_ERR_INVALID, "rl_add_rmsnorm: NULL x");
+    if ((q == nullptr) != (scale == nullptr))
+        return fail(RL_ERR_INVALID, "rl_add_rmsnorm: q and scale come together");
+    if (!x_out && !xn && !q) return fail(RL_ERR_INVALID, "rl_add_rmsnorm: no output");
+    if (x_out && x_out == xn) return fail(RL_ERR_INVALID, "rl_add_rmsnorm: x_out and xn are the same buffer");
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(res) | reinterpret_cast<uintptr_t>(gain) |
+         reinterpret_cast<uintptr_t>(x_out) | reinterpret_cast<uintptr_t>(xn) | reinterpret_cast<uintptr_t>(q)) & 15)
+        return fail(RL_ERR_INVALID, "rl_add_rmsnorm: x, res, gain, x_out, xn and q must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(scale) & 3)
+        return fail(RL_ERR_INVALID, "rl_add_rmsnorm: scale must be 4-byte aligned");
+    NormArgs a = {x, res, gain, x_out, xn, q, scale, eps, T, H, 0, 0, q ? group : 32};
+    cudaStream_t s = as_stream(stream);
+    if (dtype == RL_F32) return launch_norm<float>(a, s);
+    if (dtype == RL_F16) return launch_norm<__half>(a, s);
+    return launch_norm<__nv_bfloat16>(a, s);
+}

@@ -1,0 +1,432 @@
+// q4_matvec.cu - rl_q4_matvec: products of a matrix of 4-bit weights with group scales and a few
+// activation rows.
+//
+//   y[t][n] (+)= sum_g ws[n][g] * xs[t][g] * sum_{k in g} (q[n][k] - 8) * x[t][k]
+//
+// For a few rows the product is bound by the weights' bytes, so the work per weight has to stay
+// below about 2.8 lane instructions (128 lanes per clock and SM against 45 weights per clock and SM
+// at the measured HBM rate):
+//
+// - Two nibbles 16 bits apart become a pair of MMA operands in two instructions.  One AND-OR puts
+//   them under the exponent of 1024, where a half's last bit is 1: bits 0-3 give 1024 + q, bits 4-7
+//   give 1024 + 16 q; one packed add (-1032) or multiply-add (/16 - 72) gives q - 8, exactly.  (Read
+//   as subnormal halves the nibbles would need no second instruction, but the tensor core aligns its
+//   products by exponent, and subnormals leave the upper bits of its window empty: with f32
+//   activations the error was 3.3e-6 instead of 1e-7.)
+// - mma.m16n8k16 takes 16 weight rows as A and 8 activation columns as B, f32 accumulation.
+// - The order of k inside a group is free as long as A and B agree, so the words go to the MMA as
+//   they lie in memory (ldmatrix hands lane (g, t) word t of row g), 8 values of k per word.
+// - Activations are laid out as B fragments once per CTA.  e4m3 values are exact in half precision;
+//   f16 and bf16 rows are scaled by a power of two per group (largest magnitude to 2^14), f32 rows
+//   are scaled the same way and split into two halves (22 bits and more) in two columns.
+//
+// Weights stream through per-warp rings of 16-byte asynchronous copies (16 rows x 256 values per
+// stage), swizzled so that ldmatrix meets no bank conflict.  W warps share a 16-row tile and add
+// their partial sums in a fixed order; results do not depend on timing.
+#include "qdot.cuh"
+#include "row_types.cuh"
+
+using namespace rl;
+
+namespace {
+
+constexpr int kQ4Threads = 512, kQ4Warps = kQ4Threads / 32;
+constexpr int kQ4Stage = 16 * 128 + 16 * 16;  // 16 rows x 256 nibbles, then 16 bytes of scales per row
+constexpr int kQ4MaxStages = 6;
+constexpr int kQ4MaxK = 8192;
+
+struct Q4Args {
+    const uint8_t *w;
+    const __half *ws;
+    const void *x;
+    const float *xs;
+    void *y;
+    int N, K, T, group, xdt, ydt, acc;
+    int KC, W, stages, wide;  // stages of 256 values per row, warps per tile, ring depth, scales by wide copies
+};
+
+struct Q4Layout {
+    size_t o_sc, o_ring, o_red, total;
+    Q4Layout(int KC, int NT, int split, int group, int W, int stages) {
+        o_sc = (size_t)KC * 8 * NT * 512;
+        o_ring = o_sc + align_up((size_t)KC * (256 / group) * NT * (split ? 4 : 8) * sizeof(float), 128);
+        o_red = o_ring + (size_t)kQ4Warps * stages * kQ4Stage;
+        total = o_red + (W > 1 ? (size_t)2 * kQ4Warps * NT * (split ? 256 : 512) : 0);
+    }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int B>
+__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n copy groups have landed (n < kQ4MaxStages - 1)
+__device__ __forceinline__ void cp_async_wait(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    }
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// d += a (16 x 16, half) * b (16 x 8, half), f32 accumulation
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 activations k = 8 o .. 8 o + 7 of token `tok` as f32; zero outside the matrix
+__device__ __forceinline__ void q4_load_x(const Q4Args &a, int tok, int o, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    if (tok >= a.T || 8 * o >= a.K) return;
+    const size_t at = (size_t)tok * a.K + 8 * o;
+    if (a.xdt == RL_F32) {
+        load8(static_cast<const float *>(a.x) + at, v);
+    } else if (a.xdt == RL_F16) {
+        load8(static_cast<const __half *>(a.x) + at, v);
+    } else if (a.xdt == RL_BF16) {
+        load8(static_cast<const __nv_bfloat16 *>(a.x) + at, v);
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t two = ((j < 2 ? q.x : q.y) >> (16 * (j & 1))) & 0xffffu;
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 q4_fragment(const float (&v)[8]) {
+    return make_uint4(pack2(v[0], v[4], __half()), pack2(v[1], v[5], __half()), pack2(v[2], v[6], __half()),
+                      pack2(v[3], v[7], __half()));
+}
+
+// Lay the activations out as B fragments: the 16 bytes of (32-value chunk c, column n, quarter t)
+// at 16 * ((c * 8 NT + n) * 4 + t), so that the lanes of a warp read 512 consecutive bytes; and the
+// scale of every (group, token).
+template <int NT, bool SPLIT>
+__device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *sc) {
+    constexpr int TOK = NT * (SPLIT ? 4 : 8);
+    const int KO = a.KC * 32, gl = a.group >> 3;
+    for (int i = threadIdx.x; i < TOK * KO; i += kQ4Threads) {  // KO is a multiple of 32: whole warps
+        const int tok = i / KO, o = i - tok * KO;
+        float v[8];
+        q4_load_x(a, tok, o, v);
+        float mult = 1.f, xs = 1.f;
+        if (a.xdt == RL_F8_E4M3) {
+            xs = tok < a.T && 8 * o < a.K ? a.xs[(size_t)tok * (a.K / a.group) + 8 * o / a.group] : 0.f;
+        } else {
+            uint32_t mb = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[j]) & 0x7fffffffu);
+            for (int d = 1; d < gl; d <<= 1) mb = max(mb, __shfl_xor_sync(kFull, mb, d));
+            // 2^14 over the power of two at or below the largest magnitude (at most 2^127)
+            const int e = (int)(mb >> 23);
+            mult = __uint_as_float((uint32_t)min(268 - e, 254) << 23);
+            xs = 1.0f / mult;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= mult;
+        }
+        uint8_t *at = bs + ((size_t)(o >> 2) * NT * 8 + (SPLIT ? 2 * tok : tok)) * 64 + (o & 3) * 16;
+        if (SPLIT) {
+            float lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float hi = __half2float(__float2half_rn(v[j]));
+                lo[j] = v[j] - hi;
+                v[j] = hi;
+            }
+            *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
+            *reinterpret_cast<uint4 *>(at + 64) = q4_fragment(lo);
+        } else {
+            *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
+        }
+        if ((o & (gl - 1)) == 0) sc[(o / gl) * TOK + tok] = xs;
+    }
+}
+
+// q - 8 for the nibbles at bits 0-3 (LO) or 4-7 of both 16-bit halves of w, as a pair of halves
+template <bool LO>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
+    constexpr uint32_t m = LO ? 0x000f000fu : 0x00f000f0u;
+    const uint32_t biased = (w & m) | 0x64006400u;
+    const __half2 h = *reinterpret_cast<const __half2 *>(&biased);
+    const __half2 r = LO ? __hadd2(h, __floats2half2_rn(-1032.f, -1032.f))
+                         : __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-72.f, -72.f));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Copy stage `st` of the 16 rows from row0 into a ring slot; rows and values outside read as zero.
+__device__ __forceinline__ void q4_issue(const Q4Args &a, uint8_t *slot, int row0, int st) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(slot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 3) + 4 * i, j = lane & 7, k = (st * 8 + j) * 32;
+        const bool in = row0 + r < a.N && k < a.K;
+        const uint8_t *src = in ? a.w + (size_t)(row0 + r) * (a.K / 2) + k / 2 : a.w;
+        cp_async16(base + r * 128 + ((j ^ (r & 7)) << 4), src, in ? 16 : 0);
+    }
+    const int gs = 256 / a.group, G = a.K / a.group;  // groups per stage and per row
+    if (a.wide) {
+        if (lane < 16) {
+            const bool in = row0 + lane < a.N;
+            const __half *src = in ? a.ws + (size_t)(row0 + lane) * G + st * gs : a.ws;
+            const uint32_t dst = base + 2048 + lane * 16;
+            if (gs == 8) cp_async_ca<16>(dst, src, in ? 16 : 0);
+            else if (gs == 4) cp_async_ca<8>(dst, src, in ? 8 : 0);
+            else cp_async_ca<4>(dst, src, in ? 4 : 0);
+        }
+    } else {
+        __half *d = reinterpret_cast<__half *>(slot + 2048);
+        for (int i = lane; i < 16 * gs; i += 32) {
+            const int r = i / gs, g = st * gs + i % gs;
+            d[r * 8 + i % gs] = row0 + r < a.N && g < G ? a.ws[(size_t)(row0 + r) * G + g] : __half();
+        }
+    }
+}
+
+__device__ __forceinline__ void q4_store(const Q4Args &a, int tok, int row, float v) {
+    if (tok >= a.T || row >= a.N) return;
+    const size_t at = (size_t)tok * a.N + row;
+    if (a.ydt == RL_F32) {
+        float *y = static_cast<float *>(a.y) + at;
+        *y = a.acc ? *y + v : v;
+    } else if (a.ydt == RL_F16) {
+        __half *y = static_cast<__half *>(a.y) + at;
+        *y = __float2half_rn(a.acc ? __half2float(*y) + v : v);
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + at;
+        *y = __float2bfloat16_rn(a.acc ? __bfloat162float(*y) + v : v);
+    }
+}
+
+// NT: column tiles of 8; SPLIT: f32 activations in two columns; GL: 32-value chunks per group
+template <int NT, bool SPLIT, int GL>
+__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const Q4Layout lay) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int TOK = NT * (SPLIT ? 4 : 8);
+    constexpr int YV = SPLIT ? 2 : 4;  // outputs per lane and column tile
+    float *sc = reinterpret_cast<float *>(smem + lay.o_sc);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int grp = warp / a.W, sub = warp - grp * a.W, ngrp = kQ4Warps / a.W;
+    const int tiles = (a.N + 15) / 16, first = grp * gridDim.x + blockIdx.x, step = ngrp * gridDim.x;
+    uint8_t *ring = smem + lay.o_ring + (size_t)warp * a.stages * kQ4Stage;
+    pdl_wait();
+    pdl_trigger();
+    // fill the ring; a commit per stage keeps the group count fixed
+    int ptile = first, pst = sub, pslot = 0;
+    auto issue_next = [&]() {
+        if (ptile < tiles) {
+            q4_issue(a, ring + pslot * kQ4Stage, ptile * 16, pst);
+            pst += a.W;
+            if (pst >= a.KC) pst = sub, ptile += step;
+        }
+        cp_async_commit();
+        if (++pslot == a.stages) pslot = 0;
+    };
+    for (int s = 0; s < a.stages - 1; ++s) issue_next();
+    const uint32_t bs = smem_addr(smem) + lane * 16;
+    q4_stage_x<NT, SPLIT>(a, smem, sc);
+    __syncthreads();
+    // ldmatrix: lane l addresses row (l & 7) + 8 (bit 3 of l) of 16-byte piece 2 jj + (l >> 4)
+    const int lr = (lane & 7) + ((lane >> 3) & 1) * 8, lp = lane >> 4;
+    const uint32_t lrow = smem_addr(ring) + lr * 128;
+    int slot = 0, parity = 0;
+    for (int tile = first; tile < tiles; tile += step) {
+        float y[NT][YV];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < YV; ++i) y[n][i] = 0.f;
+        for (int st = sub; st < a.KC; st += a.W) {
+            cp_async_wait(a.stages - 2);
+            __syncwarp();  // every lane's copies of this stage; the stage before has been read
+            issue_next();
+            const uint32_t sb = lrow + slot * kQ4Stage;
+            const uint8_t *wsp = ring + slot * kQ4Stage + 2048 + g * 16;
+            float acc[NT][4];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                uint32_t r[4];
+                ldmatrix4(r, sb + (((2 * jj + lp) ^ (lr & 7)) << 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = 2 * jj + h;
+                    if (c % GL == 0) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                    }
+                    const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1], v0 = w0 >> 8, v1 = w1 >> 8;
+                    const uint32_t a0 = q4_pair<true>(w0), a1 = q4_pair<true>(w1), a2 = q4_pair<false>(w0),
+                                   a3 = q4_pair<false>(w1), a4 = q4_pair<true>(v0), a5 = q4_pair<true>(v1),
+                                   a6 = q4_pair<false>(v0), a7 = q4_pair<false>(v1);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 b = lds128(bs + ((st * 8 + c) * NT + n) * 512);
+                        mma_f16(acc[n], a0, a1, a2, a3, b.x, b.y);
+                        mma_f16(acc[n], a4, a5, a6, a7, b.z, b.w);
+                    }
+                    if (c % GL == GL - 1) {
+                        const int gi = c / GL;
+                        const float s0 = __half2float(*reinterpret_cast<const __half *>(wsp + 2 * gi));
+                        const float s1 = __half2float(*reinterpret_cast<const __half *>(wsp + 128 + 2 * gi));
+                        const float *p = sc + (st * (8 / GL) + gi) * TOK;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if (SPLIT) {
+                                const float q = p[n * 4 + t];
+                                y[n][0] = fmaf(s0 * q, acc[n][0] + acc[n][1], y[n][0]);
+                                y[n][1] = fmaf(s1 * q, acc[n][2] + acc[n][3], y[n][1]);
+                            } else {
+                                const float2 q = *reinterpret_cast<const float2 *>(p + n * 8 + 2 * t);
+                                y[n][0] = fmaf(s0 * q.x, acc[n][0], y[n][0]);
+                                y[n][1] = fmaf(s0 * q.y, acc[n][1], y[n][1]);
+                                y[n][YV - 2] = fmaf(s1 * q.x, acc[n][2], y[n][YV - 2]);
+                                y[n][YV - 1] = fmaf(s1 * q.y, acc[n][3], y[n][YV - 1]);
+                            }
+                        }
+                    }
+                }
+            }
+            if (++slot == a.stages) slot = 0;
+        }
+        // output i of column tile n: row g (+ 8 in the second half), token
+        auto put = [&](int n, int i, int ln, float v) {
+            const int row = tile * 16 + (ln >> 2) + (i >= YV / 2 ? 8 : 0);
+            const int tok = SPLIT ? n * 4 + (ln & 3) : n * 8 + 2 * (ln & 3) + (i & 1);
+            q4_store(a, tok, row, v);
+        };
+        if (a.W == 1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < YV; ++i) put(n, i, lane, y[n][i]);
+            continue;
+        }
+        // the W warps of the tile: partial sums through shared memory, two buffers in turn (a warp
+        // that writes buffer p again has passed the barrier after everybody read it)
+        constexpr int RV = NT * YV * 32;
+        float *red = reinterpret_cast<float *>(smem + lay.o_red) + parity * kQ4Warps * RV + grp * a.W * RV;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < YV; ++i) red[sub * RV + (n * YV + i) * 32 + lane] = y[n][i];
+        asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(a.W * 32) : "memory");
+        for (int e = sub; e < NT * YV; e += a.W) {
+            float v = 0.f;
+            for (int k = 0; k < a.W; ++k) v += red[k * RV + e * 32 + lane];
+            put(e / YV, e % YV, lane, v);
+        }
+        parity ^= 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+struct Q4Plan {
+    int NT, W, stages;
+};
+
+// NT column tiles: as few as hold the tokens of the launch.  W = 8 warps per tile (fewer for a short
+// K) keeps the tail of the tile loop short; four column tiles leave no room for the partial
+// sums, so they run one warp per tile, and only where the tiles fill every warp of the GPU.
+bool q4_plan(int N, int K, int cols, int group, bool split, Q4Plan &p) {
+    const int KC = (K + 255) / 256, tiles = (N + 15) / 16;
+    const size_t room = 227 * 1024;
+    p.NT = cols > 16 && tiles >= 152 * kQ4Warps ? 4 : cols > 8 ? 2 : 1;
+    for (; p.NT >= 1; p.NT >>= 1) {
+        p.W = 1;
+        if (p.NT < 4)
+            while (p.W < 8 && 2 * p.W <= KC) p.W *= 2;
+        for (; p.W >= 1; p.W >>= 1)
+            for (p.stages = kQ4MaxStages; p.stages >= 2; --p.stages)
+                if (Q4Layout(KC, p.NT, split, group, p.W, p.stages).total <= room) return true;
+    }
+    return false;
+}
+
+template <int NT, bool SPLIT>
+rl_status launch_q4(const Q4Args &a, const Q4Layout &lay, cudaStream_t s) {
+    const int tiles = (a.N + 15) / 16, sms = sm_count();
+    const dim3 grid(tiles < sms ? tiles : sms), block(kQ4Threads);
+    if (a.group == 32) return launch_pdl(q4_kernel<NT, SPLIT, 1>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+    if (a.group == 64) return launch_pdl(q4_kernel<NT, SPLIT, 2>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+    return launch_pdl(q4_kernel<NT, SPLIT, 4>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+}
+
+}  // namespace
+
+extern "C" rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t N, int32_t K, int32_t group,
+                                  const void *x, int32_t x_dtype, const float *x_scale, int32_t T, void *y,
+                                  int32_t y_dtype, int32_t accumulate, void *stream) {
+    if (x_dtype != RL_F32 && x_dtype != RL_F16 && x_dtype != RL_BF16 && x_dtype != RL_F8_E4M3)
+        return fail(RL_ERR_INVALID, "rl_q4_matvec: unknown x_dtype %d", x_dtype);
+    if (y_dtype != RL_F32 && y_dtype != RL_F16 && y_dtype != RL_BF16)
+        return fail(RL_ERR_INVALID, "rl_q4_matvec: y_dtype %d is none of RL_F32, RL_F16, RL_BF16", y_dtype);
+    if (N <= 0 || K <= 0 || T < 0) return fail(RL_ERR_INVALID, "rl_q4_matvec: N=%d K=%d T=%d", N, K, T);
+    if (!(group == 32 || group == 64 || group == 128))
+        return fail(RL_ERR_UNSUPPORTED, "rl_q4_matvec: group=%d: supported 32, 64, 128", group);
+    if (K % group != 0) return fail(RL_ERR_INVALID, "rl_q4_matvec: K=%d is not a multiple of group=%d", K, group);
+    if (K > kQ4MaxK) return fail(RL_ERR_UNSUPPORTED, "rl_q4_matvec: K=%d > %d", K, kQ4MaxK);
+    if (N > (1 << 26)) return fail(RL_ERR_UNSUPPORTED, "rl_q4_matvec: N=%d > 2^26", N);
+    if (T == 0) return RL_OK;
+    if (!w || !w_scale || !x || !y) return fail(RL_ERR_INVALID, "rl_q4_matvec: NULL buffer");
+    if ((x_dtype == RL_F8_E4M3) != (x_scale != nullptr))
+        return fail(RL_ERR_INVALID, "rl_q4_matvec: x_scale comes with RL_F8_E4M3 activations");
+    if ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(w_scale) | reinterpret_cast<uintptr_t>(x)) & 15)
+        return fail(RL_ERR_INVALID, "rl_q4_matvec: w, w_scale and x must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(x_scale) & 3 || reinterpret_cast<uintptr_t>(y) % dtype_bytes(y_dtype))
+        return fail(RL_ERR_INVALID, "rl_q4_matvec: x_scale or y misaligned");
+    const bool split = x_dtype == RL_F32;
+    const int per = split ? 2 : 1;  // columns per token
+    cudaStream_t s = as_stream(stream);
+    for (int t0 = 0; t0 < T;) {
+        Q4Plan p;
+        if (!q4_plan(N, K, (T - t0) * per < 32 ? (T - t0) * per : 32, group, split, p))
+            return fail(RL_ERR_UNSUPPORTED, "rl_q4_matvec: K=%d does not fit", K);
+        const int most = 8 * p.NT / per;
+        Q4Args a = {};
+        a.w = w;
+        a.ws = static_cast<const __half *>(w_scale);
+        a.x = static_cast<const uint8_t *>(x) + (size_t)t0 * K * dtype_bytes(x_dtype);
+        a.xs = x_scale ? x_scale + (size_t)t0 * (K / group) : nullptr;
+        a.y = static_cast<uint8_t *>(y) + (size_t)t0 * N * dtype_bytes(y_dtype);
+        a.N = N;
+        a.K = K;
+        a.T = T - t0 < most ? T - t0 : most;
+        a.group = group;
+        a.xdt = x_dtype;
+        a.ydt = y_dtype;
+        a.acc = accumulate != 0;
+        a.KC = (K + 255) / 256;
+        a.W = p.W;
+        a.stages = p.stages;
+        a.wide = K % 256 == 0;
+        const Q4Layout lay(a.KC, p.NT, split, group, p.W, p.stages);
+        const rl_status st = p.NT == 4   ? (split ? launch_q4<4, true>(a, lay, s) : launch_q4<4, false>(a, lay, s))
+                             : p.NT == 2 ? (split ? launch_q4<2, true>(a, lay, s) : launch_q4<2, false>(a, lay, s))
+                                         : (split ? launch_q4<1, true>(a, lay, s) : launch_q4<1, false>(a, lay, s));
+        if (st != RL_OK) return st;
+        t0 += a.T;
+    }
+    return RL_OK;
+}

@@ -240,6 +240,108 @@ def enqueue_decode_token_fused(model: Model, b: DecodeBuffers, x_in: torch.Tenso
 
 
 @dataclass
+class TokensBuffers:
+    """Buffers of a step of up to `T` tokens through every layer (moe_decode_tokens)."""
+    ids: torch.Tensor        # [L][T][K] int32
+    weights: torch.Tensor    # [L][T][K] f32
+    slots: torch.Tensor      # [L][T][K] u64 (as int64)
+    miss: torch.Tensor       # [L] u32 (as int32)
+    ctrl: torch.Tensor       # [2] int32
+    ws: torch.Tensor         # zero-filled: grid-barrier counter of moe_decode_tokens
+
+    @staticmethod
+    def make(model: Model, T: int) -> "TokensBuffers":
+        w, d = model.w, model.device
+        if not 1 <= T <= L.RL_MAX_DECODE_TOKENS:
+            raise ValueError(f"{T} tokens: a step holds 1 to {L.RL_MAX_DECODE_TOKENS}")
+        shape = (model.L, T, w.top_k)
+        return TokensBuffers(
+            ids=torch.zeros(shape, dtype=torch.int32, device=d), weights=torch.zeros(shape, device=d),
+            slots=torch.zeros(shape, dtype=torch.int64, device=d),
+            miss=torch.zeros(model.L, dtype=torch.int32, device=d),
+            ctrl=torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32, device=d),
+            ws=torch.zeros(L.moe_decode_tokens_workspace_bytes(model.shape, T), dtype=torch.uint8, device=d))
+
+
+def enqueue_tokens_layer(model: Model, b: TokensBuffers, layer: int, x: torch.Tensor, y: torch.Tensor,
+                         stacked: bool, routed: bool = True, logits: torch.Tensor | None = None) -> None:
+    """One layer for the b.ids.shape[1] tokens x [T][H], router and experts in ONE launch:
+    stacked: y = x + MoE(RMSNorm(x)) in place (y is x), else y = MoE(x).  routed=False runs the
+    experts with the ids and weights b holds (after a fill and rl_resolve_slots)."""
+    T = b.ids.shape[1]
+    L.moe_decode_tokens(model.shape, layer, T, x, EPS if stacked else -1.0, model.routers[layer] if routed else None,
+                        None if model.bias is None else model.bias[layer], model.table, model.codebook, b.ids[layer],
+                        b.weights[layer], b.slots[layer], b.miss, b.ctrl, logits, y, int(stacked), b.ws, b.ws.numel())
+
+
+def enqueue_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out: torch.Tensor, layer0: int = 0) -> None:
+    """Stacked decode of a few tokens, one launch per layer: y_out = x_in, then for layers
+    [layer0, L) y_out += MoE(RMSNorm(y_out)).  A layer in which some token selects an absent
+    expert raises the flag and later layers do nothing (run_bounded_tokens fills and resumes)."""
+    if y_out.data_ptr() != x_in.data_ptr():
+        y_out.copy_(x_in)
+    for l in range(layer0, model.L):
+        enqueue_tokens_layer(model, b, l, y_out, y_out, stacked=True)
+
+
+def pack_q4(weight: torch.Tensor, group: int = 128) -> tuple[torch.Tensor, torch.Tensor]:
+    """A float matrix [N][K] in the format of rl_q4_matvec: (w uint8 [N][K / 2], scale half
+    [N][K / group]), each group's largest magnitude mapped to 7."""
+    N, K = weight.shape
+    v = weight.float().view(N, K // group, group)
+    scale = (v.abs().amax(2) / 7).clamp(max=65504).half()
+    s = scale.float()[:, :, None]
+    q = torch.where(s > 0, torch.round(v / s.clamp_min(2.0 ** -24)), torch.zeros_like(v)).clamp(-8, 7) + 8
+    q = q.to(torch.uint8).view(N, K)
+    return (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous(), scale
+
+
+@dataclass
+class Head:
+    """The end of a verification step: final RMSNorm with gain into 8 bits, an output head in 4
+    bits, log probabilities.  Buffers for up to T tokens."""
+    w: torch.Tensor            # uint8 [V][H / 2]
+    scale: torch.Tensor        # half [V][H / group]
+    gain: torch.Tensor | None  # f32 [H]
+    group: int
+    q: torch.Tensor            # e4m3 [T][H]
+    q_scale: torch.Tensor      # f32 [T][H / group]
+    logits: torch.Tensor       # f32 [T][V]
+    logprob: torch.Tensor      # f32 [T]
+    entropy: torch.Tensor      # f32 [T]
+    top_ids: torch.Tensor | None
+    top_logprob: torch.Tensor | None
+    ws: torch.Tensor           # zero-filled: completion counters of rl_logprobs
+
+    @staticmethod
+    def make(weight: torch.Tensor, T: int, gain: torch.Tensor | None = None, group: int = 128, top_n: int = 0) -> "Head":
+        V, H = weight.shape
+        d = weight.device
+        w, scale = pack_q4(weight, group)
+        f = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, device=d)  # noqa: E731
+        return Head(w=w, scale=scale, gain=gain, group=group, q=f(T, H, dtype=torch.float8_e4m3fn),
+                    q_scale=f(T, H // group), logits=f(T, V), logprob=f(T), entropy=f(T),
+                    top_ids=f(T, top_n, dtype=torch.int32) if top_n else None,
+                    top_logprob=f(T, top_n) if top_n else None,
+                    ws=f(L.rl_logprobs_workspace_bytes(T, V, top_n), dtype=torch.uint8))
+
+
+def enqueue_verify(model: Model, b: TokensBuffers, head: Head, x_in: torch.Tensor, y_out: torch.Tensor,
+                   targets: torch.Tensor) -> None:
+    """A few tokens through every layer and the output head: y_out as enqueue_tokens, then
+    head.logits = head(RMSNorm(y_out)) and the log probabilities of `targets` (int32 [T]), the
+    entropies and the most probable tokens.  Valid when b.ctrl still reads (RL_NO_EARLY_OUT, 0)."""
+    T, H = x_in.shape
+    V = head.logits.shape[1]
+    enqueue_tokens(model, b, x_in, y_out)
+    L.rl_add_rmsnorm(y_out, T, H, EPS, gain=head.gain, q=head.q, scale=head.q_scale, group=head.group)
+    L.rl_q4_matvec(head.w, head.scale, head.q, head.logits, T, V, H, head.group, x_scale=head.q_scale)
+    L.rl_logprobs(head.logits, T, V, targets, head.logprob, head.entropy,
+                  0 if head.top_ids is None else head.top_ids.shape[1], head.top_ids, head.top_logprob, head.ws,
+                  head.ws.numel())
+
+
+@dataclass
 class DecodeStats:
     early_outs: list        # layers at which the chain stopped for a fill
     filled: list            # (layer, expert) filled at a stop
@@ -312,6 +414,37 @@ def run_bounded_decode_token(model: Model, b: DecodeBuffers, x_in: torch.Tensor,
                 absent = sorted({e for e in row if not model.resident[la, e]})
                 st.fill_bytes += model.fill(la, absent)
                 st.prefetched += [(la, e) for e in absent]
+        l0 = f + 1
+    return st
+
+
+def run_bounded_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out: torch.Tensor) -> DecodeStats:
+    """A few tokens through every layer with bounded residency: enqueue the layers; where some
+    token of layer f selects an absent expert the flag stops the chain with y_out = x_f, the host
+    fills the layer's missing experts, re-resolves the slots, runs the layer with the ids and
+    weights the GPU selected, and goes on at f + 1.  The caller zeroes b.miss; b.ctrl is reset here."""
+    T = b.ids.shape[1]
+    b.ctrl.copy_(torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32))
+    y_out.copy_(x_in)
+    st = DecodeStats([], [], 0, 0)
+    l0 = 0
+    while l0 < model.L:
+        enqueue_tokens(model, b, y_out, y_out, l0)
+        ctrl = b.ctrl.tolist()
+        st.syncs += 1
+        if ctrl[1] != 0:
+            raise RuntimeError(f"moe_decode_tokens: device error bits {ctrl[1]:#x}")
+        f = ctrl[0]
+        if f == RL_NO_EARLY_OUT:
+            break
+        ids, slots = b.ids[f].flatten().tolist(), b.slots[f].flatten().tolist()
+        missing = sorted({e for e, s in zip(ids, slots) if s == 0})
+        st.fill_bytes += model.fill(f, missing)
+        st.filled += [(f, e) for e in missing]
+        st.early_outs.append(f)
+        L.rl_resolve_slots(model.shape, f, T, b.ids[f], model.table, b.slots[f])
+        b.ctrl[0] = RL_NO_EARLY_OUT
+        enqueue_tokens_layer(model, b, f, y_out, y_out, stacked=True, routed=False)
         l0 = f + 1
     return st
 

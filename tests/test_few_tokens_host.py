@@ -1,0 +1,143 @@
+"""The operators of a step of a few tokens (moe_decode_tokens, rl_add_rmsnorm, rl_q4_matvec,
+rl_logprobs): refusals made on the host before any launch, and the packing of 4-bit weights.  No
+GPU needed."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from quantized_moe_expert_rl_gb300 import _lib, build
+    build.build()
+    return _lib.load()
+
+
+INVALID, UNSUPPORTED = 1, 2
+FAKE, ODD = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
+
+
+def _with(args, **changes):
+    out = dict(args)
+    out.update(changes)
+    return list(out.values())
+
+
+def test_moe_decode_tokens_refusals(lib):
+    from quantized_moe_expert_rl_gb300._lib import RlShape
+    s = RlShape.of(2048, 512, 10, 512, 4)
+    need = lib.moe_decode_tokens_workspace_bytes(ctypes.byref(s), 32)
+    assert need >= 32 * 512 * 4 + 32 * 2048 * 6 + 320 * 512 * 6
+    assert lib.moe_decode_tokens_workspace_bytes(ctypes.byref(s), 33) == 0
+    assert lib.moe_decode_tokens_workspace_bytes(ctypes.byref(s), 0) == 0
+    base = dict(shape=ctypes.byref(s), layer=3, T=32, x=FAKE, eps=-1.0, w=FAKE, bias=None, table=FAKE, codebook=FAKE,
+                ids=FAKE, weights=FAKE, slots=FAKE, miss=FAKE, ctrl=FAKE, logits=None, y=FAKE, acc=0, ws=FAKE,
+                ws_bytes=need, stream=None)
+    call = lambda **c: lib.moe_decode_tokens(*_with(base, **c))  # noqa: E731
+    for c in (dict(layer=4), dict(layer=-1), dict(T=-1), dict(ws_bytes=need - 1), dict(ws=None), dict(ws=ODD),
+              dict(x=ODD), dict(w=ODD), dict(table=None), dict(miss=None), dict(w=None, logits=FAKE),
+              *[{k: None} for k in ("x", "codebook", "ids", "weights", "slots", "ctrl", "y")]):
+        assert call(**c) == INVALID, c
+        assert b"moe_decode_tokens" in lib.rl_last_error()
+    assert call(T=33) == UNSUPPORTED
+    bad = RlShape.of(384, 512, 10, 512, 4)
+    assert call(shape=ctypes.byref(bad)) == UNSUPPORTED
+    assert lib.moe_decode_tokens_workspace_bytes(ctypes.byref(bad), 4) == 0
+    assert call(T=0, x=None, y=None, ids=None, ws=None, ws_bytes=0) == 0
+
+
+def test_add_rmsnorm_refusals(lib):
+    base = dict(x=FAKE, res=FAKE, gain=FAKE, dtype=2, T=4, H=2048, eps=1e-6, x_out=FAKE, xn=FAKE, q=FAKE, scale=FAKE,
+                group=128, stream=None)
+    call = lambda **c: lib.rl_add_rmsnorm(*_with(base, **c))  # noqa: E731
+    base["xn"] = ctypes.c_void_p(1 << 21)
+    for c in (dict(dtype=3), dict(dtype=-1), dict(T=-1), dict(H=0), dict(eps=-1.0), dict(eps=float("nan")),
+              dict(x=None), dict(q=None), dict(scale=None), dict(x_out=None, xn=None, q=None, scale=None), dict(H=2080),
+              dict(xn=FAKE), *[{k: ODD} for k in ("x", "res", "gain", "x_out", "xn", "q", "scale")]):
+        assert call(**c) == INVALID, c
+        assert b"rl_add_rmsnorm" in lib.rl_last_error()
+    for c in (dict(H=2052), dict(H=16512), dict(group=16), dict(group=256)):
+        assert call(**c) == UNSUPPORTED, c
+    assert call(T=0, x=None, q=None, scale=None, xn=None, x_out=None) == 0
+
+
+def test_q4_matvec_refusals(lib):
+    base = dict(w=FAKE, ws=FAKE, N=100, K=512, group=64, x=FAKE, xdt=3, xs=FAKE, T=4, y=FAKE, ydt=0, acc=0, stream=None)
+    call = lambda **c: lib.rl_q4_matvec(*_with(base, **c))  # noqa: E731
+    for c in (dict(xdt=4), dict(xdt=-1), dict(ydt=3), dict(N=0), dict(K=0), dict(T=-1), dict(K=544), dict(w=None),
+              dict(ws=None), dict(x=None), dict(y=None), dict(xs=None), dict(xdt=0), dict(w=ODD), dict(ws=ODD),
+              dict(x=ODD), dict(xs=ODD), dict(y=ODD)):
+        assert call(**c) == INVALID, c
+        assert b"rl_q4_matvec" in lib.rl_last_error()
+    for c in (dict(group=16), dict(group=256, K=512), dict(K=8256), dict(N=(1 << 26) + 1)):
+        assert call(**c) == UNSUPPORTED, c
+    assert call(T=0, w=None, ws=None, x=None, xs=None, y=None) == 0
+
+
+def test_logprobs_refusals(lib):
+    need = lib.rl_logprobs_workspace_bytes(16, 100003, 20)
+    assert need > 0
+    assert lib.rl_logprobs_workspace_bytes(16, 100003, 33) == 0 and lib.rl_logprobs_workspace_bytes(0, 5, 1) == 0
+    base = dict(x=FAKE, dtype=1, T=16, V=100003, targets=FAKE, logprob=FAKE, entropy=FAKE, n=20, ids=FAKE, top=FAKE,
+                ws=FAKE, ws_bytes=need, stream=None)
+    call = lambda **c: lib.rl_logprobs(*_with(base, **c))  # noqa: E731
+    odd1 = ctypes.c_void_p((1 << 20) + 1)
+    for c in (dict(dtype=3), dict(T=-1), dict(V=0), dict(n=-1), dict(n=20, V=19), dict(x=None), dict(targets=None),
+              dict(logprob=None), dict(ids=None), dict(top=None), dict(n=0), dict(ws=None), dict(ws_bytes=need - 1),
+              dict(ws=ODD), dict(x=odd1), dict(targets=ODD), dict(entropy=ODD),
+              dict(targets=None, logprob=None, entropy=None, n=0, ids=None, top=None)):
+        assert call(**c) == INVALID, c
+        assert b"rl_logprobs" in lib.rl_last_error()
+    for c in (dict(n=33), dict(V=(1 << 30) + 1)):
+        assert call(**c) == UNSUPPORTED, c
+    assert call(T=0, x=None, targets=None, logprob=None, entropy=None, ids=None, top=None, ws=None, ws_bytes=0) == 0
+
+
+def test_workspace_is_enough_for_every_split(lib):
+    """More rows than one launch takes: the rest may be few rows in more segments."""
+    for T in (1, 5, 4096, 4097, 9000):
+        for V in (1, 4096, 131072):
+            full = lib.rl_logprobs_workspace_bytes(T, V, 32)
+            rest = T % 4096 or 4096
+            assert full >= lib.rl_logprobs_workspace_bytes(min(rest, T), V, 32)
+            assert full >= lib.rl_logprobs_workspace_bytes(min(T, 4096), V, 32)
+
+
+def test_binding_checks_types_and_sizes():
+    """The library sees addresses only: the binding refuses tensors of another type or size."""
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    x = torch.zeros(2, 256)
+    with pytest.raises(ValueError, match="x:"):
+        L.rl_add_rmsnorm(x.double(), 2, 256, 1e-6, xn=x)
+    with pytest.raises(ValueError, match="x:"):
+        L.rl_add_rmsnorm(x, 3, 256, 1e-6, xn=x)
+    with pytest.raises(ValueError, match="xn:"):
+        L.rl_add_rmsnorm(x, 2, 256, 1e-6, xn=x.half())
+    with pytest.raises(ValueError, match="gain:"):
+        L.rl_add_rmsnorm(x, 2, 256, 1e-6, gain=x[0].half(), xn=x)
+    w, ws, y = torch.zeros(5, 128, dtype=torch.uint8), torch.zeros(5, 2).half(), torch.zeros(2, 5)
+    with pytest.raises(ValueError, match="w_scale:"):
+        L.rl_q4_matvec(w, ws, x, y, 2, 5, 256, 64)
+    with pytest.raises(ValueError, match="w:"):
+        L.rl_q4_matvec(w[:4], ws, x, y, 2, 5, 256, 128)
+    with pytest.raises(ValueError, match="targets:"):
+        L.rl_logprobs(x, 2, 256, torch.zeros(2, dtype=torch.int64), y, None, 0, None, None, None, 0)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_pack_q4(group):
+    """Values come back within half a step of their group's scale (rounded to half precision, 2^-11
+    relative, times at most 7 steps), zeros as zeros, the byte order as documented."""
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300.engine import pack_q4
+    torch.manual_seed(3)
+    v = torch.randn(9, 256)
+    v[4] = 0
+    w, s = pack_q4(v, group)
+    assert w.shape == (9, 128) and w.dtype == torch.uint8 and s.shape == (9, 256 // group) and s.dtype == torch.float16
+    q = torch.stack((w & 15, w >> 4), 2).view(9, 256).float() - 8
+    back = q * s.float().repeat_interleave(group, 1)
+    step = s.float().repeat_interleave(group, 1)
+    assert torch.all((back - v).abs() <= step * (0.5 + 8 * 2.0 ** -11))
+    assert torch.all(back[4] == 0)
