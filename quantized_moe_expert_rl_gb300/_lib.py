@@ -117,10 +117,24 @@ def ptr(t) -> int | None:
     return t.data_ptr() or None
 
 
+_current = None  # (device index of the calling thread, raw current stream of a device)
+
+
+def _cuda():
+    """torch's raw lookups of the current device and stream: the Stream object that
+    torch.cuda.current_stream() builds costs more (4 us) than a whole launch."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _current
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        device, raw = _cuda()
+        return raw(device()) or None
     if isinstance(s, int):
         return s or None
     return s.cuda_stream or None
@@ -221,18 +235,6 @@ def moe_decode_layer(shape, layer, x, norm_eps, w_router, bias, residency, codeb
         _stream(stream)))
 
 
-def moe_decode_tokens_workspace_bytes(shape, T) -> int:
-    return load().moe_decode_tokens_workspace_bytes(ctypes.byref(shape), T)
-
-
-def moe_decode_tokens(shape, layer, T, x, norm_eps, w_router, bias, residency, codebook, ids, weights, slots, miss,
-                      ctrl, logits_out, y, accumulate, ws, ws_bytes, stream=None):
-    _check("moe_decode_tokens", load().moe_decode_tokens(
-        ctypes.byref(shape), layer, T, ptr(x), float(norm_eps), ptr(w_router), ptr(bias), ptr(residency),
-        ptr(codebook), ptr(ids), ptr(weights), ptr(slots), ptr(miss), ptr(ctrl), ptr(logits_out), ptr(y),
-        int(accumulate), ptr(ws), ws_bytes, _stream(stream)))
-
-
 _dtypes = None
 
 
@@ -257,24 +259,56 @@ def _sized(what: str, t, itemsize: int, numel: int) -> None:
         raise ValueError(f"{what}: {numel} items of {itemsize} bytes expected, got {t.dtype} {tuple(t.shape)}")
 
 
+def _ptrs(*tensors):
+    """Raw addresses of device tensors (None: NULL), all dense and on the current device, where the
+    call will launch."""
+    device = _cuda()[0]()
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+        if t.get_device() != device:
+            raise ValueError(f"tensor on {t.device} passed to a call on cuda:{device}")
+        out.append(t.data_ptr() or None)
+    return out
+
+
 _ROW = (RL_F32, RL_F16, RL_BF16)
+
+
+def moe_decode_tokens_workspace_bytes(shape, T) -> int:
+    return load().moe_decode_tokens_workspace_bytes(ctypes.byref(shape), T)
+
+
+def moe_decode_tokens(shape, layer, T, x, norm_eps, w_router, bias, residency, codebook, ids, weights, slots, miss,
+                      ctrl, logits_out, y, accumulate, ws, ws_bytes, stream=None):
+    x, w, bias, res, cb, ids, wt, slots, miss, ctrl, lg, y, ws = _ptrs(x, w_router, bias, residency, codebook, ids,
+                                                                       weights, slots, miss, ctrl, logits_out, y, ws)
+    _check("moe_decode_tokens", load().moe_decode_tokens(
+        ctypes.byref(shape), layer, T, x, norm_eps, w, bias, res, cb, ids, wt, slots, miss, ctrl, lg, y,
+        int(accumulate), ws, ws_bytes, _stream(stream)))
 
 
 def rl_add_rmsnorm(x, T, H, eps, res=None, gain=None, x_out=None, xn=None, q=None, scale=None, group=128, stream=None):
     """x (+ res) -> x_out, RMSNorm (* gain) -> xn and, in 8 bits with group scales, (q, scale); any output
     may be None.  The row type is x's."""
-    dt = _typed("x", x, _ROW, T * H)
+    n = T * H
+    dt = _typed("x", x, _ROW, n)
     for what, t in (("res", res), ("x_out", x_out), ("xn", xn)):
-        if t is not None and _typed(what, t, _ROW, T * H) != dt:
-            raise ValueError(f"{what}: type {t.dtype} differs from x's {x.dtype}")
+        if t is not None and (t.dtype != x.dtype or t.numel() != n):
+            raise ValueError(f"{what}: {n} values of {x.dtype} expected, got {t.dtype} {tuple(t.shape)}")
     if gain is not None:
         _typed("gain", gain, (RL_F32,), H)
     if q is not None:
-        _sized("q", q, 1, T * H)
+        _sized("q", q, 1, n)
     if scale is not None and group > 0:
         _typed("scale", scale, (RL_F32,), T * (H // group))
-    _check("rl_add_rmsnorm", load().rl_add_rmsnorm(ptr(x), ptr(res), ptr(gain), dt, T, H, eps, ptr(x_out), ptr(xn),
-                                                   ptr(q), ptr(scale), group, _stream(stream)))
+    x, res, gain, x_out, xn, q, scale = _ptrs(x, res, gain, x_out, xn, q, scale)
+    _check("rl_add_rmsnorm", load().rl_add_rmsnorm(x, res, gain, dt, T, H, eps, x_out, xn, q, scale, group,
+                                                   _stream(stream)))
 
 
 def rl_q4_matvec(w, w_scale, x, y, T, N, K, group, x_scale=None, accumulate=0, stream=None):
@@ -286,8 +320,9 @@ def rl_q4_matvec(w, w_scale, x, y, T, N, K, group, x_scale=None, accumulate=0, s
         _typed("w_scale", w_scale, (RL_F16,), N * (K // group))
         if x_scale is not None:
             _typed("x_scale", x_scale, (RL_F32,), T * (K // group))
-    _check("rl_q4_matvec", load().rl_q4_matvec(ptr(w), ptr(w_scale), N, K, group, ptr(x), xdt, ptr(x_scale), T, ptr(y),
-                                               ydt, accumulate, _stream(stream)))
+    w, w_scale, x, x_scale, y = _ptrs(w, w_scale, x, x_scale, y)
+    _check("rl_q4_matvec", load().rl_q4_matvec(w, w_scale, N, K, group, x, xdt, x_scale, T, y, ydt, accumulate,
+                                               _stream(stream)))
 
 
 def rl_logprobs_workspace_bytes(T, V, top_n) -> int:
@@ -296,11 +331,14 @@ def rl_logprobs_workspace_bytes(T, V, top_n) -> int:
 
 def rl_logprobs(logits, T, V, targets, logprob, entropy, top_n, top_ids, top_logprob, ws, ws_bytes, stream=None):
     dt = _typed("logits", logits, _ROW, T * V)
-    for what, t, n in (("targets", targets, T), ("logprob", logprob, T), ("entropy", entropy, T),
-                       ("top_ids", top_ids, T * top_n), ("top_logprob", top_logprob, T * top_n)):
-        _sized(what, t, 4, n)
-    _check("rl_logprobs", load().rl_logprobs(ptr(logits), dt, T, V, ptr(targets), ptr(logprob), ptr(entropy), top_n,
-                                             ptr(top_ids), ptr(top_logprob), ptr(ws), ws_bytes, _stream(stream)))
+    _sized("targets", targets, 4, T)
+    _sized("logprob", logprob, 4, T)
+    _sized("entropy", entropy, 4, T)
+    _sized("top_ids", top_ids, 4, T * top_n)
+    _sized("top_logprob", top_logprob, 4, T * top_n)
+    x, targets, logprob, entropy, ids, top, ws = _ptrs(logits, targets, logprob, entropy, top_ids, top_logprob, ws)
+    _check("rl_logprobs", load().rl_logprobs(x, dt, T, V, targets, logprob, entropy, top_n, ids, top, ws, ws_bytes,
+                                             _stream(stream)))
 
 
 def rl_build_pairs_workspace_bytes(shape, T) -> int:

@@ -41,6 +41,7 @@ __device__ __forceinline__ float row_reduce(float v, float *part, int warp0, int
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     float r = part[warp0];
+#pragma unroll 8
     for (int i = 1; i < nwarps; ++i) r = MAX ? fmaxf(r, part[warp0 + i]) : r + part[warp0 + i];
     return r;
 }
@@ -64,13 +65,8 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[c][j] = 0.f;
         if (in) {
-            load8(static_cast<const E *>(a.x) + base + h, s[c]);
-            if (a.res) {
-                float r[8];
-                load8(static_cast<const E *>(a.res) + base + h, r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[c][j] = to_float(from_float<E>(s[c][j] + r[j]));
-            }
+            if (a.res) add8(static_cast<const E *>(a.x) + base + h, static_cast<const E *>(a.res) + base + h, s[c]);
+            else load8(static_cast<const E *>(a.x) + base + h, s[c]);
             if (a.x_out) store8(static_cast<E *>(a.x_out) + base + h, s[c]);
         }
 #pragma unroll
@@ -81,7 +77,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
     // Squares outside the f32 range (values beyond about 1e18, or all below about 1e-15): the sum is
     // taken again over values scaled by a power of two.  The vote makes the branch uniform.
     const bool odd = live && !(ss < 1e37f && ss > 1e-30f * (float)a.H);
-    if (__syncthreads_or(odd)) {
+    if (a.rows == 1 ? odd : __syncthreads_or(odd)) {
         float m = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -119,24 +115,26 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
         }
         if (a.xn && in) store8(static_cast<E *>(a.xn) + base + h, v);
         if (!a.q) continue;
-        // largest magnitude as an integer: a NaN or infinity ranks above every number and stays visible
-        uint32_t mb = 0u;
+        float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[j]) & 0x7fffffffu);
-        for (int o = 1; o < gl; o <<= 1) mb = max(mb, __shfl_xor_sync(kFull, mb, o));
+        for (int j = 0; j < 8; ++j) m = max_abs_nan(m, v[j]);
+        for (int o = 1; o < gl; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
         if (!in) continue;
-        float m = __uint_as_float(mb), up = 1.f;
-        float sc = m / 448.0f, inv = 0.f;
-        if (mb >= 0x7f800000u) {  // a group holding an infinity or a NaN: scale NaN, q 0
-            sc = __int_as_float(0x7fffffff);
-        } else if (m > 0.f) {
-            if (m < 1e-30f) up = 18446744073709551616.0f, m *= up;  // 448 / m must stay finite
-            inv = 448.0f / m;
+        float sc = m / 448.0f, inv = 448.0f / m;
+        if (!(m >= 1e-30f && m < __int_as_float(0x7f800000))) {  // zeros, far below f32's range, infinity or NaN
+            inv = 0.f;
+            if (!(m < __int_as_float(0x7f800000))) {
+                sc = __int_as_float(0x7fffffff);
+            } else if (m > 0.f) {  // 448 / m must stay finite: scale both by 2^64
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= 18446744073709551616.0f;
+                inv = 448.0f / (m * 18446744073709551616.0f);
+            }
         }
         uint2 o8 = make_uint2(0u, 0u);
         if (inv > 0.f) {
-            o8.x = pack4_e4m3(v[0] * up * inv, v[1] * up * inv, v[2] * up * inv, v[3] * up * inv);
-            o8.y = pack4_e4m3(v[4] * up * inv, v[5] * up * inv, v[6] * up * inv, v[7] * up * inv);
+            o8.x = pack4_e4m3(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+            o8.y = pack4_e4m3(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
         }
         *reinterpret_cast<uint2 *>(a.q + base + h) = o8;
         if ((lane & (gl - 1)) == 0) a.scale[(size_t)row * (a.H / a.group) + h / a.group] = sc;
@@ -145,8 +143,10 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
 
 template <typename E>
 rl_status launch_norm(NormArgs &a, cudaStream_t s) {
+    // Two runs of 8 values per thread for rows of 2048 values and more, if there are rows enough to fill
+    // the GPU: the row's reduction and addressing then cost half as many instructions per value.
     const int oct = a.H / 8;
-    const int nc = oct > 1024 ? 2 : 1;
+    const int nc = oct > 1024 || (oct >= 256 && a.T >= 2 * 152) ? 2 : 1;
     a.tpr = (int)align_up((size_t)(oct + nc - 1) / nc, 32);
     a.rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
     if (a.rows > a.T) a.rows = a.T;

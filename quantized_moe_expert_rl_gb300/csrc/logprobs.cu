@@ -11,11 +11,12 @@
 // do not depend on arrival order.
 //
 // Top n.  A candidate is a 64-bit key, order-preserving logit above ~index, so that keys are
-// distinct and equal logits go to the lower index.  Only keys above a threshold are kept.  In a
-// tile whose survivors would overflow the buffer, the threshold is raised first: the CTA's 64
-// groups of 4 threads each publish their largest key, and the n-th largest of the 64 bounds the
-// tile's n-th largest from below, which leaves at most n groups x 64 values.  The buffer is cut
-// back to its n best whenever it holds more than 256, by counting for every key the larger ones.
+// distinct and equal logits go to the lower index.  Only keys above a threshold are kept, in a buffer
+// that is cut back to its n best whenever it holds more than 128, by counting for every key the
+// larger ones.  The first tile sets the threshold: the CTA's 64 groups of 4 threads each publish
+// their largest key, and the n-th largest of the 64 bounds the tile's n-th largest from below, which
+// leaves at most n groups x 64 values.  Later tiles put their few survivors straight into the buffer;
+// a tile that overflows it (rising logits) is taken back and goes the first tile's way.
 #include "qdot.cuh"
 #include "row_types.cuh"
 #include "select.cuh"
@@ -28,7 +29,7 @@ constexpr int kLpThreads = 256, kLpEpt = 16, kLpTile = kLpThreads * kLpEpt;
 constexpr int kLpMaxN = 32, kLpMaxSeg = 32;
 constexpr int kLpMaxRows = 4096;                    // rows of one launch (more rows: more launches)
 constexpr int kLpCtas = 8 * 152;
-constexpr int kLpKeep = 256;                        // the buffer is cut back beyond this many
+constexpr int kLpKeep = 128;                        // the buffer is cut back beyond this many
 constexpr int kLpCap = kLpKeep + 64 * kLpMaxN;      // and never holds more than this
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -222,11 +223,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
             }
         }
         float tm = v[0];
-        bool nan = false;
 #pragma unroll
-        for (int i = 0; i < kLpEpt; ++i) {
-            tm = fmaxf(tm, v[i]);
-            nan |= v[i] != v[i];
+        for (int i = 1; i < kLpEpt; ++i) tm = max_nan(tm, v[i]);
+        const bool nan = tm != tm;
+        if (nan) {  // the row's sums are NaN; its top values still come from the numbers
+            tm = __int_as_float(0xff800000);
+#pragma unroll
+            for (int i = 0; i < kLpEpt; ++i) tm = fmaxf(tm, v[i]);
+            S = U = __int_as_float(0x7fffffff);
         }
         if (tm > m) {
             if (S > 0.f) {
@@ -236,7 +240,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
             }
             m = tm;
         }
-        if (nan) S = U = __int_as_float(0x7fffffff);
         if (m > __int_as_float(0xff800000)) {
 #pragma unroll
             for (int i = 0; i < kLpEpt; ++i) {
@@ -245,17 +248,45 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
                 U = fmaf(fmaxf(d, -1e4f), e, U);  // -inf contributes 0
             }
         }
-        if (a.n > 0) {
-            const uint32_t th = (uint32_t)(sh.thr >> 32);
-            if (cta_sync_or(nan || order_key(tm) >= th)) {
-                unsigned long long key[kLpEpt];
+        if (a.n == 0) continue;
+        auto key_at = [&](int i) {
+            const int idx = t0 + ((i / EV) * kLpThreads + tid) * EV + i % EV;
+            return idx >= lo && idx < hi ? lp_key(v[i], idx) : 0ull;
+        };
+        bool robust = t0 <= lo;  // the first tile
+        if (!robust) {
+            const unsigned long long thr = sh.thr;
+            const int before = sh.count;
+            const bool pass = nan || order_key(tm) >= (uint32_t)(thr >> 32);
+            // a vote on both sides of the insertions: nobody inserts before everybody has read the count
+            if (!cta_sync_or(pass)) continue;
+            if (pass) {
 #pragma unroll
                 for (int i = 0; i < kLpEpt; ++i) {
-                    const int idx = t0 + ((i / EV) * kLpThreads + tid) * EV + i % EV;
-                    key[i] = idx >= lo && idx < hi ? lp_key(v[i], idx) : 0ull;
+                    const unsigned long long k = key_at(i);
+                    if (k > thr) {
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < kLpCap) sh.cand[at] = k;
+                    }
                 }
-                lp_insert(sh, key, a.n);
             }
+            cta_sync();
+            const int cnt = sh.count;
+            if (cnt <= kLpKeep) continue;
+            robust = cnt > kLpCap;
+            cta_sync();
+            if (robust) {  // take the tile's insertions back
+                if (tid == 0) sh.count = before;
+                cta_sync();
+            } else {
+                lp_sort(sh, cnt, a.n, true);
+            }
+        }
+        if (robust) {
+            unsigned long long key[kLpEpt];
+#pragma unroll
+            for (int i = 0; i < kLpEpt; ++i) key[i] = key_at(i);
+            lp_insert(sh, key, a.n);
         }
     }
     // the CTA's triple

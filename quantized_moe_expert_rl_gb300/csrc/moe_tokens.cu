@@ -3,16 +3,22 @@
 //   logits = W_r xn (+ bias),  ids = top-K, weights = softmax over the selection,
 //   y[t] (+)= sum_k weights[t][k] * down_k(silu(gate_k xn_t) * (up_k xn_t))
 //
-// One cooperative CTA per SM: 16 computing warps and one warp that issues the weight copies.
-//   R  every CTA takes up to four router rows (a quarter row per warp, f32 dots with every
-//      token), and a share of the split of x into bf16 parts;  grid barrier
+// One cooperative CTA per SM: 16 computing warps, three finishing warps and one that issues the weight
+// copies.
+//   R  every CTA takes up to four router rows (f32 dots with every token, each warp a sixteenth
+//      of the columns), and a share of the split of x into bf16 parts;  grid barrier
 //   S  every CTA selects for itself (one warp per token, the same code on the same logits): the
 //      list of distinct experts, each with its tokens as a bit mask, and from it the whole
 //      schedule of weight copies.  CTA 0 writes ids, weights, slots, misses and the flag
-//   G  the (expert, 16 hidden rows) tiles of gate and up, in equal runs over the CTAs -> h
-//      grid barrier (the copies of D's weights are already under way)
-//   D  CTA b: output rows 16 b .. 16 b + 15 of every expert's down matrix; the partial outputs stay
-//      in shared memory, so the sum over k in selection order needs no further exchange.
+//   G  gate and up: tiles of (expert, 16 hidden rows) -> h;  grid barrier
+//   D  down: tiles of (expert, 16 to 256 output rows) -> o of every (expert, token) pair;  grid
+//      barrier (the copies of D's first weights are under way before the one in front of it)
+//   C  y = sum over k in selection order.
+// G and D run the same code on rounds of 16 units, one per computing warp: 16 weight rows x 256
+// values (one block of every row).  A round's block sums go through one of four buffers to a finishing
+// warp, which adds them and applies SwiGLU (G) or stores them (D), so that no computing warp waits
+// for another.  Every CTA takes a run of consecutive tiles of equal weight, where a tile weighs one
+// per two tokens of its expert; an expert's activations then stay in registers over its tiles.
 //
 // The matrix arithmetic.  A weight is d * (codebook value) * (sign): the codebook value is an
 // 8-bit integer, exact in bf16, so a group's 8 values are one 16-byte table entry whose signs are
@@ -30,11 +36,16 @@ using namespace rl;
 
 namespace {
 
-constexpr int kMtWarps = 16, kMtThreads = kMtWarps * 32 + 32;
+constexpr int kMtWarps = 16, kMtFin = 3;            // computing and finishing warps
+constexpr int kMtWork = (kMtWarps + kMtFin) * 32;   // threads that meet at the grid barriers
+constexpr int kMtThreads = kMtWork + 32;            // and the copying warp
+constexpr int kMtRed = 4;                           // buffers between computing and finishing warps
 constexpr int kMtMaxT = 32;
 constexpr int kMtStage = 16896;    // one round of weights: 16 units of 16 rows x 256 values
 constexpr int kMtMaxStages = 8;
+constexpr int kMtMinStages = 4;    // the selection's keys (2 KB per token) share the ring's memory
 constexpr int kMtHdr = 256;        // workspace: barrier counter, test knobs (64..71), RMS scales (128..255)
+static_assert(kMtMinStages * kMtStage >= kMtMaxT * 2048, "the keys must fit the ring");
 
 struct MtArgs {
     const float *x, *W, *bias;
@@ -49,40 +60,37 @@ struct MtArgs {
     unsigned long long *ctr;
     float *rs, *raw;       // [32] RMS scales, [T][E] router dots
     uint16_t *xs, *hs;     // [T][3][H], [T K][3][I] bf16 parts
+    float *o;              // [T K][H] expert outputs
     float eps;
     int layer, T, H, E, K, I, accumulate, stages;
 };
 
-struct MtLayout {
-    uint32_t o_red, o_list, o_mask, o_slot, o_id, o_w, o_pair, o_ptok, o_sel, o_part, o_ring, total;
-    __host__ __device__ MtLayout(int T, int K, int I, int stages) {
-        const uint32_t P = T * K;
-        o_red = 512 + kTabBytes;                       // [2][16 warps][2 tokens][16 rows] f32
-        o_list = o_red + 2 * kMtWarps * 32 * 4;        // [512] (expert, first pair, token mask, -)
-        o_mask = o_list + 512 * 16;                    // [512] u32
-        o_slot = o_mask + 512 * 4;                     // [512] u64
-        o_id = o_slot + 512 * 8;                       // [P] i32
-        o_w = o_id + 512 * 4;                          // [P] f32
-        o_pair = o_w + 512 * 4;                        // [P] u16 pair index of (t, k)
-        o_ptok = o_pair + 512 * 2;                     // [P] u8 token of a pair
-        o_sel = o_ptok + 512;                          // [16 warps] selection scratch
-        o_part = o_sel + kMtWarps * 448;               // [P][units per expert][16] f32
-        o_ring = (uint32_t)align_up(o_part + P * (I > 256 ? I / 256 : 1) * 64, 128);
-        total = o_ring + stages * kMtStage;
-    }
-};
+// shared memory: the header (barriers, scalars), the codebook table, then
+constexpr int kMtRedB = kMtRed * kMtWarps * 32 * 4;  // [kMtRed][16 units][2 tokens][16 rows] f32
+constexpr int kMtORed = 512 + kTabBytes;
+constexpr int kMtOList = kMtORed + kMtRedB;          // [512] (expert, first pair, token mask, weight before it)
+constexpr int kMtOMask = kMtOList + 512 * 16;        // [512] u32 token masks by expert
+constexpr int kMtOSlot = kMtOMask + 512 * 4;         // [512] u64 slots by expert
+constexpr int kMtOId = kMtOSlot + 512 * 8;           // [512] i32 selected ids
+constexpr int kMtOW = kMtOId + 512 * 4;              // [512] f32 selected logits, then weights
+constexpr int kMtOPair = kMtOW + 512 * 4;            // [512] u16 pair number of (t, k)
+constexpr int kMtOTok = kMtOPair + 512 * 2;          // [512] u8 token of a pair
+constexpr int kMtOSel = kMtOTok + 512;               // [16 warps][448] selection scratch
+constexpr int kMtORing = (kMtOSel + kMtWarps * 448 + 127) / 128 * 128;
 
+static_assert(kMtWork == 608, "the barriers below count 608 threads");
+// all warps but the copying one
 __device__ __forceinline__ void workers_sync() {
-    asm volatile("bar.sync 1, 512;" ::: "memory");
+    asm volatile("bar.sync 1, 608;" ::: "memory");
     __syncwarp();
 }
-// the same with a vote: true in every computing warp when any of them brought `pred`
+// the same with a vote: true everywhere when any thread brought `pred`
 __device__ __forceinline__ bool workers_sync_or(bool pred) {
     uint32_t any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 512, p;\n\t"
+        "bar.red.or.pred q, 1, 608, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
         : "r"(pred ? 1u : 0u)
@@ -91,10 +99,10 @@ __device__ __forceinline__ bool workers_sync_or(bool pred) {
     return any != 0u;
 }
 
-// The computing warps of all CTAs meet (see grid_sync in stack_kernel.cuh; the copying warp does not
+// The working warps of all CTAs meet (see grid_sync in stack_kernel.cuh; the copying warp does not
 // take part).
-__device__ __forceinline__ bool workers_grid_sync(unsigned long long *ctr, unsigned long long &target, int *ok_s,
-                                                  int32_t *ctrl, uint32_t cap) {
+__device__ __noinline__ bool workers_grid_sync(unsigned long long *ctr, unsigned long long &target, int *ok_s,
+                                               int32_t *ctrl, uint32_t cap) {
     workers_sync();
     if (threadIdx.x == 0) {
         unsigned long long old;
@@ -112,6 +120,23 @@ __device__ __forceinline__ bool workers_grid_sync(unsigned long long *ctr, unsig
     }
     workers_sync();
     return *ok_s != 0;
+}
+
+// Bounded wait of a whole warp for phase `parity` of an mbarrier, given up once *stop is set.
+__device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, const volatile int *stop) {
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < kSpinCap; ++i) {
+            if (mbar_try_wait(bar, parity)) {
+                ok = 1;
+                break;
+            }
+            if (*stop) break;
+        }
+    }
+    __syncwarp();  // rejoin the warp (see cta_sync)
+    return __shfl_sync(kFull, ok, 0) != 0;
 }
 
 // v = p[0] + p[1] + p[2] exactly, each a bf16 value (truncated, so nothing overflows)
@@ -132,84 +157,229 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// the 8 signed codebook values of the group bytes gs (index | sign mask << 8) as bf16 pairs
-__device__ __forceinline__ uint4 signed_group(uint32_t gs, const uint4 *tabc) {
-    uint4 q = tabc[(gs & 0xffu) * kTabCopies];
-    const uint32_t s = gs >> 8;
+// flip the signs of a table entry's 8 values by the 8-bit mask s (see group_fma2)
+__device__ __forceinline__ void flip_signs(uint4 &q, uint32_t s) {
     q.x ^= (s * 0x40008000u) & 0x80008000u;
     q.y ^= (s * 0x10002000u) & 0x80008000u;
     q.z ^= (s * 0x04000800u) & 0x80008000u;
     q.w ^= (s * 0x01000200u) & 0x80008000u;
-    return q;
+}
+__device__ __forceinline__ uint32_t lds_half(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
+
+// Groups of a unit and lanes.  Lane 4 g + t multiplies rows g and g + 8; in step j = 0..7 the four
+// lanes of a quad take four groups of 8 values, in any order that the activations share.
+//   WIDE: a lane reads its group bytes as aligned words (two groups each) 4 m + t, m = 0..3.  A block is
+//   66 bytes, so blocks at an odd multiple of 66 bytes start their groups on a word, (2 w, 2 w + 1) in word
+//   w; at an even multiple word w holds (2 w - 1, 2 w), the half before group 0 being the scale d, and
+//   group 31 takes its place.  Needs all rows of a unit at the same parity: two blocks or more per row.
+//   Else: 16-bit reads of group 4 j + t.
+template <bool WIDE>
+__device__ __forceinline__ int lane_group(int j, int t, bool even) {
+    if (!WIDE) return 4 * j + t;
+    const int g = 8 * (j >> 1) + 2 * t + (j & 1) - (even ? 1 : 0);
+    return g < 0 ? 31 : g;
 }
 
-// One unit: 16 rows x 32 STEPS values against two tokens.  p0, p1: this lane's first group bytes of
-// rows g and g + 8 (lane = 4 g + t, group 4 j + t in step j); b: its B fragments.  Returns, in lanes
-// t = 0, 1, token t's sums for rows g (v0) and g + 8 (v1), without the block scale.
-template <int STEPS>
-__device__ __forceinline__ void unit_dot(const uint8_t *p0, const uint8_t *p1, const uint4 (&b)[8], const uint4 *tabc,
-                                         float &v0, float &v1) {
+// One unit against two tokens: d * sums of rows g (v0) and g + 8 (v1) for token t in lanes t = 0, 1.
+// p0, p1: the block's first byte in this lane's two rows (plus, for half blocks, 16 groups in `go`).
+template <bool WIDE>
+__device__ __forceinline__ void unit_dot(const uint8_t *p0, const uint8_t *p1, int go, int steps, bool even,
+                                         const uint4 (&b)[8], const uint4 *tabc, float &v0, float &v1) {
+    const int t = threadIdx.x & 3;
     float c[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+    if (WIDE) {
+        const uint8_t *w0 = p0 + (even ? 0 : 2) + 4 * t, *w1 = p1 + (even ? 0 : 2) + 4 * t;
+        uint32_t w[4], v[4];
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-        const uint4 q = signed_group(*reinterpret_cast<const uint16_t *>(p0 + 8 * j), tabc);
-        const uint4 r = signed_group(*reinterpret_cast<const uint16_t *>(p1 + 8 * j), tabc);
-        mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
-        mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
+        for (int m = 0; m < 4; ++m) {
+            w[m] = *reinterpret_cast<const uint32_t *>(w0 + 16 * m);
+            v[m] = *reinterpret_cast<const uint32_t *>(w1 + 16 * m);
+        }
+        if (even && t == 0) {
+            w[0] = (w[0] & 0xffff0000u) | lds_half(p0 + 64);
+            v[0] = (v[0] & 0xffff0000u) | lds_half(p1 + 64);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t gw = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+            const uint32_t gv = (j & 1) ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu;
+            uint4 q = tabc[(gw & 0xffu) * kTabCopies], r = tabc[(gv & 0xffu) * kTabCopies];
+            flip_signs(q, gw >> 8);
+            flip_signs(r, gv >> 8);
+            mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
+            mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= steps) break;
+            const uint32_t gw = lds_half(p0 + go + 2 + 8 * j + 2 * t), gv = lds_half(p1 + go + 2 + 8 * j + 2 * t);
+            uint4 q = tabc[(gw & 0xffu) * kTabCopies], r = tabc[(gv & 0xffu) * kTabCopies];
+            flip_signs(q, gw >> 8);
+            flip_signs(r, gv >> 8);
+            mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
+            mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
+        }
     }
     // columns 0, 1: token 0 leading and middle parts; 2, 3: token 1; 4: token 0 last part; 5: token 1
-    const int src = (threadIdx.x & 28) | 2, t = threadIdx.x & 3;
+    const int src = (threadIdx.x & 28) | 2;
     const float c0 = c[0] + e[0], c1 = c[1] + e[1], c2 = c[2] + e[2], c3 = c[3] + e[3];
     const float l0 = __shfl_sync(kFull, c0, src), l1 = __shfl_sync(kFull, c1, src);
     const float l2 = __shfl_sync(kFull, c2, src), l3 = __shfl_sync(kFull, c3, src);
-    v0 = (c0 + c1) + (t == 0 ? l0 : l1);
-    v1 = (c2 + c3) + (t == 0 ? l2 : l3);
+    v0 = fp16_bits_to_float(lds_half(p0)) * ((c0 + c1) + (t == 0 ? l0 : l1));
+    v1 = fp16_bits_to_float(lds_half(p1)) * ((c2 + c3) + (t == 0 ? l2 : l3));
 }
 
 // B fragments of two rows of bf16 parts (rowA, rowB: [3][width], rowB may be NULL), values from
-// `at` on: lane (n, t) holds column n's groups 4 j + t.
-template <int STEPS>
-__device__ __forceinline__ void load_b(uint4 (&b)[8], const uint16_t *rowA, const uint16_t *rowB, int width, int at) {
+// `at` on: lane (n, t) holds its groups of column n.
+template <bool WIDE>
+__device__ __forceinline__ void load_b(uint4 (&b)[8], const uint16_t *rowA, const uint16_t *rowB, int width, int at,
+                                       int steps, bool even) {
     const int n = (threadIdx.x >> 2) & 7, t = threadIdx.x & 3;
     const uint16_t *row = (n == 2 || n == 3 || n == 5) ? rowB : rowA;
     const int part = n >= 4 ? 2 : n & 1;
     const bool in = n < 6 && row != nullptr;
-    const uint4 *p = reinterpret_cast<const uint4 *>(row + part * width + at) + t;
+    const uint4 *p = reinterpret_cast<const uint4 *>(row + part * width + at);
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) b[j] = in ? __ldcg(p + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < 8; ++j)
+        b[j] = in && (WIDE || j < steps) ? __ldcg(p + lane_group<WIDE>(j, t, even)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The K best of the E keys in shared memory (key, then lower index; E <= 512, key[e] = 0 from E on) by
+// one warp: lane r < K gets the r-th.  The threshold is the K-th largest of the 32 lane maxima (so at
+// least K keys reach it); the few keys at or above it are ranked exactly, and with more than 32 of
+// them (heavy ties) K rounds of arg-max take over.  As warp_topk_thr, in rolled loops over
+// shared memory: this code runs once per launch, and fetching it costs more than executing it.
+__device__ __noinline__ void warp_topk_smem(const uint32_t *key, int E, int K, uint8_t *scratch, int &my_id,
+                                            float &my_val) {
+    const int lane = threadIdx.x & 31;
+    uint32_t *wm = reinterpret_cast<uint32_t *>(scratch);
+    uint2 *cand = reinterpret_cast<uint2 *>(scratch + 128);
+    int *sel = reinterpret_cast<int *>(scratch + 384);
+    const uint4 *k4 = reinterpret_cast<const uint4 *>(key) + lane;  // keys 128 j + 4 lane + c
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v = k4[32 * j];
+        m = max(max(m, max(v.x, v.y)), max(v.z, v.w));
+    }
+    wm[lane] = m;
+    __syncwarp();
+    int rank = 0;
+#pragma unroll 4
+    for (int q = 0; q < 32; ++q) rank += wm[q] > m || (wm[q] == m && q < lane) ? 1 : 0;
+    const uint32_t thr = __shfl_sync(kFull, m, __ffs(__ballot_sync(kFull, rank == K - 1)) - 1);
+    int n = 0;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v = k4[32 * j];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t k = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+            const int e = 128 * j + 4 * lane + c;
+            const bool in = e < E && k >= thr;
+            const unsigned bal = __ballot_sync(kFull, in);
+            const int at = n + __popc(bal & ((1u << lane) - 1u));
+            if (in && at < 32) cand[at] = make_uint2(k, (uint32_t)e);
+            n += __popc(bal);
+        }
+    }
+    __syncwarp();
+    my_id = 0;
+    my_val = 0.f;
+    if (n <= 32) {
+        const uint2 me = lane < n ? cand[lane] : make_uint2(0u, 0x7fffffffu);
+        int r = 0;
+#pragma unroll 4
+        for (int d = 0; d < n; ++d) {
+            const uint2 o = cand[d];
+            r += precedes(o.x, (int)o.y, me.x, (int)me.y) ? 1 : 0;
+        }
+        if (lane < n && r < K) sel[r] = lane;
+        __syncwarp();
+        if (lane < K) {
+            const uint2 c = cand[sel[lane]];
+            my_id = (int)c.y;
+            my_val = key_value(c.x);
+        }
+    } else {
+        unsigned taken = 0u;  // bit i: this lane's expert lane + 32 i
+#pragma unroll 1
+        for (int r = 0; r < K; ++r) {
+            uint32_t bk = 0u;
+            int bi = 0x7fffffff;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const int e = lane + 32 * i;
+                if (e < E && !((taken >> i) & 1u) && precedes(key[e], e, bk, bi)) bk = key[e], bi = e;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint32_t ok = __shfl_xor_sync(kFull, bk, o);
+                const int oi = __shfl_xor_sync(kFull, bi, o);
+                if (precedes(ok, oi, bk, bi)) bk = ok, bi = oi;
+            }
+            if (lane == r) my_id = bi, my_val = key_value(bk);
+            if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
+        }
+    }
+    __syncwarp();
+}
+
+// First tile of CTA b's run: tiles are numbered expert by expert, 2^lg each; expert i's tiles weigh
+// (tokens + 1) / 2 each and list[i].w is the weight of the experts before it, per tile.
+__device__ __forceinline__ int run_start(const int4 *list, int n, int total, int lg, int b, int G) {
+    const long long pos = (((long long)total << lg) * b) / G;
+    int at = 0, left = n;
+    while (left > 1) {
+        const int h = left >> 1;
+        if (((long long)list[at + h].w << lg) <= pos) at += h, left -= h;
+        else left = h;
+    }
+    const int c = (__popc((uint32_t)list[at].z) + 1) >> 1, in = (int)(pos - ((long long)list[at].w << lg));
+    return (at << lg) + (in + c - 1) / c;
+}
+
+template <bool WIDE>
 __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_constant__ MtArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const MtLayout lay(a.T, a.K, a.I, a.stages);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + kMtMaxStages;
-    int *ok_s = reinterpret_cast<int *>(smem + 128);
-    volatile int *stop_s = reinterpret_cast<volatile int *>(smem + 132);
-    int *bad_s = reinterpret_cast<int *>(smem + 136);    // bit 0: a slot is absent, bit 1: misaligned, bit 2: bad id
-    int *scan_s = reinterpret_cast<int *>(smem + 160);   // [16][2] warp totals of the list
-    uint32_t *cap_s = reinterpret_cast<uint32_t *>(smem + 140);
-    int *skip_s = reinterpret_cast<int *>(smem + 144);
-    int *nd_s = reinterpret_cast<int *>(smem + 148);
-    int *hold_s = reinterpret_cast<int *>(smem + 152);
+    uint64_t *redfull = empty + kMtMaxStages, *redempty = redfull + kMtRed;
+    int *ok_s = reinterpret_cast<int *>(smem + 192);
+    volatile int *stop_s = reinterpret_cast<volatile int *>(smem + 196);
+    int *bad_s = reinterpret_cast<int *>(smem + 200);    // bit 0: a slot is absent, 1: misaligned, 2: bad id, 3: NaN
+    uint32_t *cap_s = reinterpret_cast<uint32_t *>(smem + 204);
+    int *skip_s = reinterpret_cast<int *>(smem + 208);
+    int *nd_s = reinterpret_cast<int *>(smem + 212);
+    int *hold_s = reinterpret_cast<int *>(smem + 216);
+    int *run_s = reinterpret_cast<int *>(smem + 224);      // [4] this CTA's runs: G first, last + 1, D first, last + 1
+    float *rs_s = reinterpret_cast<float *>(smem + 240);   // [32] RMS scales (to 368)
+    int *scan_s = reinterpret_cast<int *>(smem + 368);     // [8]; the rest of the scan shares the reduction buffer
     uint4 *tab = reinterpret_cast<uint4 *>(smem + 512);
-    float *red = reinterpret_cast<float *>(smem + lay.o_red);
-    int4 *list = reinterpret_cast<int4 *>(smem + lay.o_list);
-    uint32_t *mask_s = reinterpret_cast<uint32_t *>(smem + lay.o_mask);
-    uint64_t *slot_s = reinterpret_cast<uint64_t *>(smem + lay.o_slot);
-    int *id_s = reinterpret_cast<int *>(smem + lay.o_id);
-    float *w_s = reinterpret_cast<float *>(smem + lay.o_w);
-    uint16_t *pair_s = reinterpret_cast<uint16_t *>(smem + lay.o_pair);
-    uint8_t *ptok_s = smem + lay.o_ptok;
-    float *part = reinterpret_cast<float *>(smem + lay.o_part);
-    uint8_t *ring = smem + lay.o_ring;
+    float *red = reinterpret_cast<float *>(smem + kMtORed);
+    int4 *list = reinterpret_cast<int4 *>(smem + kMtOList);
+    uint32_t *mask_s = reinterpret_cast<uint32_t *>(smem + kMtOMask);
+    uint64_t *slot_s = reinterpret_cast<uint64_t *>(smem + kMtOSlot);
+    int *id_s = reinterpret_cast<int *>(smem + kMtOId);
+    float *w_s = reinterpret_cast<float *>(smem + kMtOW);
+    uint16_t *pair_s = reinterpret_cast<uint16_t *>(smem + kMtOPair);
+    uint8_t *ptok_s = smem + kMtOTok;
+    uint8_t *ring = smem + kMtORing;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = gridDim.x, cta = blockIdx.x;
-    const int T = a.T, H = a.H, E = a.E, K = a.K, I = a.I;
+    const int T = a.T, H = a.H, E = a.E, K = a.K, I = a.I, lgH = 31 - __clz(H);
     const bool routed = a.W != nullptr;  // else ids, weights and slots are given
 
     if (tid == 0) {
+#pragma unroll 1
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, kMtWarps);
+        }
+#pragma unroll 1
+        for (int s = 0; s < kMtRed; ++s) {
+            mbar_init(redfull + s, kMtWarps);
+            mbar_init(redempty + s, 1);
         }
         fence_mbar_init();
         *stop_s = 0;
@@ -220,44 +390,61 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         const int flag = ld_ctrl(a.ctrl);
         *skip_s = routed ? flag < a.layer : flag <= a.layer;
     }
-    // R: the router rows of this CTA (row r -> expert cta + r G), a quarter of a row per warp
-    const int q4 = H / 4, wrow = warp >> 2, wexp = cta + wrow * G, wcol = (warp & 3) * q4 + 4 * lane;
-    const bool wmine = routed && warp < kMtWarps && wexp < E;
+    // R: the router rows of this CTA (row r: expert cta + r G); warp w holds columns [w H/16, (w + 1) H/16)
+    const int rcol = warp * (H >> 4) + 4 * lane;
+    const bool rmine = routed && warp < kMtWarps && 4 * lane < (H >> 4);
     float4 wv[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        wv[j] = wmine && 128 * j + 4 * lane < q4
-                    ? __ldg(reinterpret_cast<const float4 *>(a.W + (size_t)wexp * H + wcol + 128 * j))
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int e = tid; e < 512; e += kMtThreads) mask_s[e] = 0u;
+    for (int r = 0; r < 4; ++r)
+        wv[r] = rmine && cta + r * G < E ? __ldg(reinterpret_cast<const float4 *>(a.W + (size_t)(cta + r * G) * H + rcol))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < 512) {
+        mask_s[tid] = 0u;
+        if (routed && tid < E) slot_s[tid] = a.table[tid];
+    }
     build_pair_table(tab, a.codebook, nullptr);  // ends with a CTA barrier
     if (*skip_s) return;
     unsigned long long target = 0ull;
-    if (warp < kMtWarps) {
-        if (wmine)
+    bool ok = true;
+    if (tid < kMtWork) {
+        if (routed && warp < kMtWarps) {
+            float4 xv[4];
+            auto load_x = [&](int t0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    xv[u] = rmine && t0 + u < T ? *reinterpret_cast<const float4 *>(a.x + (size_t)(t0 + u) * H + rcol)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            load_x(0);
+#pragma unroll 1
             for (int t0 = 0; t0 < T; t0 += 4) {
-                float s[4];
+                float s[16];  // [token][row]
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    s[u] = 0.f;
-                    const int t = t0 + u < T ? t0 + u : T - 1;
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (128 * j + 4 * lane < q4) {
-                            const float4 v = *reinterpret_cast<const float4 *>(a.x + (size_t)t * H + wcol + 128 * j);
-                            s[u] = fmaf(wv[j].x, v.x, fmaf(wv[j].y, v.y, fmaf(wv[j].z, v.z, fmaf(wv[j].w, v.w, s[u]))));
-                        }
+                    for (int r = 0; r < 4; ++r)
+                        s[4 * u + r] = fmaf(wv[r].x, xv[u].x, fmaf(wv[r].y, xv[u].y, fmaf(wv[r].z, xv[u].z, wv[r].w * xv[u].w)));
+                load_x(t0 + 4);
+                // transposing reduction: each step halves the values a lane holds; lane l ends with value l & 15
+#pragma unroll
+                for (int h = 8; h > 0; h >>= 1) {
+                    const bool up = (lane & h) != 0;
+#pragma unroll
+                    for (int i = 0; i < h; ++i) {
+                        const float give = up ? s[i] : s[i + h], keep = up ? s[i + h] : s[i];
+                        s[i] = keep + __shfl_xor_sync(kFull, give, h);
+                    }
                 }
+                s[0] += __shfl_xor_sync(kFull, s[0], 16);
+                // partial dots [16 warps][32 tokens][4 rows] in the (still unused) reduction buffers
+                if (lane < 16) red[(warp * 32 + t0) * 4 + lane] = s[0];
                 __syncwarp();
-#pragma unroll
-                for (int u = 0; u < 4; ++u) s[u] = warp_sum(s[u]);
-                // partial dots [4 rows][4 quarters][32 tokens] in the (still unused) reduction buffer
-                if (lane < 4 && t0 + lane < T)
-                    red[warp * 32 + t0 + lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
             }
+        }
         // x as bf16 parts, 8 values at a time over the whole grid
-        for (int i = cta * 512 + tid; i < T * H / 8; i += G * 512) {
-            const int t = i / (H / 8), h = (i - t * (H / 8)) * 8;
+#pragma unroll 1
+        for (int i = cta * kMtWork + tid; i < T * H / 8; i += G * kMtWork) {
+            const int t = i >> (lgH - 3), h = (i << 3) & (H - 1);
             const float4 v0 = *reinterpret_cast<const float4 *>(a.x + (size_t)t * H + h);
             const float4 v1 = *reinterpret_cast<const float4 *>(a.x + (size_t)t * H + h + 4);
             const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -271,7 +458,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                                   p[6][k] | p[7][k] << 16));
         }
         // RMS scale of token t by CTA G - 1 - t (the CTAs with the fewest router rows)
-        if (warp == kMtWarps - 1 && G - 1 - cta < T) {
+        if (warp == kMtWarps && G - 1 - cta < T) {
             const int t = G - 1 - cta;
             bool range = false;
             const float r = a.eps >= 0.f ? rms_scale_warp(a.x + (size_t)t * H, H, a.eps, &range) : 1.f;
@@ -283,147 +470,162 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         }
         workers_sync();
         if (routed && tid < 4 * T) {
-            const int r = tid / T, t = tid - r * T, e = cta + r * G;
-            if (e < E)
-                __stcg(a.raw + (size_t)t * E + e, (red[(4 * r) * 32 + t] + red[(4 * r + 1) * 32 + t]) +
-                                                      (red[(4 * r + 2) * 32 + t] + red[(4 * r + 3) * 32 + t]));
+            const int t = tid >> 2, r = tid & 3, e = cta + r * G;
+            if (e < E) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kMtWarps; ++w) v += red[(w * 32 + t) * 4 + r];
+                __stcg(a.raw + (size_t)t * E + e, v);
+            }
         }
-        bool ok = *hold_s - 1 != cta;  // test knob: this CTA leaves before its arrival
+        ok = *hold_s - 1 != cta;  // test knob: this CTA leaves before its arrival
         if (ok) ok = workers_grid_sync(a.ctr, target, ok_s, a.ctrl, *cap_s);
         if (!ok && tid == 0) *stop_s = 1;
-        // S: selection, one warp per token
-        if (ok)
+        // S: selection.  Keys of every (token, expert) into shared memory, then one warp per token.
+        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
+        if (ok) {
+            if (tid < T) rs_s[tid] = __ldcg(a.rs + tid);
+            if (routed) {
+#pragma unroll 2
+                for (int i = tid; i < 512 * T; i += kMtWork) {
+                    const int t = i >> 9, e = i & 511;
+                    uint32_t k = 0u;
+                    if (e < E) {
+                        const float v = __ldcg(a.rs + t) * __ldcg(a.raw + (size_t)t * E + e) + (a.bias ? a.bias[e] : 0.f);
+                        if (v != v) atomicOr(bad_s, 8);
+                        k = order_key(v);
+                        if (a.logits_out && cta == 0) a.logits_out[(size_t)t * E + e] = v;
+                    }
+                    keys[i] = k;
+                }
+            }
+        }
+        workers_sync();
+        if (ok && warp < kMtWarps) {
+#pragma unroll 1
             for (int t = warp; t < T; t += kMtWarps) {
                 int my_id = 0;
-                float my_val = 0.f, w = 0.f;
+                float my_val = 0.f;
                 uint64_t slot = 1;
                 if (routed) {
-                    const float rs = __ldcg(a.rs + t);
-                    uint32_t key[16];
-                    bool nan = false;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int e = sel_id(lane, j);
-                        float v = 0.f;
-                        key[j] = 0u;
-                        if (e < E) {
-                            v = rs * __ldcg(a.raw + (size_t)t * E + e) + (a.bias ? a.bias[e] : 0.f);
-                            nan |= v != v;
-                            key[j] = order_key(v);
-                            if (a.logits_out && cta == 0) a.logits_out[(size_t)t * E + e] = v;
-                        }
-                    }
-                    if (__any_sync(kFull, nan) && lane == 0 && cta == 0) dev_error(a.ctrl, RL_DEVERR_NAN);
-                    __syncwarp();
-                    uint8_t *sc = smem + lay.o_sel + warp * 448;
-                    warp_topk_thr(key, E, K, reinterpret_cast<uint32_t *>(sc), reinterpret_cast<uint2 *>(sc + 128),
-                                  reinterpret_cast<int *>(sc + 384), my_id, my_val);
-                    w = topk_weight(my_val, K);
-                    if (lane < K) slot = a.table[my_id];
+                    warp_topk_smem(keys + 512 * t, E, K, smem + kMtOSel + warp * 448, my_id, my_val);
+                    if (lane < K) slot = slot_s[my_id];
                 } else if (lane < K) {
                     my_id = a.ids[t * K + lane];
-                    w = a.weights[t * K + lane];
+                    my_val = a.weights[t * K + lane];
                     slot = a.slots[t * K + lane];
                     if (my_id < 0 || my_id >= E) {
                         atomicOr(bad_s, 4);
                         my_id = 0;
                     }
+                    slot_s[my_id] = slot;
                 }
                 __syncwarp();
                 if (lane < K) {
                     id_s[t * K + lane] = my_id;
-                    w_s[t * K + lane] = w;
-                    slot_s[my_id] = slot;
+                    w_s[t * K + lane] = my_val;
                     atomicOr(mask_s + my_id, 1u << t);
                     if (slot == 0) atomicOr(bad_s, 1);
                     if (slot & 15) atomicOr(bad_s, 2);
-                    if (routed && cta == 0) {
-                        a.ids[t * K + lane] = my_id;
-                        a.weights[t * K + lane] = w;
-                        a.slots[t * K + lane] = slot;
-                    }
-                }
-                const int nmiss = __popc(__ballot_sync(kFull, lane < K && slot == 0));
-                if (lane == 0 && nmiss > 0 && cta == 0 && routed) {
-                    atomicAdd(a.miss, (uint32_t)nmiss);
-                    atomicMin(a.ctrl, a.layer);
                 }
                 __syncwarp();
             }
+        }
+        fence_proxy_async_smem();  // the ring's copies come after the keys
     }
     cta_sync();
     if (*stop_s) return;
-    if (*bad_s) {
+    const int bad = *bad_s;
+    if (routed && cta == 0 && warp < kMtWarps) {  // the outputs of the selection
+#pragma unroll 1
+        for (int t = warp; t < T; t += kMtWarps) {
+            const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
+            uint64_t slot = 1;
+            if (lane < K) {
+                const int e = id_s[t * K + lane];
+                slot = slot_s[e];
+                a.ids[t * K + lane] = e;
+                a.weights[t * K + lane] = w;
+                a.slots[t * K + lane] = slot;
+            }
+            const int nmiss = __popc(__ballot_sync(kFull, lane < K && slot == 0));
+            if (lane == 0 && nmiss > 0) {
+                atomicAdd(a.miss, (uint32_t)nmiss);
+                atomicMin(a.ctrl, a.layer);
+            }
+            __syncwarp();
+        }
+    }
+    if (bad) {
         if (tid == 0 && cta == 0) {
-            const int b = *bad_s;
-            const int bits = ((b & 1) && !routed ? RL_DEVERR_MISSING : 0) | (b & 2 ? RL_DEVERR_SLOT_ALIGN : 0) |
-                             (b & 4 ? RL_DEVERR_BAD_ID : 0);
+            const int bits = ((bad & 1) && !routed ? RL_DEVERR_MISSING : 0) | (bad & 2 ? RL_DEVERR_SLOT_ALIGN : 0) |
+                             (bad & 4 ? RL_DEVERR_BAD_ID : 0) | (bad & 8 ? RL_DEVERR_NAN : 0);
             if (bits) dev_error(a.ctrl, bits);
         }
-        return;
+        if (bad & 7) return;
     }
     // The list of distinct experts in index order: thread e holds expert e; its pairs (expert, token)
-    // are numbered in token order from `off`.
-    uint32_t m = 0u;
-    int incl = 0;
-    if (warp < kMtWarps) {
-        m = tid < E ? mask_s[tid] : 0u;
-        incl = __popc(m);
+    // are numbered in token order from `off`, and `before` is the weight of the experts before it.
+    if (tid < kMtWork) {
+        int *scan = reinterpret_cast<int *>(red);  // [16 warps][4]
+        const uint32_t m = tid < 512 ? mask_s[tid] : 0u;
+        const int cnt = __popc(m);
+        uint32_t incl = (uint32_t)cnt | (uint32_t)((cnt + 1) >> 1) << 16;  // pairs | weight
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, incl, o);
+            const uint32_t v = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += v;
         }
         const unsigned has = __ballot_sync(kFull, m != 0u);
-        if (lane == 31) {
-            scan_s[2 * warp] = __popc(has);
-            scan_s[2 * warp + 1] = incl;
+        if (lane == 31 && warp < kMtWarps) {
+            scan[2 * warp] = __popc(has);
+            scan[2 * warp + 1] = (int)incl;
         }
         __syncwarp();
         workers_sync();
-        int at = __popc(has & ((1u << lane) - 1u)), off = incl - __popc(m);
-        for (int w = 0; w < warp; ++w) {
-            at += scan_s[2 * w];
-            off += scan_s[2 * w + 1];
+        int at = 0;
+        uint32_t base = 0u;
+#pragma unroll 4
+        for (int w = 0; w < kMtWarps; ++w) {
+            if (w < warp) {
+                at += scan[2 * w];
+                base += (uint32_t)scan[2 * w + 1];
+            }
+        }
+        if (tid == kMtWarps * 32 - 1) {  // the last expert's thread knows the totals
+            *nd_s = at + __popc(has);
+            scan_s[0] = (int)((base + incl) >> 16);
         }
         if (m) {
-            list[at] = make_int4(tid, off, (int)m, 0);
+            at += __popc(has & ((1u << lane) - 1u));
+            const uint32_t ex = base + incl - ((uint32_t)cnt | (uint32_t)((cnt + 1) >> 1) << 16);
+            list[at] = make_int4(tid, (int)(ex & 0xffffu), (int)m, (int)(ex >> 16));
             uint32_t left = m;
-            for (int i = 0; left; ++i, left &= left - 1u) ptok_s[off + i] = (uint8_t)(__ffs(left) - 1);
+#pragma unroll 1
+            for (int i = (int)(ex & 0xffffu); left; ++i, left &= left - 1u) ptok_s[i] = (uint8_t)(__ffs(left) - 1);
         }
         __syncwarp();
-        if (tid == 0) {
-            int n = 0;
-            for (int w = 0; w < kMtWarps; ++w) n += scan_s[2 * w];
-            *nd_s = n;
-        }
+        workers_sync();
+        const int lgG = 31 - __clz(I >> 4);                      // gate/up tiles of 16 rows per expert
+        const int lgD = 31 - __clz((H >> 4) * (I > 256 ? I >> 8 : 1) >> 4);  // down tiles of 16 units
+        if (tid < 4) run_s[tid] = run_start(list, *nd_s, scan_s[0], tid < 2 ? lgG : lgD, cta + (tid & 1), G);
     }
     cta_sync();
-    const int nD = *nd_s;
-    // schedule: gate/up tiles [g0, g1) of this CTA, then the down rows of every expert
-    const int RT = I / 16, nb = H / 256, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb;
-    const int tiles = nD * RT, g0 = (int)((long long)cta * tiles / G), g1 = (int)((long long)(cta + 1) * tiles / G);
-    const int gr = (g1 - g0 + tpr - 1) / tpr;
-    const int upe = I > 256 ? I / 256 : 1, epr = kMtWarps / upe, dnb = I * kBlockBytes / 16;
-    const int dr = cta < H / 16 ? (nD + epr - 1) / epr : 0;
+    // Tiles.  G: 16 rows of gate and up, 2 nb units; tpr of them per round.  D: 16 units, upe per row.
+    const int nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb, lgnb = 31 - __clz(nb);
+    const int lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, lgu = 31 - __clz(upe), lgD = 31 - __clz((H * upe) >> 8);
+    const int dbytes = I >= 256 ? kMtStage : kMtStage / 2;  // bytes of a down tile
+    const int g0 = run_s[0], g1 = run_s[1], d0 = run_s[2], d1 = run_s[3];
+    const int gr = (g1 - g0 + tpr - 1) / tpr, dr = d1 - d0;
 
-    if (warp == kMtWarps) {  // the copying warp
+    if (tid >= kMtWork) {  // the copying warp
         const size_t mat = (size_t)I * rowb;
-        int slot = 0, turn = 0;
-        bool ok = true;
-        int issued = 0;
-        for (int r = 0; r < gr + dr && ok; ++r) {
-            if (turn > 0) {
-                ok = false;
-                for (uint32_t i = 0; i < kSpinCap && !ok; ++i) {
-                    ok = mbar_try_wait(empty + slot, (turn - 1) & 1);
-                    if (*stop_s) break;
-                }
-                ok = __all_sync(kFull, ok) != 0;
-                if (!ok) {
-                    if (lane == 0) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
-                    break;
-                }
+        int slot = 0, turn = 0, issued = 0;
+#pragma unroll 1
+        for (int r = 0; r < gr + dr; ++r) {
+            if (turn > 0 && !wait_or_stop(empty + slot, (turn - 1) & 1, stop_s)) {
+                if (lane == 0) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
+                break;
             }
             uint8_t *dst = ring + slot * kMtStage;
             if (r < gr) {
@@ -431,171 +633,221 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 if (lane == 0) mbar_arrive_expect_tx(full + slot, n * tileb);
                 __syncwarp();
                 if (lane < 2 * n) {
-                    const int tile = g0 + r * tpr + (lane >> 1), ei = tile / RT, rt = tile - ei * RT;
-                    const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[ei].x]);
+                    const int tile = g0 + r * tpr + (lane >> 1);
+                    const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[tile >> lgG].x]);
                     bulk_g2s(dst + (lane >> 1) * tileb + (lane & 1) * 16 * rowb,
-                             rec + (lane & 1) * mat + (size_t)rt * 16 * rowb, 16 * rowb, full + slot);
+                             rec + (lane & 1) * mat + (size_t)(tile & ((1 << lgG) - 1)) * 16 * rowb, 16 * rowb, full + slot);
                 }
-            } else {
-                const int e0 = (r - gr) * epr, n = min(epr, nD - e0);
-                if (lane == 0) mbar_arrive_expect_tx(full + slot, n * dnb);
-                __syncwarp();
-                if (lane < n) {
-                    const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[e0 + lane].x]);
-                    bulk_g2s(dst + lane * dnb, rec + 2 * mat + (size_t)cta * dnb, dnb, full + slot);
-                }
+            } else if (lane == 0) {
+                const int tile = d0 + r - gr;
+                const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[tile >> lgD].x]);
+                mbar_arrive_expect_tx(full + slot, dbytes);
+                bulk_g2s(dst, rec + 2 * mat + (size_t)(tile & ((1 << lgD) - 1)) * dbytes, dbytes, full + slot);
             }
             __syncwarp();
             ++issued;
             if (++slot == a.stages) slot = 0, ++turn;
         }
         // every copy issued has landed before the CTA's shared memory goes away
+#pragma unroll 1
         for (int r = max(0, issued - a.stages); r < issued; ++r) mbar_wait_warp(full + r % a.stages, (r / a.stages) & 1);
         return;
     }
 
-    // pair numbers of (t, k)
-    for (int e = tid; e < nD; e += 512) mask_s[list[e].x] = (uint32_t)e;  // expert -> position in the list
-    workers_sync();
-    for (int i = tid; i < T * K; i += 512) {
-        const int4 l = list[mask_s[id_s[i]]];
-        pair_s[i] = (uint16_t)(l.y + __popc((uint32_t)l.z & ((1u << (i / K)) - 1u)));
-    }
     const int g = lane >> 2, t4 = lane & 3;
     const uint4 *tabc = tab + (lane & (kTabCopies - 1));
-    int slot = 0, turn = 0, buf = 0, haveA = -1, haveB = -1;
+    // D's units take every `stride`-th row of a tile, so that the rows of a unit lie 132 words apart and
+    // their lanes meet different banks
+    const int lgs = I >= 512 ? 11 - (31 - __clz(I)) : 0;
+    int slot = 0, turn = 0, s = 0;
     uint4 b[8];
-    bool ok = true;
-    // G: gate and up
-    for (int r = 0; r < gr && ok; ++r) {
-        const int ti = warp / (2 * nb), tile = g0 + r * tpr + ti, ei = tile / RT;
-        const bool mine = tile < g1;
-        const int4 l = mine ? list[ei] : make_int4(0, 0, 0, 0);
-        const int ntok = __popc((uint32_t)l.z);
-        int passes = 1;  // two tokens each; the same for every warp of the CTA
-        for (int i = 0; i < tpr; ++i)
-            if (g0 + r * tpr + i < g1) passes = max(passes, (__popc((uint32_t)list[(g0 + r * tpr + i) / RT].z) + 1) / 2);
-        const int blk = warp % nb;
-        const uint8_t *base = ring + slot * kMtStage + ti * tileb + ((warp / nb) & 1) * 16 * rowb + blk * kBlockBytes;
-        const uint8_t *p0 = base + g * rowb, *p1 = p0 + 8 * rowb;
-        for (int p = 0; p < passes; ++p) {
-            if (mine && 2 * p < ntok) {
-                const int tA = ptok_s[l.y + 2 * p], tB = 2 * p + 1 < ntok ? ptok_s[l.y + 2 * p + 1] : -1;
-                if (tA != haveA || tB != haveB) {
-                    load_b<8>(b, a.xs + (size_t)tA * 3 * H, tB < 0 ? nullptr : a.xs + (size_t)tB * 3 * H, H, blk * 256);
-                    haveA = tA;
-                    haveB = tB;
+#pragma unroll 1
+    for (int ph = 0; ph < 2; ++ph) {
+        const bool down = ph == 1;
+        const int r0 = down ? d0 : g0, r1 = down ? d1 : g1, per = down ? 1 : tpr, lgt = down ? lgD : lgG;
+        const int rounds = down ? dr : gr;
+        // a round's passes (two tokens each): as many as its most shared expert needs
+        auto passes_of = [&](int r) {
+            int n = 1;
+#pragma unroll 1
+            for (int i = 0; i < per; ++i) {
+                const int tile = r0 + r * per + i;
+                if (tile < r1) n = max(n, (__popc((uint32_t)list[tile >> lgt].z) + 1) >> 1);
+            }
+            return n;
+        };
+        if (warp >= kMtWarps) {
+            if (!down && routed) {  // renormalised weights, for the combine
+#pragma unroll 1
+                for (int t = warp - kMtWarps; t < T; t += kMtFin) {
+                    const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
+                    if (lane < K) w_s[t * K + lane] = w;
+                    __syncwarp();
                 }
             }
-            if (p == 0) ok = mbar_wait_warp(full + slot, turn & 1);
-            if (mine && 2 * p < ntok && ok) {
-                float v0, v1;
-                unit_dot<8>(p0 + 2 + 2 * t4, p1 + 2 + 2 * t4, b, tabc, v0, v1);
-                const float d0 = fp16_bits_to_float(*reinterpret_cast<const uint16_t *>(p0));
-                const float d1 = fp16_bits_to_float(*reinterpret_cast<const uint16_t *>(p1));
-                if (t4 < 2) {
-                    float *o = red + (buf * kMtWarps + warp) * 32 + t4 * 16;
-                    o[g] = d0 * v0;
-                    o[g + 8] = d1 * v1;
-                }
-            }
-            __syncwarp();
-            if (p == passes - 1 && lane == 0) mbar_arrive(empty + slot);
-            ok = !workers_sync_or(!ok);
-            if (!ok) break;
-            // h of tile i by one warp: lane = 16 token + row
-            for (int i = 0; i < tpr; ++i) {
-                const int tl = g0 + r * tpr + i;
-                if (tl >= g1 || ((r + p) * tpr + i) % kMtWarps != warp) continue;
-                const int4 q = list[tl / RT];
-                const int row = lane & 15, s = lane >> 4, tk = 2 * p + s;
-                if (tk < __popc((uint32_t)q.z)) {
-                    const float *o = red + (buf * kMtWarps + i * 2 * nb) * 32 + s * 16 + row;
-                    float gv = 0.f, uv = 0.f;
-                    for (int k = 0; k < nb; ++k) {
-                        gv += o[k * 32];
-                        uv += o[(nb + k) * 32];
+            if (!down) {  // pair numbers of (t, k)
+#pragma unroll 1
+                for (int i = tid - kMtWarps * 32; i < T * K; i += kMtFin * 32) {
+                    const int e = id_s[i];
+                    int at = 0, n = *nd_s;  // position of e in the list (sorted by expert)
+                    while (n > 1) {
+                        const int h = n >> 1;
+                        if (list[at + h].x <= e) at += h, n -= h;
+                        else n = h;
                     }
-                    const float rs = __ldcg(a.rs + ptok_s[q.y + tk]);
-                    uint32_t h3[3];
-                    split3(silu(rs * gv) * (rs * uv), h3);
-                    uint16_t *h = a.hs + (size_t)(q.y + tk) * 3 * I + (tl % RT) * 16 + row;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
+                    pair_s[i] = (uint16_t)(list[at].y + __popc((uint32_t)list[at].z & ((1u << (i / K)) - 1u)));
                 }
                 __syncwarp();
             }
-            buf ^= 1;
+#pragma unroll 1
+            for (int r = 0; r < rounds && ok; ++r) {
+                const int passes = passes_of(r);
+#pragma unroll 1
+                for (int p = 0; p < passes && ok; ++p, ++s) {
+                    if (s % kMtFin != warp - kMtWarps) continue;
+                    const int buf = s % kMtRed;
+                    ok = wait_or_stop(redfull + buf, (s / kMtRed) & 1, stop_s);
+                    if (!ok) break;
+                    const float *rb = red + buf * kMtWarps * 32;
+                    if (!down) {  // lane = 16 token + row
+                        const int row = lane & 15, tk = 2 * p + (lane >> 4);
+#pragma unroll 1
+                        for (int i = 0; i < per; ++i) {
+                            const int tl = g0 + r * per + i;
+                            if (tl >= g1) break;
+                            const int4 q = list[tl >> lgG];
+                            if (tk < __popc((uint32_t)q.z)) {
+                                const float *v = rb + i * 2 * nb * 32 + lane;
+                                float gv = 0.f, uv = 0.f;
+#pragma unroll 1
+                                for (int k = 0; k < nb; ++k) {
+                                    gv += v[k * 32];
+                                    uv += v[(nb + k) * 32];
+                                }
+                                const float rs = rs_s[ptok_s[q.y + tk]];
+                                uint32_t h3[3];
+                                split3(silu(rs * gv) * (rs * uv), h3);
+                                uint16_t *h = a.hs + (size_t)(q.y + tk) * 3 * I + ((tl & ((1 << lgG) - 1)) << 4) + row;
+#pragma unroll
+                                for (int k = 0; k < 3; ++k)
+                                    __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
+                            }
+                            __syncwarp();
+                        }
+                    } else {
+                        const int tl = d0 + r, rows = 256 >> lgu;
+                        const int4 q = list[tl >> lgD];
+                        const int left = __popc((uint32_t)q.z) - 2 * p;
+                        float *o = a.o + (size_t)(q.y + 2 * p) * H + (tl & ((1 << lgD) - 1)) * rows;
+#pragma unroll 1
+                        for (int i = lane; i < rows * (left > 1 ? 2 : 1); i += 32) {
+                            const int tk = i >= rows ? 1 : 0, row = i - tk * rows;
+                            // row = 16 stride (rg / stride) + stride i + rg % stride of row group rg
+                            const int rg = ((row >> (4 + lgs)) << lgs) + (row & ((1 << lgs) - 1)), ri = (row >> lgs) & 15;
+                            float v = 0.f;
+#pragma unroll 1
+                            for (int k = 0; k < upe; ++k) v += rb[((rg << lgu) + k) * 32 + tk * 16 + ri];
+                            __stcg(o + (size_t)tk * H + row, v);
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(redempty + buf);
+                    __syncwarp();
+                }
+            }
+        } else {
+            // this warp's unit: G (tile ti of the round, gate or up, block blk), D (row group, block)
+            const int ti = down ? 0 : warp >> (lgnb + 1), blk = down ? warp & (upe - 1) : warp & (nb - 1);
+            const int width = down ? I : H, steps = down && I < 256 ? 4 : 8, go = down && I < 256 ? 32 * (g & 1) : 0;
+            const bool even = (blk & 1) == 0;
+            int off, off8;  // bytes of rows g and g + 8 in the stage
+            if (!down) {
+                off = ti * tileb + (((warp >> lgnb) & 1) * 16 + g) * rowb + blk * kBlockBytes;
+                off8 = off + 8 * rowb;
+            } else {
+                const int rg = warp >> lgu, row = ((rg >> lgs) << (4 + lgs)) + (rg & ((1 << lgs) - 1));
+                // a row of 128 values is half a block: rows 2 i and 2 i + 1 share block i
+                off = I >= 256 ? ((row + (g << lgs)) << lgu) * kBlockBytes + blk * kBlockBytes
+                               : ((row + g) >> 1) * kBlockBytes;
+                off8 = off + (I >= 256 ? (8 << lgs) << lgu : 4) * kBlockBytes;
+            }
+            // The B fragments of the next pass are loaded as soon as the present ones have been
+            // used; they stay while the rows do.
+            int haveA = -1, haveB = -1;
+            auto fetch = [&](int r, int p) {
+                const int tile = r0 + r * per + ti;
+                if (r >= rounds || tile >= r1) return;
+                const int4 l = list[tile >> lgt];
+                const int ntok = __popc((uint32_t)l.z), at = l.y + 2 * p;
+                if (2 * p >= ntok) return;
+                const int rA = down ? at : ptok_s[at], rB = 2 * p + 1 < ntok ? (down ? at + 1 : ptok_s[at + 1]) : -1;
+                if (rA == haveA && rB == haveB) return;
+                const uint16_t *src = down ? a.hs : a.xs;
+                load_b<WIDE>(b, src + (size_t)rA * 3 * width, rB < 0 ? nullptr : src + (size_t)rB * 3 * width, width,
+                             blk * 256, steps, even);
+                haveA = rA;
+                haveB = rB;
+            };
+            fetch(0, 0);
+#pragma unroll 1
+            for (int r = 0; r < rounds && ok; ++r) {
+                const int tile = r0 + r * per + ti, passes = passes_of(r);
+                const int ntok = tile < r1 ? __popc((uint32_t)list[tile >> lgt].z) : 0;
+                const uint8_t *st = ring + slot * kMtStage;
+                ok = wait_or_stop(full + slot, turn & 1, stop_s);
+#pragma unroll 1
+                for (int p = 0; p < passes && ok; ++p, ++s) {
+                    const int buf = s % kMtRed;
+                    float v0 = 0.f, v1 = 0.f;
+                    if (2 * p < ntok) unit_dot<WIDE>(st + off, st + off8, go, steps, even, b, tabc, v0, v1);
+                    const bool last = p == passes - 1;
+                    if (last) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty + slot);
+                    }
+                    fetch(last ? r + 1 : r, last ? 0 : p + 1);
+                    if (s >= kMtRed) ok = wait_or_stop(redempty + buf, (s / kMtRed - 1) & 1, stop_s);
+                    if (t4 < 2 && 2 * p < ntok) {
+                        float *v = red + (buf * kMtWarps + warp) * 32 + t4 * 16;
+                        v[g] = v0;
+                        v[g + 8] = v1;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(redfull + buf);
+                }
+                if (++slot == a.stages) slot = 0, ++turn;
+            }
         }
-        if (++slot == a.stages) slot = 0, ++turn;
-    }
-    if (!ok) {
-        if (lane == 0) {
+        if (!ok && lane == 0) {
             dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
             *stop_s = 1;
         }
-        return;
-    }
-    if (!workers_grid_sync(a.ctr, target, ok_s, a.ctrl, *cap_s)) {
-        if (tid == 0) *stop_s = 1;
-        return;
-    }
-    if (dr == 0) return;
-    // D: this CTA's 16 output rows of every expert
-    const int ui = warp / upe, blk = warp % upe;
-    for (int r = 0; r < dr; ++r) {
-        const int ei = r * epr + ui;
-        const bool mine = ei < nD;
-        const int4 l = mine ? list[ei] : make_int4(0, 0, 0, 0);
-        const int ntok = __popc((uint32_t)l.z);
-        const uint8_t *base = ring + slot * kMtStage + ui * dnb;
-        // a row of 128 values is half a block: rows 2 i and 2 i + 1 share block i
-        const uint8_t *p0 = I >= 256 ? base + g * (I / 256 * kBlockBytes) + blk * kBlockBytes : base + (g >> 1) * kBlockBytes;
-        const uint8_t *p1 = p0 + (I >= 256 ? 8 * (I / 256) : 4) * kBlockBytes;
-        const int go = I >= 256 ? 0 : 32 * (g & 1);
-        for (int p = 0; 2 * p < ntok || p == 0; ++p) {
-            if (mine) {
-                const int pa = l.y + 2 * p;
-                const uint16_t *A = a.hs + (size_t)pa * 3 * I, *B = 2 * p + 1 < ntok ? A + 3 * I : nullptr;
-                if (I >= 256) load_b<8>(b, A, B, I, blk * 256);
-                else load_b<4>(b, A, B, I, 0);
-            }
-            if (p == 0) ok = mbar_wait_warp(full + slot, turn & 1);
-            if (mine && ok) {
-                float v0, v1;
-                if (I >= 256) unit_dot<8>(p0 + 2 + 2 * t4, p1 + 2 + 2 * t4, b, tabc, v0, v1);
-                else unit_dot<4>(p0 + go + 2 + 2 * t4, p1 + go + 2 + 2 * t4, b, tabc, v0, v1);
-                const float d0 = fp16_bits_to_float(*reinterpret_cast<const uint16_t *>(p0));
-                const float d1 = fp16_bits_to_float(*reinterpret_cast<const uint16_t *>(p1));
-                if (t4 < 2 && 2 * p + t4 < ntok) {
-                    float *o = part + ((size_t)(l.y + 2 * p + t4) * upe + blk) * 16;
-                    o[g] = d0 * v0;
-                    o[g + 8] = d1 * v1;
-                }
-            }
-        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty + slot);
-        if (!ok) break;
-        if (++slot == a.stages) slot = 0, ++turn;
-    }
-    if (!ok && lane == 0) {
-        dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
-        *stop_s = 1;
-    }
-    __syncwarp();
-    if (workers_sync_or(!ok)) return;
-    for (int i = tid; i < 16 * T; i += 512) {
-        const int t = i >> 4, row = i & 15;
-        float acc = 0.f;
-        for (int k = 0; k < K; ++k) {
-            const float *o = part + (size_t)pair_s[t * K + k] * upe * 16 + row;
-            float v = 0.f;
-            for (int j = 0; j < upe; ++j) v += o[j * 16];
-            acc = fmaf(w_s[t * K + k], v, acc);
+        if (workers_sync_or(!ok)) return;
+        if (!workers_grid_sync(a.ctr, target, ok_s, a.ctrl, *cap_s)) {
+            if (tid == 0) *stop_s = 1;
+            return;
         }
-        float *y = a.y + (size_t)t * H + cta * 16 + row;
-        *y = a.accumulate ? *y + acc : acc;
+    }
+    // C: four outputs per thread over the whole grid
+#pragma unroll 1
+    for (int i = cta * kMtWork + tid; i < T * H / 4; i += G * kMtWork) {
+        const int t = i >> (lgH - 2), h = (i << 2) & (H - 1);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < K; ++k) {
+            const float w = w_s[t * K + k];
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o + (size_t)pair_s[t * K + k] * H + h));
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        float *y = a.y + (size_t)t * H + h;
+        y[0] = a.accumulate ? y[0] + acc.x : acc.x;
+        y[1] = a.accumulate ? y[1] + acc.y : acc.y;
+        y[2] = a.accumulate ? y[2] + acc.z : acc.z;
+        y[3] = a.accumulate ? y[3] + acc.w : acc.w;
     }
 }
 
@@ -607,7 +859,7 @@ size_t mt_x_bytes(int T, int H) { return align_up((size_t)T * 3 * H * sizeof(uin
 extern "C" size_t moe_decode_tokens_workspace_bytes(const rl_moe_shape *shp, int32_t T) {
     if (check_shape(shp) != RL_OK || T <= 0 || T > kMtMaxT) return 0;
     return kMtHdr + mt_raw_bytes(T, shp->n_experts) + mt_x_bytes(T, shp->hidden) +
-           mt_x_bytes(T * shp->top_k, shp->inter);
+           mt_x_bytes(T * shp->top_k, shp->inter) + (size_t)T * shp->top_k * shp->hidden * sizeof(float);
 }
 
 extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, int32_t T, const float *x,
@@ -650,6 +902,7 @@ extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, i
     a.raw = reinterpret_cast<float *>(w8 + kMtHdr);
     a.xs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T, shp->n_experts));
     a.hs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T, shp->n_experts) + mt_x_bytes(T, shp->hidden));
+    a.o = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.hs) + mt_x_bytes(T * shp->top_k, shp->inter));
     a.eps = norm_eps;
     a.layer = layer;
     a.T = T;
@@ -658,17 +911,16 @@ extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, i
     a.K = shp->top_k;
     a.I = shp->inter;
     a.accumulate = accumulate != 0;
-    for (a.stages = kMtMaxStages; a.stages > 2; --a.stages)
-        if (MtLayout(T, a.K, a.I, a.stages).total <= 227 * 1024) break;
-    const size_t smem = MtLayout(T, a.K, a.I, a.stages).total;
+    a.stages = (227 * 1024 - kMtORing) / kMtStage < kMtMaxStages ? (227 * 1024 - kMtORing) / kMtStage : kMtMaxStages;
+    const size_t smem = kMtORing + (size_t)a.stages * kMtStage;
     const int G = sm_count();
-    if (G < 128 || smem > 227 * 1024)
-        return fail(RL_ERR_UNSUPPORTED, "moe_decode_tokens: needs 128 SMs and 227 KB of shared memory");
-    const rl_status sa = allow_smem((const void *)moe_tokens_kernel, smem);
+    if (G < 128) return fail(RL_ERR_UNSUPPORTED, "moe_decode_tokens: needs a GPU of 128 SMs or more");
+    // 32-bit reads of the group bytes need two blocks or more per matrix row
+    const void *kernel = a.H >= 512 && a.I >= 512 ? (const void *)moe_tokens_kernel<true> : (const void *)moe_tokens_kernel<false>;
+    const rl_status sa = allow_smem(kernel, smem);
     if (sa != RL_OK) return sa;
     void *args[] = {&a};
-    const cudaError_t e = cudaLaunchCooperativeKernel((const void *)moe_tokens_kernel, dim3(G), dim3(kMtThreads), args,
-                                                      smem, as_stream(stream));
+    const cudaError_t e = cudaLaunchCooperativeKernel(kernel, dim3(G), dim3(kMtThreads), args, smem, as_stream(stream));
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(RL_ERR_CUDA, "moe_decode_tokens: launch failed: %s", cudaGetErrorString(e));

@@ -34,6 +34,7 @@ constexpr int kQ4Threads = 512, kQ4Warps = kQ4Threads / 32;
 constexpr int kQ4Stage = 16 * 128 + 16 * 16;  // 16 rows x 256 nibbles, then 16 bytes of scales per row
 constexpr int kQ4MaxStages = 6;
 constexpr int kQ4MaxK = 8192;
+constexpr int kQ4Rounds = 1;
 
 struct Q4Args {
     const uint8_t *w;
@@ -173,32 +174,51 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Copy stage `st` of the 16 rows from row0 into a ring slot; rows and values outside read as zero.
-__device__ __forceinline__ void q4_issue(const Q4Args &a, uint8_t *slot, int row0, int st) {
+// The copies of one warp: 16 rows x 256 values per stage, every W-th stage of its tiles.
+struct Q4Feed {
+    const uint8_t *p;   // this lane's 16 bytes of rows (lane / 8) + 4 i, i = 0..3, at the present stage
+    const __half *q;    // lanes 0..15: the scales of row `lane` at the present stage
+    int tile, st;
+    bool full;          // all 16 rows are in the matrix
+};
+__device__ __forceinline__ void q4_seek(const Q4Args &a, Q4Feed &f, int tile, int st) {
     const int lane = threadIdx.x & 31;
-    const uint32_t base = smem_addr(slot);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 3) + 4 * i, j = lane & 7, k = (st * 8 + j) * 32;
-        const bool in = row0 + r < a.N && k < a.K;
-        const uint8_t *src = in ? a.w + (size_t)(row0 + r) * (a.K / 2) + k / 2 : a.w;
-        cp_async16(base + r * 128 + ((j ^ (r & 7)) << 4), src, in ? 16 : 0);
-    }
-    const int gs = 256 / a.group, G = a.K / a.group;  // groups per stage and per row
-    if (a.wide) {
+    f.tile = tile;
+    f.st = st;
+    f.full = tile * 16 + 16 <= a.N;
+    f.p = a.w + (size_t)(tile * 16 + (lane >> 3)) * (a.K >> 1) + st * 128 + (lane & 7) * 16;
+    f.q = a.ws + (size_t)(tile * 16 + (lane & 15)) * (a.K / a.group) + st * (256 / a.group);
+}
+// Copy the present stage into a ring slot (row r's piece j of 16 bytes at 128 r + 16 (j ^ (r & 7)), then 16
+// bytes of scales per row); rows and values outside read as zero.
+template <int GL>
+__device__ __forceinline__ void q4_issue(const Q4Args &a, const Q4Feed &f, uint8_t *slot) {
+    constexpr int gs = 8 / GL;  // groups per stage
+    const int lane = threadIdx.x & 31, r0 = lane >> 3, j = lane & 7;
+    const uint32_t base = smem_addr(slot), d0 = base + r0 * 128 + ((j ^ r0) << 4), d1 = (d0 ^ 64) + 512;
+    const size_t step = (size_t)a.K * 2;  // four rows
+    if (a.wide && f.full) {
+        cp_async16(d0, f.p, 16);
+        cp_async16(d1, f.p + step, 16);
+        cp_async16(d0 + 1024, f.p + 2 * step, 16);
+        cp_async16(d1 + 1024, f.p + 3 * step, 16);
         if (lane < 16) {
-            const bool in = row0 + lane < a.N;
-            const __half *src = in ? a.ws + (size_t)(row0 + lane) * G + st * gs : a.ws;
             const uint32_t dst = base + 2048 + lane * 16;
-            if (gs == 8) cp_async_ca<16>(dst, src, in ? 16 : 0);
-            else if (gs == 4) cp_async_ca<8>(dst, src, in ? 8 : 0);
-            else cp_async_ca<4>(dst, src, in ? 4 : 0);
+            if (gs == 8) cp_async16(dst, f.q, 16);
+            else cp_async_ca<gs * 2>(dst, f.q, gs * 2);
         }
     } else {
+        const bool kin = (f.st * 8 + j) * 32 < a.K;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = kin && f.tile * 16 + r0 + 4 * i < a.N;
+            cp_async16((i & 1 ? d1 : d0) + (i >> 1) * 1024, in ? f.p + i * step : a.w, in ? 16 : 0);
+        }
+        const int G = a.K / a.group;
         __half *d = reinterpret_cast<__half *>(slot + 2048);
         for (int i = lane; i < 16 * gs; i += 32) {
-            const int r = i / gs, g = st * gs + i % gs;
-            d[r * 8 + i % gs] = row0 + r < a.N && g < G ? a.ws[(size_t)(row0 + r) * G + g] : __half();
+            const int r = i / gs, g = f.st * gs + i % gs, row = f.tile * 16 + r;
+            d[r * 8 + i % gs] = row < a.N && g < G ? a.ws[(size_t)row * G + g] : __half();
         }
     }
 }
@@ -232,12 +252,19 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
     pdl_wait();
     pdl_trigger();
     // fill the ring; a commit per stage keeps the group count fixed
-    int ptile = first, pst = sub, pslot = 0;
+    Q4Feed feed;
+    q4_seek(a, feed, first, sub);
+    int pslot = 0;
     auto issue_next = [&]() {
-        if (ptile < tiles) {
-            q4_issue(a, ring + pslot * kQ4Stage, ptile * 16, pst);
-            pst += a.W;
-            if (pst >= a.KC) pst = sub, ptile += step;
+        if (feed.tile < tiles) {
+            q4_issue<GL>(a, feed, ring + pslot * kQ4Stage);
+            feed.st += a.W;
+            if (feed.st >= a.KC) {
+                q4_seek(a, feed, feed.tile + step, sub);
+            } else {
+                feed.p += a.W * 128;
+                feed.q += a.W * (8 / GL);
+            }
         }
         cp_async_commit();
         if (++pslot == a.stages) pslot = 0;
@@ -356,7 +383,7 @@ bool q4_plan(int N, int K, int cols, int group, bool split, Q4Plan &p) {
     for (; p.NT >= 1; p.NT >>= 1) {
         p.W = 1;
         if (p.NT < 4)
-            while (p.W < 8 && 2 * p.W <= KC) p.W *= 2;
+            while (p.W < 8 && 2 * p.W <= KC && tiles * p.W < 152 * kQ4Warps * kQ4Rounds) p.W *= 2;
         for (; p.W >= 1; p.W >>= 1)
             for (p.stages = kQ4MaxStages; p.stages >= 2; --p.stages)
                 if (Q4Layout(KC, p.NT, split, group, p.W, p.stages).total <= room) return true;

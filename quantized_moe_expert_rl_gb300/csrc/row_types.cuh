@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "rl_common.cuh"
 
 namespace rl {
@@ -50,6 +52,44 @@ template <>
 __device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+// v = a + b rounded to the element type.  A 16-bit add rounds the exact sum once, which is what adding in
+// f32 and rounding gives: the f32 sum is exact unless the smaller term is below 2^-8 of half a step.
+template <typename E>
+__device__ __forceinline__ void add8(const E *a, const E *b, float (&v)[8]) {
+    const uint4 p = *reinterpret_cast<const uint4 *>(a), q = *reinterpret_cast<const uint4 *>(b);
+    const uint32_t x[4] = {p.x, p.y, p.z, p.w}, y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t s;
+        if constexpr (sizeof(E) == 2) {
+            using E2 = typename std::conditional<std::is_same<E, __half>::value, __half2, __nv_bfloat162>::type;
+            const E2 t = __hadd2_rn(*reinterpret_cast<const E2 *>(&x[i]), *reinterpret_cast<const E2 *>(&y[i]));
+            s = *reinterpret_cast<const uint32_t *>(&t);
+        }
+        const float2 f = unpack2(s, E());
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+template <>
+__device__ __forceinline__ void add8<float>(const float *a, const float *b, float (&v)[8]) {
+    float w[8];
+    load8(a, v);
+    load8(b, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
+}
+// larger magnitude; a NaN wins
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
