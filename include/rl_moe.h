@@ -428,8 +428,9 @@ rl_status rl_add_rmsnorm(const void *x, const void *res, const float *gain, int3
  * w_scale IEEE half [N][K / group]; group 32, 64 or 128, K a multiple of it, K <= 8192, N <= 2^26.
  * x [T][K] of x_dtype: RL_F32, RL_F16, RL_BF16, or RL_F8_E4M3 with x_scale f32 [T][K / group] (else
  * NULL), as rl_add_rmsnorm writes them with the same group.  y [T][N] of y_dtype (not
- * RL_F8_E4M3), rounded once.  f32 accumulation; f32 activations carry at least 22 bits relative to
- * the largest of their group.  An infinity or a NaN in x reaches its own token's outputs only.
+ * RL_F8_E4M3), rounded once.  f32 accumulation; f32 activations are held to 22 bits each, and f32,
+ * f16 and bf16 ones to no finer than 2^-38 of their row's largest magnitude.  An infinity or a NaN in
+ * x reaches its own token's outputs only.
  * Any T >= 0; weights are read once per 32 (or, with f32 x or a small matrix, 16 or 8) columns.
  * w, w_scale, x 16-byte aligned; y must not overlap an input.
  */

@@ -46,7 +46,8 @@ __device__ __forceinline__ float row_reduce(float v, float *part, int warp0, int
     return r;
 }
 
-template <typename E, int NC>
+// GL: lanes per group of the 8-bit copy (0: no copy)
+template <typename E, int NC, int GL>
 __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
     __shared__ float part[32];
     const int rowi = threadIdx.x / a.tpr, tr = threadIdx.x - rowi * a.tpr;
@@ -61,14 +62,17 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int h = 8 * (c * a.tpr + tr);
-        const bool in = live && h < a.H;
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[c][j] = 0.f;
-        if (in) {
+        if (live && h < a.H) {
             if (a.res) add8(static_cast<const E *>(a.x) + base + h, static_cast<const E *>(a.res) + base + h, s[c]);
             else load8(static_cast<const E *>(a.x) + base + h, s[c]);
-            if (a.x_out) store8(static_cast<E *>(a.x_out) + base + h, s[c]);
         }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int h = 8 * (c * a.tpr + tr);
+        if (a.x_out && live && h < a.H) store8(static_cast<E *>(a.x_out) + base + h, s[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(s[c][j], s[c][j], ss);
     }
@@ -99,7 +103,6 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
         if (odd && fin && s2 == s2)
             r = (float)(1.0 / sqrt(ldexp((double)s2 / a.H, 2 * ex) + (double)a.eps));
     }
-    const int gl = a.group >> 3;  // lanes per group
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int h = 8 * (c * a.tpr + tr);
@@ -114,13 +117,14 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
             for (int j = 0; j < 8; ++j) v[j] = s[c][j] * r;
         }
         if (a.xn && in) store8(static_cast<E *>(a.xn) + base + h, v);
-        if (!a.q) continue;
+        if (GL == 0) continue;
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max_abs_nan(m, v[j]);
-        for (int o = 1; o < gl; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
+#pragma unroll
+        for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
         if (!in) continue;
-        float sc = m / 448.0f, inv = 448.0f / m;
+        float sc = m * (1.0f / 448.0f), inv = __fdividef(448.0f, m);
         if (!(m >= 1e-30f && m < __int_as_float(0x7f800000))) {  // zeros, far below f32's range, infinity or NaN
             inv = 0.f;
             if (!(m < __int_as_float(0x7f800000))) {
@@ -137,22 +141,26 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
             o8.y = pack4_e4m3(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
         }
         *reinterpret_cast<uint2 *>(a.q + base + h) = o8;
-        if ((lane & (gl - 1)) == 0) a.scale[(size_t)row * (a.H / a.group) + h / a.group] = sc;
+        if ((lane & (GL - 1)) == 0) a.scale[(size_t)row * (a.H / (8 * (GL ? GL : 1))) + h / (8 * (GL ? GL : 1))] = sc;
     }
 }
 
 template <typename E>
 rl_status launch_norm(NormArgs &a, cudaStream_t s) {
-    // Two runs of 8 values per thread for rows of 2048 values and more, if there are rows enough to fill
-    // the GPU: the row's reduction and addressing then cost half as many instructions per value.
-    const int oct = a.H / 8;
-    const int nc = oct > 1024 || (oct >= 256 && a.T >= 2 * 152) ? 2 : 1;
+    // A thread per 8 values up to rows of 8192 (two runs per thread beyond).  Two and four runs per thread,
+    // which leave fewer warps to meet per row, measured the same to 15% slower from 2048 rows on.
+    const int oct = a.H / 8, nc = oct > 1024 ? 2 : 1;
     a.tpr = (int)align_up((size_t)(oct + nc - 1) / nc, 32);
     a.rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
     if (a.rows > a.T) a.rows = a.T;
     const dim3 grid((a.T + a.rows - 1) / a.rows), block(a.tpr * a.rows);
-    return nc == 2 ? launch_pdl(add_norm_kernel<E, 2>, grid, block, 0, s, "rl_add_rmsnorm", a)
-                   : launch_pdl(add_norm_kernel<E, 1>, grid, block, 0, s, "rl_add_rmsnorm", a);
+#define RL_NORM(NC)                                                                                             \
+    (a.group == 0    ? launch_pdl(add_norm_kernel<E, NC, 0>, grid, block, 0, s, "rl_add_rmsnorm", a)              \
+     : a.group == 32 ? launch_pdl(add_norm_kernel<E, NC, 4>, grid, block, 0, s, "rl_add_rmsnorm", a)              \
+     : a.group == 64 ? launch_pdl(add_norm_kernel<E, NC, 8>, grid, block, 0, s, "rl_add_rmsnorm", a)              \
+                     : launch_pdl(add_norm_kernel<E, NC, 16>, grid, block, 0, s, "rl_add_rmsnorm", a))
+    return nc == 2 ? RL_NORM(2) : RL_NORM(1);
+#undef RL_NORM
 }
 
 }  // namespace
@@ -180,7 +188,7 @@ extern "C" rl_status rl_add_rmsnorm(const void *x, const void *res, const float 
         return fail(RL_ERR_INVALID, "rl_add_rmsnorm: x, res, gain, x_out, xn and q must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(scale) & 3)
         return fail(RL_ERR_INVALID, "rl_add_rmsnorm: scale must be 4-byte aligned");
-    NormArgs a = {x, res, gain, x_out, xn, q, scale, eps, T, H, 0, 0, q ? group : 32};
+    NormArgs a = {x, res, gain, x_out, xn, q, scale, eps, T, H, 0, 0, q ? group : 0};
     cudaStream_t s = as_stream(stream);
     if (dtype == RL_F32) return launch_norm<float>(a, s);
     if (dtype == RL_F16) return launch_norm<__half>(a, s);

@@ -4,19 +4,25 @@
 //   lse = m + log S,  S = sum e^(x - m),  U = sum (x - m) e^(x - m),  m = max x
 //   logprob = x_target - lse,  entropy = log S - U / S
 //
-// A row is split into segments, one CTA each; a CTA streams its segment in tiles of 4096 values
-// held in registers.  Every thread keeps a running (m, S, U): when a tile raises m by d, S and U
-// are rescaled by e^-d (U loses d S first).  The segments' triples meet in the row's last CTA to
-// finish (a completion counter in the workspace), which merges them in segment order, so results
-// do not depend on arrival order.
+// The logits of all rows are one long array, cut into equal runs, one per CTA (three CTAs per SM), so
+// that any number of rows keeps the GPU evenly busy.  A CTA streams its run in tiles of 4096 values;
+// every thread copies the 16-byte pieces that it will read itself, three tiles
+// ahead and on across the rows, so that no barrier stands between the copies and their use.  Rows
+// that lie whole in a run are finished at once.  Every thread keeps a running (m, S, U): when a tile raises m by d, S and U are rescaled by
+// e^-d (U loses d S first).  The pieces of a row cut by a run's end meet in the last of their CTAs to
+// finish (a completion counter in the workspace), which merges them in row order, so results do not
+// depend on arrival order.
 //
 // Top n.  A candidate is a 64-bit key, order-preserving logit above ~index, so that keys are
 // distinct and equal logits go to the lower index.  Only keys above a threshold are kept, in a buffer
 // that is cut back to its n best whenever it holds more than 128, by counting for every key the
-// larger ones.  The first tile sets the threshold: the CTA's 64 groups of 4 threads each publish
+// larger ones.  A row's first tile sets the threshold: the CTA's 64 groups of 4 threads each publish
 // their largest key, and the n-th largest of the 64 bounds the tile's n-th largest from below, which
-// leaves at most n groups x 64 values.  Later tiles put their few survivors straight into the buffer;
-// a tile that overflows it (rising logits) is taken back and goes the first tile's way.
+// leaves at most n groups x 64 values.  Later tiles put their few survivors straight into the buffer,
+// without a barrier; every fourth tile the CTA meets, cuts the buffer back if need be, and if it
+// overflowed (rising logits) goes through those tiles again the first tile's way.
+#include <math.h>
+
 #include "qdot.cuh"
 #include "row_types.cuh"
 #include "select.cuh"
@@ -26,9 +32,11 @@ using namespace rl;
 namespace {
 
 constexpr int kLpThreads = 256, kLpEpt = 16, kLpTile = kLpThreads * kLpEpt;
-constexpr int kLpMaxN = 32, kLpMaxSeg = 32;
-constexpr int kLpMaxRows = 4096;                    // rows of one launch (more rows: more launches)
-constexpr int kLpCtas = 8 * 152;
+constexpr int kLpMaxN = 32;
+constexpr int kLpMaxCtas = 3 * 152;
+constexpr int kLpMaxPieces = 64;                    // of one row
+constexpr int kLpDepth = 3;                         // tiles on their way
+constexpr int kLpTurn = 4;                          // tiles between two meetings of the CTA
 constexpr int kLpKeep = 128;                        // the buffer is cut back beyond this many
 constexpr int kLpCap = kLpKeep + 64 * kLpMaxN;      // and never holds more than this
 constexpr float kLog2e = 1.4426950408889634f;
@@ -39,10 +47,11 @@ struct LpArgs {
     float *logprob, *entropy;
     int32_t *top_ids;
     float *top_logprob;
-    float *part;               // [T][segs][4] (m, S, U)
-    unsigned long long *keys;  // [T][segs][n]
-    uint32_t *done;            // [T], zero between calls
-    int V, n, segs, seglen;
+    float *part;               // [CTAs][2][4] (m, S, U) of the run's first and last piece
+    unsigned long long *keys;  // [CTAs][2][n]
+    uint32_t *done;            // [CTAs], by the CTA of a row's first piece; zero between calls
+    long long total, run;      // values in all, per CTA
+    int V, n, per_row;         // per_row > 0: that many CTAs per row, none over a row's end
 };
 
 struct LpShared {
@@ -50,14 +59,26 @@ struct LpShared {
     unsigned long long sorted[kLpMaxN];
     unsigned long long heads[64];
     unsigned long long thr;
-    float red[3][kLpThreads / 32];
-    int count, last;
+    float red[3][kLpThreads / 32], xt[2];
+    int count, merge[2];
 };
 
 __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+__device__ __forceinline__ unsigned long long dup2(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ unsigned long long fadd2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long fmul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // (m, S, U) of two disjoint parts
@@ -78,12 +99,16 @@ __device__ __forceinline__ void lp_merge(float &m, float &S, float &U, float m2,
 
 // The n largest of the `cnt` (> 0) keys in sh.cand, in descending order, into sh.sorted; with
 // `keep` also back into sh.cand with the threshold at the n-th.  Whole CTA.
-__device__ __forceinline__ void lp_sort(LpShared &sh, int cnt, int n, bool keep) {
-    for (int i = threadIdx.x; i < cnt; i += kLpThreads) {
-        const unsigned long long k = sh.cand[i];
+__device__ __noinline__ void lp_sort(LpShared &sh, int cnt, int n, bool keep) {
+    for (int i0 = 0; i0 < cnt; i0 += kLpThreads / 8) {  // 8 lanes per key
+        const int i = i0 + (threadIdx.x >> 3);
+        const unsigned long long k = i < cnt ? sh.cand[i] : 0ull;
         int rank = 0;
-        for (int j = 0; j < cnt; ++j) rank += sh.cand[j] > k ? 1 : 0;
-        if (rank < n) sh.sorted[rank] = k;
+#pragma unroll 4
+        for (int j = threadIdx.x & 7; j < cnt; j += 8) rank += sh.cand[j] > k ? 1 : 0;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
+        if (i < cnt && rank < n && (threadIdx.x & 7) == 0) sh.sorted[rank] = k;
     }
     cta_sync();
     if (keep) {
@@ -96,44 +121,29 @@ __device__ __forceinline__ void lp_sort(LpShared &sh, int cnt, int n, bool keep)
     }
 }
 
-// Put the keys (0 = none) above the threshold into the buffer.  Whole CTA; the buffer holds at
-// most kLpKeep keys before the call and fewer than or as many after it.
+// Put the keys (0 = none) above the threshold into the buffer, after raising the threshold to the
+// n-th largest of the 64 groups' largest keys.  Whole CTA; the buffer holds at most kLpKeep keys before
+// the call and as many after it.
 template <int M>
 __device__ __forceinline__ void lp_insert(LpShared &sh, const unsigned long long (&key)[M], int n) {
-    const int lane = threadIdx.x & 31;
-    const unsigned long long thr = sh.thr;
-    const int before = sh.count;
-    int c = 0;
+    unsigned long long m = 0ull;
 #pragma unroll
-    for (int i = 0; i < M; ++i) c += key[i] > thr ? 1 : 0;
-    int total = c;
+    for (int i = 0; i < M; ++i) m = key[i] > m ? key[i] : m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
-    cta_sync();  // everybody has read thr and count
-    if (lane == 0 && total) atomicAdd(&sh.count, total);
-    cta_sync();
-    const bool over = sh.count - before > kLpKeep;
-    cta_sync();
-    if (threadIdx.x == 0) sh.count = before;
-    if (over) {  // raise the threshold to the n-th largest of the 64 groups' largest keys
-        unsigned long long m = 0ull;
-#pragma unroll
-        for (int i = 0; i < M; ++i) m = key[i] > m ? key[i] : m;
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            const unsigned long long v = __shfl_xor_sync(kFull, m, o);
-            m = v > m ? v : m;
-        }
-        if ((threadIdx.x & 3) == 0) sh.heads[threadIdx.x >> 2] = m;
-        cta_sync();
-        if (threadIdx.x < 64) {
-            const unsigned long long k = sh.heads[threadIdx.x];
-            int rank = 0;
-            for (int j = 0; j < 64; ++j) rank += (sh.heads[j] > k || (sh.heads[j] == k && j < threadIdx.x)) ? 1 : 0;
-            // one below the n-th head, so that the head itself passes
-            if (rank == n - 1 && k > 0ull && k - 1ull > thr) sh.thr = k - 1ull;
-        }
+    for (int o = 1; o < 4; o <<= 1) {
+        const unsigned long long v = __shfl_xor_sync(kFull, m, o);
+        m = v > m ? v : m;
     }
+    if ((threadIdx.x & 3) == 0) sh.heads[threadIdx.x >> 2] = m;
+    cta_sync();
+    // rank of this group's head, 16 comparisons per lane (equal heads are all 0)
+    int rank = 0;
+#pragma unroll 8
+    for (int j = threadIdx.x & 3; j < 64; j += 4) rank += sh.heads[j] > m ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
+    // one below the n-th head, so that the head itself passes
+    if ((threadIdx.x & 3) == 0 && rank == n - 1 && m > 0ull && m - 1ull > sh.thr) sh.thr = m - 1ull;
     cta_sync();
     const unsigned long long t2 = sh.thr;
 #pragma unroll
@@ -141,235 +151,488 @@ __device__ __forceinline__ void lp_insert(LpShared &sh, const unsigned long long
         if (key[i] > t2) sh.cand[atomicAdd(&sh.count, 1)] = key[i];
     cta_sync();
     const int cnt = sh.count;
-    if (cnt > kLpKeep) lp_sort(sh, cnt, n, true);
+    if (cnt > kLpKeep) {
+        cta_sync();
+        lp_sort(sh, cnt, n, true);
+    }
 }
 
 __device__ __forceinline__ unsigned long long lp_key(float v, int idx) {
     return ((unsigned long long)order_key(v) << 32) | (uint32_t)~idx;
 }
 
-// Final outputs of a row from its (m, S, U) and the n sorted keys in sh.sorted
+// one value at a shared-window address
 template <typename E>
-__device__ __forceinline__ void lp_finish(const LpArgs &a, LpShared &sh, int row, float m, float S, float U) {
-    const float ninf = __int_as_float(0xff800000);
+__device__ __forceinline__ float lds_value(uint32_t at) {
+    if constexpr (sizeof(E) == 4) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+        return v;
+    } else {
+        const unsigned short b = (unsigned short)lds_u16(at);
+        return to_float(*reinterpret_cast<const E *>(&b));
+    }
+}
+
+// Where the 16-byte pieces of a tile lie in a row: piece j of this thread starts at value
+// t0 + (256 j + tid) EV of the row; -inf outside [lo, hi).
+template <typename E>
+struct LpTile {
+    static constexpr int EV = 16 / sizeof(E), NV = kLpEpt / EV;  // values per piece, pieces per thread
+    // first tile of values from l on: pieces start at aligned addresses, up to EV - 1 values before l
+    static __device__ __forceinline__ int first(const E *p, int l) {
+        return l - (int)((reinterpret_cast<uintptr_t>(p + l) & 15) / sizeof(E));
+    }
+    static __device__ __forceinline__ uint4 edge(const E *p, int l, int h, int i0) {
+        E e[EV];
+#pragma unroll
+        for (int k = 0; k < EV; ++k) e[k] = i0 + k >= l && i0 + k < h ? p[i0 + k] : from_float<E>(-INFINITY);
+        return *reinterpret_cast<const uint4 *>(e);
+    }
+    static __device__ __forceinline__ void unpack(const uint4 (&q)[NV], float (&v)[kLpEpt]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                if constexpr (sizeof(E) == 4) {
+                    v[j * EV + p] = __uint_as_float(w[p]);
+                } else {
+                    const float2 f = unpack2(w[p], E());
+                    v[j * EV + 2 * p] = f.x, v[j * EV + 2 * p + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+
+// The cold parts are functions of their own, so that the tile loop keeps its registers.
+
+// Tiles t0, t0 + kLpTile, .. t1 into the buffer with the threshold raised tile by tile; from ring slot
+// `slot` (one tile), or 0 for the logits' own memory.  Whole CTA.
+template <typename E>
+__device__ __noinline__ void lp_robust(LpShared &sh, const E *x, int lo, int hi, int t0, int t1, int n, uint32_t slot) {
+    using Tile = LpTile<E>;
+#pragma unroll 1
+    for (int tt = t0; tt <= t1; tt += kLpTile) {
+        uint4 q[Tile::NV];
+        float v[kLpEpt];
+#pragma unroll
+        for (int j = 0; j < Tile::NV; ++j) {
+            const int i0 = tt + (j * kLpThreads + threadIdx.x) * Tile::EV;
+            q[j] = !(i0 >= lo && i0 + Tile::EV <= hi) ? Tile::edge(x, lo, hi, i0)
+                   : slot ? lds128(slot + j * kLpThreads * 16) : *reinterpret_cast<const uint4 *>(x + i0);
+        }
+        Tile::unpack(q, v);
+        unsigned long long key[kLpEpt];
+#pragma unroll
+        for (int i = 0; i < kLpEpt; ++i) {
+            const int idx = tt + ((i / Tile::EV) * kLpThreads + threadIdx.x) * Tile::EV + i % Tile::EV;
+            key[i] = idx >= lo && idx < hi ? lp_key(v[i], idx) : 0ull;
+        }
+        lp_insert(sh, key, n);
+    }
+    cta_sync();
+}
+
+// Final outputs of a row from its (m, S, U), its target's logit xt (thread t = 0; NaN for a target outside
+// the vocabulary) and its n best keys in order (thread t has the t-th)
+__device__ __forceinline__ void lp_finish(const LpArgs &a, int t, unsigned long long k, int row, float m, float S,
+                                          float U, float xt) {
+    const float ninf = -INFINITY, nan = __int_as_float(0x7fffffff);
     // a row of -inf only: no distribution; -inf for every token, entropy 0
     const bool empty = m == ninf && S == 0.f;
     const float ls = logf(S);
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         if (a.entropy) a.entropy[row] = empty ? 0.f : ls - U / S;
-        if (a.logprob) {
-            const int t = a.targets[row];
-            float v = __int_as_float(0x7fffffff);
-            if (t >= 0 && t < a.V) {
-                const float x = to_float(static_cast<const E *>(a.x)[(size_t)row * a.V + t]);
-                v = empty ? ninf : (x - m) - ls;
-                if (S != S) v = S;
-            }
-            a.logprob[row] = v;
-        }
+        if (a.logprob) a.logprob[row] = S != S || xt != xt ? nan : empty ? ninf : (xt - m) - ls;
     }
-    if (threadIdx.x < a.n) {
-        const unsigned long long k = sh.sorted[threadIdx.x];
+    if (t < a.n) {
         const uint32_t hi = (uint32_t)(k >> 32);
-        a.top_ids[(size_t)row * a.n + threadIdx.x] = (int)~(uint32_t)k;
-        float v = hi == 0u ? __int_as_float(0x7fffffff) : (empty ? ninf : (key_value(hi) - m) - ls);
-        if (S != S) v = S;
-        a.top_logprob[(size_t)row * a.n + threadIdx.x] = v;
+        a.top_ids[(size_t)row * a.n + t] = (int)~(uint32_t)k;
+        a.top_logprob[(size_t)row * a.n + t] = S != S || hi == 0u ? nan : empty ? ninf : (key_value(hi) - m) - ls;
+    }
+}
+
+// the lanes' triples as one, in a fixed order; every lane ends with the same bits
+__device__ __forceinline__ void lp_merge_lanes(float &m, float &S, float &U) {
+    float M = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    // a side of -inf only has S = U = 0 (or NaN, which stays)
+    const float d = fmaxf(m - M, -1e4f), f = ex2(d * kLog2e);
+    U = f * fmaf(d, S, U);
+    S *= f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        S += __shfl_xor_sync(kFull, S, o);
+        U += __shfl_xor_sync(kFull, U, o);
+    }
+    m = M;
+}
+
+// The end of a piece: the CTA's triple and its n best keys; a whole row is finished, another is
+// published in slot `at`.  Leaves the buffer empty.
+__device__ __noinline__ void lp_piece_end(const LpArgs &a, LpShared &sh, int row, bool whole, int at, float m, float S,
+                                          float U, float xt) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n;
+    lp_merge_lanes(m, S, U);
+    if (lane == 0) sh.red[0][warp] = m, sh.red[1][warp] = S, sh.red[2][warp] = U;
+    cta_sync();
+    const int mine = sh.count;
+    if (n > 0) lp_sort(sh, mine, n, false);
+    if (warp == 0) {  // the warps' triples, lane w holding warp w's
+        m = lane < kLpThreads / 32 ? sh.red[0][lane] : -INFINITY;
+        S = lane < kLpThreads / 32 ? sh.red[1][lane] : 0.f;
+        U = lane < kLpThreads / 32 ? sh.red[2][lane] : 0.f;
+        lp_merge_lanes(m, S, U);
+        if (whole) {
+            lp_finish(a, lane, lane < n ? sh.sorted[lane] : 0ull, row, m, S, U, xt);
+        } else {
+            if (lane < n) __stcg(a.keys + (size_t)at * n + lane, lane < mine ? sh.sorted[lane] : 0ull);
+            if (lane == 0) {
+                __stcg(a.part + 4 * at, m);
+                __stcg(a.part + 4 * at + 1, S);
+                __stcg(a.part + 4 * at + 2, U);
+                sh.xt[at & 1] = xt;
+            }
+        }
+        __syncwarp();
+    }
+    cta_sync();
+    if (tid == 0) {
+        sh.count = 0;
+        sh.thr = 0ull;
+    }
+    cta_sync();
+}
+
+// The rows of this run's first and last pieces (r0, r1; -1: none) that other CTAs hold pieces of: the last of
+// a row's CTAs to arrive merges them all, slot 1 of CTA c0, where the row begins, and slot 0 of the CTAs
+// after it up to c1.
+__device__ __noinline__ void lp_cut_rows(const LpArgs &a, LpShared &sh, int r0, int r1) {
+    const int tid = threadIdx.x, lane = tid & 31, n = a.n;
+    __threadfence();
+    cta_sync();
+    const int k = (tid >> 5) & 1, r = k ? r1 : r0;  // warp 0 takes r0, warp 1 r1
+    const long long at = (long long)(r < 0 ? 0 : r) * a.V;
+    const int c0 = a.per_row ? r * a.per_row : (int)(at / a.run);
+    const int c1 = a.per_row ? c0 + a.per_row - 1 : (int)((at + a.V - 1) / a.run);
+    const int total = (c1 - c0 + 1) * n;
+    const unsigned long long *keys = a.keys + (size_t)2 * c0 * n;
+    auto key_at = [&](int j) {  // piece 0 is slot 2 c0 + 1, piece i slot 2 (c0 + i)
+        return j < total ? __ldcg(keys + (j < n ? n + j : j / n * 2 * n + j % n)) : 0ull;
+    };
+    auto triple = [&](float &m, float &S, float &U) {
+        m = -INFINITY, S = 0.f, U = 0.f;
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            const float *p = a.part + 4 * (2 * (size_t)c + (c == c0 ? 1 : 0));
+            lp_merge(m, S, U, __ldcg(p), __ldcg(p + 1), __ldcg(p + 2));
+        }
+        __syncwarp();
+        lp_merge_lanes(m, S, U);
+    };
+    if (tid < 64) {
+        int last = 0;
+        if (r >= 0 && lane == 0) {
+            last = atomicAdd(a.done + c0, 1u) == (uint32_t)(c1 - c0);
+            if (last) a.done[c0] = 0u;
+            __threadfence();
+        }
+        last = __shfl_sync(kFull, last, 0);
+        if (last && total <= 64) {  // few keys: a warp ranks them by itself
+            unsigned long long *cand = sh.cand + k * 64;
+            unsigned long long key[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                key[i] = n > 0 ? key_at(lane + 32 * i) : 0ull;
+                cand[lane + 32 * i] = key[i];
+            }
+            float m, S, U;
+            triple(m, S, U);
+            __syncwarp();
+            int rank[2] = {};
+#pragma unroll 4
+            for (int j = 0; j < total; ++j) {
+                const unsigned long long o = cand[j];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) rank[i] += o > key[i] ? 1 : 0;
+            }
+            if (lane == 0 && n == 0) lp_finish(a, 0, 0ull, r, m, S, U, sh.xt[k]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (key[i] != 0ull && rank[i] < n) lp_finish(a, rank[i], key[i], r, m, S, U, sh.xt[k]);
+            last = 0;
+        }
+        if (lane == 0) sh.merge[k] = last;
+        __syncwarp();
+    }
+    cta_sync();
+    // many pieces: the CTA finds the best keys together
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+        if (!sh.merge[q]) continue;
+        if (n > 0) {
+            const int rr = q ? r1 : r0, cc = a.per_row ? rr * a.per_row : (int)((long long)rr * a.V / a.run);
+            const int ce = a.per_row ? cc + a.per_row - 1 : (int)(((long long)rr * a.V + a.V - 1) / a.run);
+            const unsigned long long *kk = a.keys + (size_t)2 * cc * n;
+            const int tt = (ce - cc + 1) * n;
+            constexpr int M = 4;
+            auto at = [&](int j) { return j < tt ? __ldcg(kk + (j < n ? n + j : j / n * 2 * n + j % n)) : 0ull; };
+            if (tt <= kLpThreads) {
+                sh.cand[tid] = at(tid);
+                if (tid == 0) sh.count = tt;
+                cta_sync();
+            } else {
+#pragma unroll 1
+                for (int base = 0; base < tt; base += M * kLpThreads) {
+                    unsigned long long key[M];
+#pragma unroll
+                    for (int i = 0; i < M; ++i) key[i] = at(base + i * kLpThreads + tid);
+                    lp_insert(sh, key, n);
+                    cta_sync();
+                }
+            }
+            lp_sort(sh, sh.count, n, false);
+        }
+        if ((tid >> 5) == q) {
+            float m, S, U;
+            triple(m, S, U);
+            lp_finish(a, lane, lane < n ? sh.sorted[lane] : 0ull, r, m, S, U, sh.xt[k]);
+        }
+        cta_sync();
+        if (tid == 0) {
+            sh.count = 0;
+            sh.thr = 0ull;
+        }
+        cta_sync();
     }
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const __grid_constant__ LpArgs a) {
+    using Tile = LpTile<E>;
+    constexpr int EV = Tile::EV, NV = Tile::NV;
+    constexpr float kNinf = -INFINITY;
     __shared__ LpShared sh;
-    const int row = blockIdx.y, seg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int EV = 16 / sizeof(E);       // values per 16-byte load
-    constexpr int NV = kLpEpt / EV;          // loads per thread and tile
+    extern __shared__ __align__(16) uint8_t ring_s[];
+    const int tid = threadIdx.x, n = a.n, V = a.V;
+    int row, lo;
+    long long left;  // values of the run from here on
+    if (a.per_row) {
+        row = blockIdx.x / a.per_row;
+        lo = (blockIdx.x - row * a.per_row) * (int)a.run;
+        left = lo + a.run < V ? a.run : V - lo;
+    } else {
+        const long long pos = a.run * blockIdx.x;
+        row = (int)(pos / V);
+        lo = (int)(pos - (long long)row * V);
+        left = pos + a.run < a.total ? a.run : a.total - pos;
+    }
+    const E *x = static_cast<const E *>(a.x) + (size_t)row * V;
+    int hi = lo + left < V ? (int)(lo + left) : V, r0 = -1, r1 = -1;
     if (tid == 0) {
         sh.count = 0;
         sh.thr = 0ull;
     }
     pdl_wait();
     pdl_trigger();
-    const E *x = static_cast<const E *>(a.x) + (size_t)row * a.V;
-    const int lo = seg * a.seglen, hi = min(a.V, lo + a.seglen);
-    // 16-byte loads start at aligned addresses: `mis` values of the first one lie before `lo`
-    const int mis = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15) / sizeof(E));
-    float m = __int_as_float(0xff800000), S = 0.f, U = 0.f;
+    // this thread's pieces of tile k of the run lie in slot k % kLpDepth; the cursor runs ahead across rows
+    const uint32_t ring = smem_addr(ring_s) + tid * 16;
+    constexpr uint32_t kPiece = kLpThreads * 16, kSlot = kPiece * NV;
+    int t0 = Tile::first(x, lo);
+    const E *px = x;
+    int plo = lo, phi = hi, pt0 = t0;
+    long long pleft = left;
+    uint32_t pslot = ring, slot = ring;
+    auto issue = [&]() {
+        if (pleft > 0) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i0 = pt0 + (j * kLpThreads + tid) * EV;
+                if (i0 >= plo && i0 + EV <= phi) cp_async16(pslot + j * kPiece, px + i0, 16);
+            }
+            pt0 += kLpTile;
+            if (pt0 >= phi) {
+                pleft -= phi - plo;
+                px += V;
+                plo = 0;
+                phi = pleft < V ? (int)pleft : V;
+                pt0 = Tile::first(px, 0);
+            }
+        }
+        pslot = pslot == ring + (kLpDepth - 1) * kSlot ? ring : pslot + kSlot;
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kLpDepth; ++k) issue();
     cta_sync();
-    for (int t0 = lo - mis; t0 < hi; t0 += kLpTile) {
-        float v[kLpEpt];
+#pragma unroll 1
+    for (;;) {  // the rows of the run
+        float m = kNinf, xt = __int_as_float(0x7fffffff);
+        if (tid == 0 && a.logprob) {  // the target's logit, while the first tile is on its way
+            const int t = a.targets[row];
+            if (t >= 0 && t < V) xt = to_float(x[t]);
+        }
+        unsigned long long S2 = 0ull, U2 = 0ull;  // packed pairs of partial sums
+        int since = 0, tb = t0, before = 0;       // tiles since the last meeting, the first of them, keys before it
+        const int begin = t0;
+#pragma unroll 1
+        for (; t0 < hi; t0 += kLpTile) {  // its tiles
+            float v[kLpEpt];
+            cp_async_wait_all_but<kLpDepth - 1>();
+            {
+                uint4 q[NV];
+                if (t0 >= lo && t0 + kLpTile <= hi) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i0 = t0 + (j * kLpThreads + tid) * EV;
-            if (i0 >= lo && i0 + EV <= hi) {
-                const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(x + i0));
-                if constexpr (sizeof(E) == 4) {
-                    v[j * EV] = __uint_as_float(q.x), v[j * EV + 1] = __uint_as_float(q.y);
-                    v[j * EV + 2] = __uint_as_float(q.z), v[j * EV + 3] = __uint_as_float(q.w);
-                } else {
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    for (int j = 0; j < NV; ++j) q[j] = lds128(slot + j * kPiece);
+                } else {  // pieces that reach over the ends are read value by value
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const float2 f = unpack2(w[p], E());
-                        v[j * EV + 2 * p] = f.x, v[j * EV + 2 * p + 1] = f.y;
+                    for (int j = 0; j < NV; ++j) {
+                        const int i0 = t0 + (j * kLpThreads + tid) * EV;
+                        if (i0 >= lo && i0 + EV <= hi) q[j] = lds128(slot + j * kPiece);
+                        else q[j] = Tile::edge(x, lo, hi, i0);
                     }
                 }
-            } else {
+                Tile::unpack(q, v);
+            }
+            float tm = v[0];
 #pragma unroll
-                for (int p = 0; p < EV; ++p) {
-                    const int i = i0 + p;
-                    v[j * EV + p] = i >= lo && i < hi ? to_float(x[i]) : __int_as_float(0xff800000);
+            for (int i = 1; i < kLpEpt; ++i) tm = max_nan(tm, v[i]);
+            const bool nan = tm != tm;
+            if (nan) {  // the row's sums are NaN; its top values still come from the numbers
+                tm = kNinf;
+#pragma unroll
+                for (int i = 0; i < kLpEpt; ++i) tm = fmaxf(tm, v[i]);
+                S2 = U2 = 0x7fffffff7fffffffull;
+            }
+            if (tm > m) {
+                if (m > kNinf) {
+                    const float d = fmaxf(m - tm, -1e4f), f = ex2(d * kLog2e);
+                    U2 = fmul2(dup2(f), ffma2(dup2(d), S2, U2));
+                    S2 = fmul2(dup2(f), S2);
                 }
+                m = tm;
             }
-        }
-        float tm = v[0];
+            if (m > kNinf) {
+                const unsigned long long nm = dup2(-m), l2 = dup2(kLog2e), u0 = U2;
 #pragma unroll
-        for (int i = 1; i < kLpEpt; ++i) tm = max_nan(tm, v[i]);
-        const bool nan = tm != tm;
-        if (nan) {  // the row's sums are NaN; its top values still come from the numbers
-            tm = __int_as_float(0xff800000);
+                for (int i = 0; i < kLpEpt; i += 2) {
+                    const unsigned long long d = fadd2(pack2(__float_as_uint(v[i]), __float_as_uint(v[i + 1])), nm);
+                    const unsigned long long t = fmul2(d, l2);
+                    const unsigned long long e = pack2(__float_as_uint(ex2(__uint_as_float((uint32_t)t))),
+                                                       __float_as_uint(ex2(__uint_as_float((uint32_t)(t >> 32)))));
+                    S2 = fadd2(S2, e);
+                    U2 = ffma2(d, e, U2);
+                }
+                const float u = hsum2(U2);
+                if (u != u) {  // a value of -inf (its 0 * -inf contributes 0), or a NaN
+                    U2 = u0;
 #pragma unroll
-            for (int i = 0; i < kLpEpt; ++i) tm = fmaxf(tm, v[i]);
-            S = U = __int_as_float(0x7fffffff);
-        }
-        if (tm > m) {
-            if (S > 0.f) {
-                const float d = fmaxf(m - tm, -1e4f), f = ex2(d * kLog2e);
-                U = f * fmaf(d, S, U);
-                S *= f;
-            }
-            m = tm;
-        }
-        if (m > __int_as_float(0xff800000)) {
-#pragma unroll
-            for (int i = 0; i < kLpEpt; ++i) {
-                const float d = v[i] - m, e = ex2(d * kLog2e);
-                S += e;
-                U = fmaf(fmaxf(d, -1e4f), e, U);  // -inf contributes 0
-            }
-        }
-        if (a.n == 0) continue;
-        auto key_at = [&](int i) {
-            const int idx = t0 + ((i / EV) * kLpThreads + tid) * EV + i % EV;
-            return idx >= lo && idx < hi ? lp_key(v[i], idx) : 0ull;
-        };
-        bool robust = t0 <= lo;  // the first tile
-        if (!robust) {
-            const unsigned long long thr = sh.thr;
-            const int before = sh.count;
-            const bool pass = nan || order_key(tm) >= (uint32_t)(thr >> 32);
-            // a vote on both sides of the insertions: nobody inserts before everybody has read the count
-            if (!cta_sync_or(pass)) continue;
-            if (pass) {
-#pragma unroll
-                for (int i = 0; i < kLpEpt; ++i) {
-                    const unsigned long long k = key_at(i);
-                    if (k > thr) {
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < kLpCap) sh.cand[at] = k;
+                    for (int i = 0; i < kLpEpt; i += 2) {
+                        const float d0 = v[i] - m, d1 = v[i + 1] - m;
+                        const float c0 = fmaxf(d0, -1e4f) * ex2(d0 * kLog2e), c1 = fmaxf(d1, -1e4f) * ex2(d1 * kLog2e);
+                        U2 = fadd2(U2, pack2(__float_as_uint(c0), __float_as_uint(c1)));
                     }
                 }
             }
-            cta_sync();
-            const int cnt = sh.count;
-            if (cnt <= kLpKeep) continue;
-            robust = cnt > kLpCap;
-            cta_sync();
-            if (robust) {  // take the tile's insertions back
-                if (tid == 0) sh.count = before;
+            if (n > 0 && t0 != begin) {
+                const unsigned long long thr = sh.thr;
+                const uint32_t th = (uint32_t)(thr >> 32);
+                if (nan || order_key(tm) >= th) {
+                    const float tv = th ? key_value(th) : __int_as_float(0x7fffffff);
+                    uint32_t pass = 0u;
+#pragma unroll
+                    for (int i = 0; i < kLpEpt; ++i) pass |= v[i] < tv ? 0u : 1u << i;
+                    while (pass) {  // a value in thousands: read again where it lies
+                        const int i = __ffs(pass) - 1, idx = t0 + ((i / EV) * kLpThreads + tid) * EV + i % EV;
+                        pass &= pass - 1u;
+                        if (idx < lo || idx >= hi) continue;
+                        const uint32_t at_s = slot + (i / EV) * kPiece + (i % EV) * (int)sizeof(E);
+                        const bool inner = idx - i % EV >= lo && idx - i % EV + EV <= hi;  // else not in the ring
+                        const float w = !inner ? to_float(x[idx]) : lds_value<E>(at_s);
+                        const unsigned long long k = lp_key(w, idx);
+                        if (k > thr) {
+                            const int at = atomicAdd(&sh.count, 1);
+                            if (at < kLpCap) sh.cand[at] = k;
+                        }
+                    }
+                }
+                __syncwarp();  // rejoin the warp (see cta_sync): here, where every lane comes by
+            }
+            if (n > 0 && t0 == begin) lp_robust(sh, x, lo, hi, t0, t0, n, slot);
+            slot = slot == ring + (kLpDepth - 1) * kSlot ? ring : slot + kSlot;
+            issue();  // into the slot just read
+            if (n == 0) continue;
+            if (t0 == begin) {
+                before = sh.count;
+                tb = t0 + kLpTile;
                 cta_sync();
-            } else {
-                lp_sort(sh, cnt, a.n, true);
+                continue;
+            }
+            if (++since == kLpTurn || t0 + kLpTile >= hi) {
+                cta_sync();
+                const int cnt = sh.count;
+                cta_sync();  // everybody has read the count
+                if (cnt > kLpCap) {  // again, from the tiles' memory
+                    if (tid == 0) sh.count = before;
+                    cta_sync();
+                    lp_robust(sh, x, lo, hi, tb, t0, n, 0u);
+                } else if (cnt > kLpKeep) {
+                    lp_sort(sh, cnt, n, true);
+                }
+                before = sh.count;
+                since = 0;
+                tb = t0 + kLpTile;
+                cta_sync();
             }
         }
-        if (robust) {
-            unsigned long long key[kLpEpt];
-#pragma unroll
-            for (int i = 0; i < kLpEpt; ++i) key[i] = key_at(i);
-            lp_insert(sh, key, a.n);
+        const bool whole = lo == 0 && hi == V;
+        if (!whole) {
+            if (lo == 0) r1 = row;
+            else r0 = row;
         }
+        lp_piece_end(a, sh, row, whole, 2 * blockIdx.x + (lo == 0 ? 1 : 0), m, hsum2(S2), hsum2(U2), xt);
+        left -= hi - lo;
+        if (left <= 0) break;
+        ++row;
+        x += V;
+        lo = 0;
+        hi = left < V ? (int)left : V;
+        t0 = Tile::first(x, 0);
     }
-    // the CTA's triple
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(kFull, m, o), S2 = __shfl_xor_sync(kFull, S, o), U2 = __shfl_xor_sync(kFull, U, o);
-        // the same order on both sides, so that every lane ends with the same bits
-        float ma = lane & o ? m2 : m, Sa = lane & o ? S2 : S, Ua = lane & o ? U2 : U;
-        lp_merge(ma, Sa, Ua, lane & o ? m : m2, lane & o ? S : S2, lane & o ? U : U2);
-        m = ma, S = Sa, U = Ua;
-    }
-    if (lane == 0) sh.red[0][warp] = m, sh.red[1][warp] = S, sh.red[2][warp] = U;
-    cta_sync();
-    m = sh.red[0][0], S = sh.red[1][0], U = sh.red[2][0];
-#pragma unroll
-    for (int w = 1; w < kLpThreads / 32; ++w) lp_merge(m, S, U, sh.red[0][w], sh.red[1][w], sh.red[2][w]);
-    const int mine = sh.count;
-    if (a.n > 0 && mine > 0) lp_sort(sh, mine, a.n, false);
-    if (a.segs == 1) {
-        lp_finish<E>(a, sh, row, m, S, U);
-        return;
-    }
-    // publish, then the last CTA of the row merges
-    const size_t at = (size_t)row * a.segs + seg;
-    if (tid < a.n) __stcg(a.keys + at * a.n + tid, tid < mine ? sh.sorted[tid] : 0ull);
-    if (tid == 0) {
-        __stcg(a.part + 4 * at, m);
-        __stcg(a.part + 4 * at + 1, S);
-        __stcg(a.part + 4 * at + 2, U);
-    }
-    __threadfence();
-    cta_sync();
-    if (tid == 0) sh.last = atomicAdd(a.done + row, 1u) == (uint32_t)a.segs - 1u;
-    cta_sync();
-    if (!sh.last) return;
-    __threadfence();
-    if (tid == 0) {
-        a.done[row] = 0u;
-        sh.count = 0;
-        sh.thr = 0ull;
-    }
-    cta_sync();
-    if (a.n > 0) {
-        constexpr int M = kLpMaxSeg * kLpMaxN / kLpThreads;
-        unsigned long long key[M];
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-            const int j = i * kLpThreads + tid;
-            key[i] = j < a.segs * a.n ? __ldcg(a.keys + (size_t)row * a.segs * a.n + j) : 0ull;
-        }
-        lp_insert(sh, key, a.n);
-        lp_sort(sh, sh.count, a.n, false);
-    }
-    const float *p = a.part + 4 * (size_t)row * a.segs;
-    m = __ldcg(p), S = __ldcg(p + 1), U = __ldcg(p + 2);
-    for (int s = 1; s < a.segs; ++s) lp_merge(m, S, U, __ldcg(p + 4 * s), __ldcg(p + 4 * s + 1), __ldcg(p + 4 * s + 2));
-    lp_finish<E>(a, sh, row, m, S, U);
+    if (r0 >= 0 || r1 >= 0) lp_cut_rows(a, sh, r0, r1);
 }
 
-// Segments per row: about eight CTAs per SM over all rows, but no segment shorter than one tile
-// (4096 values), which is what a single CTA reads in one round trip.
-int lp_segments(int T, int V) {
-    const int want = (kLpCtas + T - 1) / T, most = (V + kLpTile - 1) / kLpTile;
-    const int s = want < most ? want : most;
-    return s > kLpMaxSeg ? kLpMaxSeg : s;
+// Few values: every row in pieces of about one tile (4096 values, what a CTA reads in one round trip),
+// a CTA each.  Else equal runs over as many CTAs as the GPU holds at once (three per SM), but none
+// shorter than 1/62 of a row, so that a row has at most kLpMaxPieces pieces.
+void lp_runs(int T, int V, LpArgs &a, int &ctas) {
+    const long long total = (long long)T * V, tiles = (V + kLpTile - 1) / kLpTile;
+    const int most = kLpMaxPieces - 2, pieces = (int)(tiles < most ? tiles : most);
+    if ((long long)T * pieces <= kLpMaxCtas) {
+        a.run = (long long)align_up((V + pieces - 1) / pieces, 16);
+        a.per_row = (int)((V + a.run - 1) / a.run);
+        ctas = T * a.per_row;
+        return;
+    }
+    a.per_row = 0;
+    a.run = (total + kLpMaxCtas - 1) / kLpMaxCtas;
+    if (a.run < (V + most - 1) / most) a.run = (V + most - 1) / most;
+    ctas = (int)((total + a.run - 1) / a.run);
 }
 
 // Workspace: the completion counters (zero between calls, at the same place whatever the sizes),
-// then the triples and the keys of a launch's segments.
-constexpr size_t kLpDoneBytes = kLpMaxRows * sizeof(uint32_t);
-size_t lp_part_bytes(int T, int V) { return align_up((size_t)T * lp_segments(T, V) * 4 * sizeof(float), 256); }
+// then the triples and the keys of two pieces per CTA.
+constexpr size_t kLpDoneBytes = (kLpMaxCtas * sizeof(uint32_t) + 255) / 256 * 256;
+constexpr size_t kLpPartBytes = (kLpMaxCtas * 2 * 4 * sizeof(float) + 255) / 256 * 256;
 
 }  // namespace
 
 extern "C" size_t rl_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t top_n) {
     if (T <= 0 || V <= 0 || top_n < 0 || top_n > kLpMaxN) return 0;
-    size_t most = 0;  // the last launch of many rows may hold few rows in more segments
-    for (int t = T; t > 0; t -= kLpMaxRows) {
-        const int rows = t < kLpMaxRows ? t : kLpMaxRows;
-        const size_t b = lp_part_bytes(rows, V) + (size_t)rows * lp_segments(rows, V) * top_n * sizeof(unsigned long long);
-        most = b > most ? b : most;
-    }
-    return kLpDoneBytes + most;
+    return kLpDoneBytes + kLpPartBytes + (size_t)kLpMaxCtas * 2 * top_n * sizeof(unsigned long long);
 }
 
 extern "C" rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, int32_t V, const int32_t *targets,
@@ -398,29 +661,25 @@ extern "C" rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, i
     if (!ws || ws_bytes < need) return fail(RL_ERR_INVALID, "rl_logprobs: workspace of %zu B needed, %zu given", need, ws_bytes);
     if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(RL_ERR_INVALID, "rl_logprobs: ws must be 16-byte aligned");
     uint8_t *w8 = static_cast<uint8_t *>(ws);
-    for (int t0 = 0; t0 < T; t0 += kLpMaxRows) {
-        LpArgs a = {};
-        a.x = static_cast<const uint8_t *>(logits) + (size_t)t0 * V * es;
-        a.targets = targets ? targets + t0 : nullptr;
-        a.logprob = logprob ? logprob + t0 : nullptr;
-        a.entropy = entropy ? entropy + t0 : nullptr;
-        a.top_ids = top_ids ? top_ids + (size_t)t0 * top_n : nullptr;
-        a.top_logprob = top_logprob ? top_logprob + (size_t)t0 * top_n : nullptr;
-        const int rows = T - t0 < kLpMaxRows ? T - t0 : kLpMaxRows;
-        a.done = reinterpret_cast<uint32_t *>(w8);
-        a.part = reinterpret_cast<float *>(w8 + kLpDoneBytes);
-        a.keys = reinterpret_cast<unsigned long long *>(w8 + kLpDoneBytes + lp_part_bytes(rows, V));
-        a.V = V;
-        a.n = top_n;
-        a.segs = lp_segments(rows, V);
-        a.seglen = (int)align_up((V + a.segs - 1) / a.segs, 16);
-        a.segs = (V + a.seglen - 1) / a.seglen;
-        const dim3 grid(a.segs, rows), block(kLpThreads);
-        cudaStream_t s = as_stream(stream);
-        const rl_status st = dtype == RL_F32   ? launch_pdl(logprobs_kernel<float>, grid, block, 0, s, "rl_logprobs", a)
-                             : dtype == RL_F16 ? launch_pdl(logprobs_kernel<__half>, grid, block, 0, s, "rl_logprobs", a)
-                                               : launch_pdl(logprobs_kernel<__nv_bfloat16>, grid, block, 0, s, "rl_logprobs", a);
-        if (st != RL_OK) return st;
-    }
-    return RL_OK;
+    LpArgs a = {};
+    a.x = logits;
+    a.targets = targets;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprob = top_logprob;
+    a.done = reinterpret_cast<uint32_t *>(w8);
+    a.part = reinterpret_cast<float *>(w8 + kLpDoneBytes);
+    a.keys = reinterpret_cast<unsigned long long *>(w8 + kLpDoneBytes + kLpPartBytes);
+    a.total = (long long)T * V;
+    a.V = V;
+    a.n = top_n;
+    int ctas = 0;
+    lp_runs(T, V, a, ctas);
+    const dim3 grid(ctas), block(kLpThreads);
+    cudaStream_t s = as_stream(stream);
+    const size_t smem = (size_t)kLpDepth * kLpTile * es;
+    if (dtype == RL_F32) return launch_pdl(logprobs_kernel<float>, grid, block, smem, s, "rl_logprobs", a);
+    if (dtype == RL_F16) return launch_pdl(logprobs_kernel<__half>, grid, block, smem, s, "rl_logprobs", a);
+    return launch_pdl(logprobs_kernel<__nv_bfloat16>, grid, block, smem, s, "rl_logprobs", a);
 }

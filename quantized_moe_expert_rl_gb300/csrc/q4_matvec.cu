@@ -16,9 +16,10 @@
 // - mma.m16n8k16 takes 16 weight rows as A and 8 activation columns as B, f32 accumulation.
 // - The order of k inside a group is free as long as A and B agree, so the words go to the MMA as
 //   they lie in memory (ldmatrix hands lane (g, t) word t of row g), 8 values of k per word.
-// - Activations are laid out as B fragments once per CTA.  e4m3 values are exact in half precision;
-//   f16 and bf16 rows are scaled by a power of two per group (largest magnitude to 2^14), f32 rows
-//   are scaled the same way and split into two halves (22 bits and more) in two columns.
+// - Activations are laid out as B fragments once per CTA.  e4m3 values are exact in half precision and
+//   keep their group scales; f16 and bf16 rows are scaled by one power of two (the row's largest
+//   magnitude to 2^14, so that a half resolves 2^-38 of it), f32 rows the same way and split into two
+//   halves (22 bits) in two columns.
 //
 // Weights stream through per-warp rings of 16-byte asynchronous copies (16 rows x 256 values per
 // stage), swizzled so that ldmatrix meets no bank conflict.  W warps share a 16-row tile and add
@@ -32,9 +33,10 @@ namespace {
 
 constexpr int kQ4Threads = 512, kQ4Warps = kQ4Threads / 32;
 constexpr int kQ4Stage = 16 * 128 + 16 * 16;  // 16 rows x 256 nibbles, then 16 bytes of scales per row
-constexpr int kQ4MaxStages = 6;
 constexpr int kQ4MaxK = 8192;
-constexpr int kQ4Rounds = 1;
+
+// activations: e4m3 with group scales; f16 or bf16; f32 in two columns per token
+enum { kQ4F8 = 0, kQ4Half = 1, kQ4Split = 2 };
 
 struct Q4Args {
     const uint8_t *w;
@@ -48,32 +50,16 @@ struct Q4Args {
 
 struct Q4Layout {
     size_t o_sc, o_ring, o_red, total;
-    Q4Layout(int KC, int NT, int split, int group, int W, int stages) {
+    Q4Layout(int KC, int NT, int kind, int group, int W, int stages) {
+        const bool split = kind == kQ4Split;
         o_sc = (size_t)KC * 8 * NT * 512;
-        o_ring = o_sc + align_up((size_t)KC * (256 / group) * NT * (split ? 4 : 8) * sizeof(float), 128);
+        // e4m3: a scale per (group, token); else one per token, and its largest magnitude
+        o_ring = o_sc + align_up(kind == kQ4F8 ? (size_t)KC * (256 / group) * NT * 8 * sizeof(float) : (size_t)NT * 8 * 2 * sizeof(float), 128);
         o_red = o_ring + (size_t)kQ4Warps * stages * kQ4Stage;
         total = o_red + (W > 1 ? (size_t)2 * kQ4Warps * NT * (split ? 256 : 512) : 0);
     }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-template <int B>
-__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest n copy groups have landed (n < kQ4MaxStages - 1)
-__device__ __forceinline__ void cp_async_wait(int n) {
-    switch (n) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    }
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -120,33 +106,48 @@ __device__ __forceinline__ uint4 q4_fragment(const float (&v)[8]) {
 }
 
 // Lay the activations out as B fragments: the 16 bytes of (32-value chunk c, column n, quarter t)
-// at 16 * ((c * 8 NT + n) * 4 + t), so that the lanes of a warp read 512 consecutive bytes; and the
-// scale of every (group, token).
-template <int NT, bool SPLIT>
+// at 16 * ((c * 8 NT + n) * 4 + t), so that the lanes of a warp read 512 consecutive bytes; and their
+// scales: sc[group][token] for e4m3, else sc[token].
+template <int NT, int KIND>
 __device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *sc) {
-    constexpr int TOK = NT * (SPLIT ? 4 : 8);
-    const int KO = a.KC * 32, gl = a.group >> 3;
-    for (int i = threadIdx.x; i < TOK * KO; i += kQ4Threads) {  // KO is a multiple of 32: whole warps
-        const int tok = i / KO, o = i - tok * KO;
-        float v[8];
-        q4_load_x(a, tok, o, v);
-        float mult = 1.f, xs = 1.f;
-        if (a.xdt == RL_F8_E4M3) {
-            xs = tok < a.T && 8 * o < a.K ? a.xs[(size_t)tok * (a.K / a.group) + 8 * o / a.group] : 0.f;
-        } else {
+    constexpr int TOK = NT * (KIND == kQ4Split ? 4 : 8);
+    const int KO = a.KC * 32, lane = threadIdx.x & 31;
+    uint32_t *top = reinterpret_cast<uint32_t *>(sc + TOK);  // [TOK]
+    if (KIND != kQ4F8) {  // the largest magnitude of every row, as an integer (a NaN or infinity ranks highest)
+        if (threadIdx.x < TOK) top[threadIdx.x] = 0u;
+        __syncthreads();
+#pragma unroll 2
+        for (int i = threadIdx.x; i < a.T * KO; i += kQ4Threads) {  // KO is a multiple of 32: whole warps
+            const int tok = i / KO, o = i - tok * KO;
+            float v[8];
+            q4_load_x(a, tok, o, v);
             uint32_t mb = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[j]) & 0x7fffffffu);
-            for (int d = 1; d < gl; d <<= 1) mb = max(mb, __shfl_xor_sync(kFull, mb, d));
+            mb = __reduce_max_sync(kFull, mb);
+            if (lane == 0) atomicMax(top + tok, mb);
+        }
+        __syncthreads();
+        if (threadIdx.x < TOK) {
+            const uint32_t mb = top[threadIdx.x];
             // 2^14 over the power of two at or below the largest magnitude (at most 2^127)
-            const int e = (int)(mb >> 23);
-            mult = __uint_as_float((uint32_t)min(268 - e, 254) << 23);
-            xs = 1.0f / mult;
+            sc[threadIdx.x] = 1.0f / __uint_as_float((uint32_t)min(268 - (int)(mb >> 23), 254) << 23);
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < TOK * KO; i += kQ4Threads) {
+        const int tok = i / KO, o = i - tok * KO;
+        float v[8];
+        q4_load_x(a, tok, o, v);
+        uint8_t *at = bs + ((size_t)(o >> 2) * NT * 8 + (KIND == kQ4Split ? 2 * tok : tok)) * 64 + (o & 3) * 16;
+        if (KIND != kQ4F8) {
+            const float mult = 1.0f / sc[tok];  // a power of two: exact
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= mult;
+        } else if ((8 * o) % a.group == 0) {
+            sc[(8 * o / a.group) * TOK + tok] = tok < a.T && 8 * o < a.K ? a.xs[(size_t)tok * (a.K / a.group) + 8 * o / a.group] : 0.f;
         }
-        uint8_t *at = bs + ((size_t)(o >> 2) * NT * 8 + (SPLIT ? 2 * tok : tok)) * 64 + (o & 3) * 16;
-        if (SPLIT) {
+        if (KIND == kQ4Split) {
             float lo[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -159,7 +160,6 @@ __device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *
         } else {
             *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
         }
-        if ((o & (gl - 1)) == 0) sc[(o / gl) * TOK + tok] = xs;
     }
 }
 
@@ -238,9 +238,10 @@ __device__ __forceinline__ void q4_store(const Q4Args &a, int tok, int row, floa
     }
 }
 
-// NT: column tiles of 8; SPLIT: f32 activations in two columns; GL: 32-value chunks per group
-template <int NT, bool SPLIT, int GL>
+// NT: column tiles of 8; GL: 32-value chunks per group
+template <int NT, int KIND, int GL>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const Q4Layout lay) {
+    constexpr bool SPLIT = KIND == kQ4Split;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int TOK = NT * (SPLIT ? 4 : 8);
     constexpr int YV = SPLIT ? 2 : 4;  // outputs per lane and column tile
@@ -270,12 +271,12 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
         if (++pslot == a.stages) pslot = 0;
     };
     for (int s = 0; s < a.stages - 1; ++s) issue_next();
-    const uint32_t bs = smem_addr(smem) + lane * 16;
-    q4_stage_x<NT, SPLIT>(a, smem, sc);
+    q4_stage_x<NT, KIND>(a, smem, sc);
     __syncthreads();
+    const uint4 *bs = reinterpret_cast<const uint4 *>(smem) + lane;
     // ldmatrix: lane l addresses row (l & 7) + 8 (bit 3 of l) of 16-byte piece 2 jj + (l >> 4)
     const int lr = (lane & 7) + ((lane >> 3) & 1) * 8, lp = lane >> 4;
-    const uint32_t lrow = smem_addr(ring) + lr * 128;
+    const uint32_t lrow = smem_addr(ring) + lr * 128, x0 = (lp ^ (lr & 7)) << 4, x1 = x0 ^ 32, x2 = x0 ^ 64, x3 = x0 ^ 96;
     int slot = 0, parity = 0;
     for (int tile = first; tile < tiles; tile += step) {
         float y[NT][YV];
@@ -284,16 +285,18 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
 #pragma unroll
             for (int i = 0; i < YV; ++i) y[n][i] = 0.f;
         for (int st = sub; st < a.KC; st += a.W) {
-            cp_async_wait(a.stages - 2);
+            if (a.stages == 4) cp_async_wait_all_but<2>();
+            else cp_async_wait_all_but<0>();
             __syncwarp();  // every lane's copies of this stage; the stage before has been read
             issue_next();
             const uint32_t sb = lrow + slot * kQ4Stage;
+            const uint4 *bst = bs + st * (8 * NT * 32);
             const uint8_t *wsp = ring + slot * kQ4Stage + 2048 + g * 16;
             float acc[NT][4];
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 uint32_t r[4];
-                ldmatrix4(r, sb + (((2 * jj + lp) ^ (lr & 7)) << 4));
+                ldmatrix4(r, sb + (jj == 0 ? x0 : jj == 1 ? x1 : jj == 2 ? x2 : x3));
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = 2 * jj + h;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
                                    a6 = q4_pair<false>(v0), a7 = q4_pair<false>(v1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint4 b = lds128(bs + ((st * 8 + c) * NT + n) * 512);
+                        const uint4 b = bst[(c * NT + n) * 32];
                         mma_f16(acc[n], a0, a1, a2, a3, b.x, b.y);
                         mma_f16(acc[n], a4, a5, a6, a7, b.z, b.w);
                     }
@@ -320,16 +323,16 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
                         const float *p = sc + (st * (8 / GL) + gi) * TOK;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            if (SPLIT) {
-                                const float q = p[n * 4 + t];
-                                y[n][0] = fmaf(s0 * q, acc[n][0] + acc[n][1], y[n][0]);
-                                y[n][1] = fmaf(s1 * q, acc[n][2] + acc[n][3], y[n][1]);
+                            if (KIND == kQ4Split) {
+                                y[n][0] = fmaf(s0, acc[n][0] + acc[n][1], y[n][0]);
+                                y[n][1] = fmaf(s1, acc[n][2] + acc[n][3], y[n][1]);
                             } else {
-                                const float2 q = *reinterpret_cast<const float2 *>(p + n * 8 + 2 * t);
-                                y[n][0] = fmaf(s0 * q.x, acc[n][0], y[n][0]);
-                                y[n][1] = fmaf(s0 * q.y, acc[n][1], y[n][1]);
-                                y[n][YV - 2] = fmaf(s1 * q.x, acc[n][2], y[n][YV - 2]);
-                                y[n][YV - 1] = fmaf(s1 * q.y, acc[n][3], y[n][YV - 1]);
+                                float2 q = make_float2(1.f, 1.f);
+                                if (KIND == kQ4F8) q = *reinterpret_cast<const float2 *>(p + n * 8 + 2 * t);
+                                y[n][0] = fmaf(KIND == kQ4F8 ? s0 * q.x : s0, acc[n][0], y[n][0]);
+                                y[n][1] = fmaf(KIND == kQ4F8 ? s0 * q.y : s0, acc[n][1], y[n][1]);
+                                y[n][YV - 2] = fmaf(KIND == kQ4F8 ? s1 * q.x : s1, acc[n][2], y[n][YV - 2]);
+                                y[n][YV - 1] = fmaf(KIND == kQ4F8 ? s1 * q.y : s1, acc[n][3], y[n][YV - 1]);
                             }
                         }
                     }
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
         auto put = [&](int n, int i, int ln, float v) {
             const int row = tile * 16 + (ln >> 2) + (i >= YV / 2 ? 8 : 0);
             const int tok = SPLIT ? n * 4 + (ln & 3) : n * 8 + 2 * (ln & 3) + (i & 1);
-            q4_store(a, tok, row, v);
+            q4_store(a, tok, row, KIND == kQ4F8 ? v : v * sc[tok]);
         };
         if (a.W == 1) {
 #pragma unroll
@@ -376,28 +379,33 @@ struct Q4Plan {
 // NT column tiles: as few as hold the tokens of the launch.  W = 8 warps per tile (fewer for a short
 // K) keeps the tail of the tile loop short; four column tiles leave no room for the partial
 // sums, so they run one warp per tile, and only where the tiles fill every warp of the GPU.
-bool q4_plan(int N, int K, int cols, int group, bool split, Q4Plan &p) {
+bool q4_plan(int N, int K, int cols, int group, int kind, Q4Plan &p) {
     const int KC = (K + 255) / 256, tiles = (N + 15) / 16;
     const size_t room = 227 * 1024;
     p.NT = cols > 16 && tiles >= 152 * kQ4Warps ? 4 : cols > 8 ? 2 : 1;
     for (; p.NT >= 1; p.NT >>= 1) {
         p.W = 1;
         if (p.NT < 4)
-            while (p.W < 8 && 2 * p.W <= KC && tiles * p.W < 152 * kQ4Warps * kQ4Rounds) p.W *= 2;
+            while (p.W < 8 && 2 * p.W <= KC && tiles * p.W < 152 * kQ4Warps) p.W *= 2;
         for (; p.W >= 1; p.W >>= 1)
-            for (p.stages = kQ4MaxStages; p.stages >= 2; --p.stages)
-                if (Q4Layout(KC, p.NT, split, group, p.W, p.stages).total <= room) return true;
+            for (p.stages = 4; p.stages >= 2; p.stages -= 2)
+                if (Q4Layout(KC, p.NT, kind, group, p.W, p.stages).total <= room) return true;
     }
     return false;
 }
 
-template <int NT, bool SPLIT>
+template <int NT, int KIND>
 rl_status launch_q4(const Q4Args &a, const Q4Layout &lay, cudaStream_t s) {
     const int tiles = (a.N + 15) / 16, sms = sm_count();
     const dim3 grid(tiles < sms ? tiles : sms), block(kQ4Threads);
-    if (a.group == 32) return launch_pdl(q4_kernel<NT, SPLIT, 1>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
-    if (a.group == 64) return launch_pdl(q4_kernel<NT, SPLIT, 2>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
-    return launch_pdl(q4_kernel<NT, SPLIT, 4>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+    if (a.group == 32) return launch_pdl(q4_kernel<NT, KIND, 1>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+    if (a.group == 64) return launch_pdl(q4_kernel<NT, KIND, 2>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+    return launch_pdl(q4_kernel<NT, KIND, 4>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
+}
+
+template <int KIND>
+rl_status launch_q4_kind(const Q4Args &a, const Q4Layout &lay, int NT, cudaStream_t s) {
+    return NT == 4 ? launch_q4<4, KIND>(a, lay, s) : NT == 2 ? launch_q4<2, KIND>(a, lay, s) : launch_q4<1, KIND>(a, lay, s);
 }
 
 }  // namespace
@@ -423,12 +431,12 @@ extern "C" rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t
         return fail(RL_ERR_INVALID, "rl_q4_matvec: w, w_scale and x must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(x_scale) & 3 || reinterpret_cast<uintptr_t>(y) % dtype_bytes(y_dtype))
         return fail(RL_ERR_INVALID, "rl_q4_matvec: x_scale or y misaligned");
-    const bool split = x_dtype == RL_F32;
-    const int per = split ? 2 : 1;  // columns per token
+    const int kind = x_dtype == RL_F32 ? kQ4Split : x_dtype == RL_F8_E4M3 ? kQ4F8 : kQ4Half;
+    const int per = kind == kQ4Split ? 2 : 1;  // columns per token
     cudaStream_t s = as_stream(stream);
     for (int t0 = 0; t0 < T;) {
         Q4Plan p;
-        if (!q4_plan(N, K, (T - t0) * per < 32 ? (T - t0) * per : 32, group, split, p))
+        if (!q4_plan(N, K, (T - t0) * per < 32 ? (T - t0) * per : 32, group, kind, p))
             return fail(RL_ERR_UNSUPPORTED, "rl_q4_matvec: K=%d does not fit", K);
         const int most = 8 * p.NT / per;
         Q4Args a = {};
@@ -448,10 +456,10 @@ extern "C" rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t
         a.W = p.W;
         a.stages = p.stages;
         a.wide = K % 256 == 0;
-        const Q4Layout lay(a.KC, p.NT, split, group, p.W, p.stages);
-        const rl_status st = p.NT == 4   ? (split ? launch_q4<4, true>(a, lay, s) : launch_q4<4, false>(a, lay, s))
-                             : p.NT == 2 ? (split ? launch_q4<2, true>(a, lay, s) : launch_q4<2, false>(a, lay, s))
-                                         : (split ? launch_q4<1, true>(a, lay, s) : launch_q4<1, false>(a, lay, s));
+        const Q4Layout lay(a.KC, p.NT, kind, group, p.W, p.stages);
+        const rl_status st = kind == kQ4Split ? launch_q4_kind<kQ4Split>(a, lay, p.NT, s)
+                             : kind == kQ4F8  ? launch_q4_kind<kQ4F8>(a, lay, p.NT, s)
+                                              : launch_q4_kind<kQ4Half>(a, lay, p.NT, s);
         if (st != RL_OK) return st;
         t0 += a.T;
     }

@@ -242,7 +242,8 @@ def check_lp(o, x, targets, n):
 
 
 @pytest.mark.parametrize("T,V,n", [(1, 1, 1), (1, 131072, 20), (2, 4097, 32), (3, 33, 5), (1, 100003, 1), (5, 50001, 7),
-                                   (40, 12289, 20), (700, 1000, 3), (16, 100003, 0), (4100, 77, 2)])
+                                   (40, 12289, 20), (700, 1000, 3), (16, 100003, 0), (4100, 77, 2),
+                                   (9, 300001, 32), (500, 20011, 20), (3, 1000003, 17)])
 @pytest.mark.parametrize("dt", list(TYPES))
 def test_logprobs(L, T, V, n, dt):
     x = (3 * randn(T, V, seed=V)).to(TYPES[dt])
