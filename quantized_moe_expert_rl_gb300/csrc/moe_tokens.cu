@@ -10,15 +10,19 @@
 //   S  every CTA selects for itself (one warp per token, the same code on the same logits): the
 //      list of distinct experts, each with its tokens as a bit mask, and from it the whole
 //      schedule of weight copies.  CTA 0 writes ids, weights, slots, misses and the flag
-//   G  gate and up: tiles of (expert, 16 hidden rows) -> h;  grid barrier
-//   D  down: tiles of (expert, 16 to 256 output rows) -> o of every (expert, token) pair;  grid
-//      barrier (the copies of D's first weights are under way before the one in front of it)
-//   C  y = sum over k in selection order.
+//   G  gate and up: tiles of (expert, 16 hidden rows) -> h;  grid barrier (the copies of D's first
+//      weights are already under way)
+//   D  down: CTA b has output rows 16 b .. 16 b + 15 of every expert, so that the sum over k in
+//      selection order needs no further exchange.  (Tiles of 128 rows spread over all SMs, with the
+//      outputs exchanged through a third grid barrier, were no faster at 32 tokens and 3 us slower at 1.)
 // G and D run the same code on rounds of 16 units, one per computing warp: 16 weight rows x 256
-// values (one block of every row).  A round's block sums go through one of four buffers to a finishing
-// warp, which adds them and applies SwiGLU (G) or stores them (D), so that no computing warp waits
-// for another.  Every CTA takes a run of consecutive tiles of equal weight, where a tile weighs one
-// per two tokens of its expert; an expert's activations then stay in registers over its tiles.
+// values (one block of every row).  In G a round's block sums go through one of four buffers to a
+// finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
+// CTA takes a run of consecutive G tiles of equal weight, where a tile weighs one per two tokens of its
+// expert; an expert's activations then stay in registers over its tiles.
+// For one token the launch is a chain of latencies, much of it the first fetch of each phase's code.
+// So the codebook table is built, and the unit loop run once on whatever the ring holds (with
+// its waits and stores turned off), while the first grid barrier is pending.
 //
 // The matrix arithmetic.  A weight is d * (codebook value) * (sign): the codebook value is an
 // 8-bit integer, exact in bf16, so a group's 8 values are one 16-byte table entry whose signs are
@@ -43,9 +47,7 @@ constexpr int kMtRed = 4;                           // buffers between computing
 constexpr int kMtMaxT = 32;
 constexpr int kMtStage = 16896;    // one round of weights: 16 units of 16 rows x 256 values
 constexpr int kMtMaxStages = 8;
-constexpr int kMtMinStages = 4;    // the selection's keys (2 KB per token) share the ring's memory
 constexpr int kMtHdr = 256;        // workspace: barrier counter, test knobs (64..71), RMS scales (128..255)
-static_assert(kMtMinStages * kMtStage >= kMtMaxT * 2048, "the keys must fit the ring");
 
 struct MtArgs {
     const float *x, *W, *bias;
@@ -58,9 +60,8 @@ struct MtArgs {
     int32_t *ctrl;
     float *logits_out, *y;
     unsigned long long *ctr;
-    float *rs, *raw;       // [32] RMS scales, [T][E] router dots
+    float *rs, *raw;       // [32] RMS scales, [T][512] router dots
     uint16_t *xs, *hs;     // [T][3][H], [T K][3][I] bf16 parts
-    float *o;              // [T K][H] expert outputs
     float eps;
     int layer, T, H, E, K, I, accumulate, stages;
 };
@@ -75,8 +76,14 @@ constexpr int kMtOId = kMtOSlot + 512 * 8;           // [512] i32 selected ids
 constexpr int kMtOW = kMtOId + 512 * 4;              // [512] f32 selected logits, then weights
 constexpr int kMtOPair = kMtOW + 512 * 4;            // [512] u16 pair number of (t, k)
 constexpr int kMtOTok = kMtOPair + 512 * 2;          // [512] u8 token of a pair
-constexpr int kMtOSel = kMtOTok + 512;               // [16 warps][448] selection scratch
-constexpr int kMtORing = (kMtOSel + kMtWarps * 448 + 127) / 128 * 128;
+// partial outputs [pairs][units per row][16] f32; before that the selection's scratch [16 warps][448] and
+// keys [T][512], which reach into the ring behind it
+constexpr int kMtOPart = kMtOTok + 512;
+constexpr int kMtSelB = kMtWarps * 448;
+__host__ __device__ inline int mt_ring(int T, int K, int I) {
+    const int part = T * K * (I > 256 ? I / 256 : 1) * 64;
+    return (int)align_up(kMtOPart + (part > kMtSelB ? part : kMtSelB), 128);
+}
 
 static_assert(kMtWork == 608, "the barriers below count 608 threads");
 // all warps but the copying one
@@ -99,31 +106,40 @@ __device__ __forceinline__ bool workers_sync_or(bool pred) {
     return any != 0u;
 }
 
-// The working warps of all CTAs meet (see grid_sync in stack_kernel.cuh; the copying warp does not
-// take part).
-__device__ __noinline__ bool workers_grid_sync(unsigned long long *ctr, unsigned long long &target, int *ok_s,
-                                               int32_t *ctrl, uint32_t cap) {
+// The working warps of all CTAs meet (see grid_sync in stack_kernel.cuh; the copying warp does not take
+// part), in two halves: what the CTA wrote before its arrival is visible to every CTA after the wait.
+__device__ __forceinline__ void grid_arrive(unsigned long long *ctr, unsigned long long &target) {
     workers_sync();
     if (threadIdx.x == 0) {
         unsigned long long old;
         asm volatile("atom.add.release.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(ctr) : "memory");
         if (target == 0ull) target = old - old % gridDim.x;
         target += gridDim.x;
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ bool grid_wait(unsigned long long *ctr, unsigned long long target, volatile int *stop,
+                                          int32_t *ctrl, uint32_t cap) {
+    if (threadIdx.x == 0) {
         bool ok = false;
+#pragma unroll 1
         for (uint32_t i = 0; i < cap; ++i)
             if (ld_acquire_u64(ctr) >= target) {
                 ok = true;
                 break;
             }
-        if (!ok) dev_error(ctrl, RL_DEVERR_WAIT_TIMEOUT);
-        *ok_s = ok;
+        if (!ok) {
+            dev_error(ctrl, RL_DEVERR_WAIT_TIMEOUT);
+            *stop = 1;
+        }
     }
     workers_sync();
-    return *ok_s != 0;
+    return *stop == 0;
 }
 
 // Bounded wait of a whole warp for phase `parity` of an mbarrier, given up once *stop is set.
 __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, const volatile int *stop) {
+    if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
     int ok = 0;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll 1
@@ -201,11 +217,11 @@ __device__ __forceinline__ void unit_dot(const uint8_t *p0, const uint8_t *p1, i
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t gw = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
-            const uint32_t gv = (j & 1) ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu;
-            uint4 q = tabc[(gw & 0xffu) * kTabCopies], r = tabc[(gv & 0xffu) * kTabCopies];
-            flip_signs(q, gw >> 8);
-            flip_signs(r, gv >> 8);
+            const uint32_t x = w[j >> 1], y = v[j >> 1];
+            uint4 q = tabc[((j & 1) ? __byte_perm(x, 0, 0x4442) : x & 0xffu) * kTabCopies];
+            uint4 r = tabc[((j & 1) ? __byte_perm(y, 0, 0x4442) : y & 0xffu) * kTabCopies];
+            flip_signs(q, (j & 1) ? x >> 24 : __byte_perm(x, 0, 0x4441));
+            flip_signs(r, (j & 1) ? y >> 24 : __byte_perm(y, 0, 0x4441));
             mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
             mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
         }
@@ -330,14 +346,15 @@ __device__ __noinline__ void warp_topk_smem(const uint32_t *key, int E, int K, u
 // First tile of CTA b's run: tiles are numbered expert by expert, 2^lg each; expert i's tiles weigh
 // (tokens + 1) / 2 each and list[i].w is the weight of the experts before it, per tile.
 __device__ __forceinline__ int run_start(const int4 *list, int n, int total, int lg, int b, int G) {
-    const long long pos = (((long long)total << lg) * b) / G;
+    const int pos = (int)((uint32_t)((total << lg) * b) / (uint32_t)G);  // at most 512 << 7, times 152
     int at = 0, left = n;
+#pragma unroll 1
     while (left > 1) {
         const int h = left >> 1;
-        if (((long long)list[at + h].w << lg) <= pos) at += h, left -= h;
+        if (list[at + h].w << lg <= pos) at += h, left -= h;
         else left = h;
     }
-    const int c = (__popc((uint32_t)list[at].z) + 1) >> 1, in = (int)(pos - ((long long)list[at].w << lg));
+    const int c = (__popc((uint32_t)list[at].z) + 1) >> 1, in = pos - (list[at].w << lg);
     return (at << lg) + (in + c - 1) / c;
 }
 
@@ -346,16 +363,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + kMtMaxStages;
     uint64_t *redfull = empty + kMtMaxStages, *redempty = redfull + kMtRed;
-    int *ok_s = reinterpret_cast<int *>(smem + 192);
-    volatile int *stop_s = reinterpret_cast<volatile int *>(smem + 196);
-    int *bad_s = reinterpret_cast<int *>(smem + 200);    // bit 0: a slot is absent, 1: misaligned, 2: bad id, 3: NaN
-    uint32_t *cap_s = reinterpret_cast<uint32_t *>(smem + 204);
-    int *skip_s = reinterpret_cast<int *>(smem + 208);
-    int *nd_s = reinterpret_cast<int *>(smem + 212);
-    int *hold_s = reinterpret_cast<int *>(smem + 216);
-    int *run_s = reinterpret_cast<int *>(smem + 224);      // [4] this CTA's runs: G first, last + 1, D first, last + 1
-    float *rs_s = reinterpret_cast<float *>(smem + 240);   // [32] RMS scales (to 368)
-    int *scan_s = reinterpret_cast<int *>(smem + 368);     // [8]; the rest of the scan shares the reduction buffer
+    volatile int *stop_s = reinterpret_cast<volatile int *>(smem + 192);
+    int *bad_s = reinterpret_cast<int *>(smem + 196);    // bit 0: a slot is absent, 1: misaligned, 2: bad id, 3: NaN
+    int *nd_s = reinterpret_cast<int *>(smem + 200);
+    int *weight_s = reinterpret_cast<int *>(smem + 204);   // weight of all experts' tiles, per tile
+    int *run_s = reinterpret_cast<int *>(smem + 208);      // [2] this CTA's run of G tiles: first, last + 1
+    float *rs_s = reinterpret_cast<float *>(smem + 224);   // [32] RMS scales (to 352)
     uint4 *tab = reinterpret_cast<uint4 *>(smem + 512);
     float *red = reinterpret_cast<float *>(smem + kMtORed);
     int4 *list = reinterpret_cast<int4 *>(smem + kMtOList);
@@ -365,49 +378,28 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
     float *w_s = reinterpret_cast<float *>(smem + kMtOW);
     uint16_t *pair_s = reinterpret_cast<uint16_t *>(smem + kMtOPair);
     uint8_t *ptok_s = smem + kMtOTok;
-    uint8_t *ring = smem + kMtORing;
+    float *part = reinterpret_cast<float *>(smem + kMtOPart);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = gridDim.x, cta = blockIdx.x;
     const int T = a.T, H = a.H, E = a.E, K = a.K, I = a.I, lgH = 31 - __clz(H);
+    uint8_t *ring = smem + mt_ring(T, K, I);
     const bool routed = a.W != nullptr;  // else ids, weights and slots are given
+    const int flag = ld_ctrl(a.ctrl);    // the same for every thread: this launch raises it to `layer` at most
+    if (routed ? flag < a.layer : flag <= a.layer) return;
+    const uint2 knob = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint32_t *>(a.ctr) + 16);  // test knobs
+    const uint32_t cap = knob.x ? knob.x : kSpinCap;
 
-    if (tid == 0) {
-#pragma unroll 1
-        for (int s = 0; s < a.stages; ++s) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, kMtWarps);
-        }
-#pragma unroll 1
-        for (int s = 0; s < kMtRed; ++s) {
-            mbar_init(redfull + s, kMtWarps);
-            mbar_init(redempty + s, 1);
-        }
-        fence_mbar_init();
-        *stop_s = 0;
-        *bad_s = 0;
-        const uint32_t *knob = reinterpret_cast<const uint32_t *>(a.ctr) + 16;
-        *cap_s = knob[0] ? knob[0] : kSpinCap;
-        *hold_s = (int)knob[1];
-        const int flag = ld_ctrl(a.ctrl);
-        *skip_s = routed ? flag < a.layer : flag <= a.layer;
-    }
     // R: the router rows of this CTA (row r: expert cta + r G); warp w holds columns [w H/16, (w + 1) H/16)
     const int rcol = warp * (H >> 4) + 4 * lane;
     const bool rmine = routed && warp < kMtWarps && 4 * lane < (H >> 4);
-    float4 wv[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        wv[r] = rmine && cta + r * G < E ? __ldg(reinterpret_cast<const float4 *>(a.W + (size_t)(cta + r * G) * H + rcol))
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < 512) {
-        mask_s[tid] = 0u;
-        if (routed && tid < E) slot_s[tid] = a.table[tid];
-    }
-    build_pair_table(tab, a.codebook, nullptr);  // ends with a CTA barrier
-    if (*skip_s) return;
     unsigned long long target = 0ull;
     bool ok = true;
     if (tid < kMtWork) {
         if (routed && warp < kMtWarps) {
+            float4 wv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                wv[r] = rmine && cta + r * G < E ? __ldg(reinterpret_cast<const float4 *>(a.W + (size_t)(cta + r * G) * H + rcol))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             float4 xv[4];
             auto load_x = [&](int t0) {
 #pragma unroll
@@ -468,6 +460,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
             }
             __syncwarp();
         }
+        if (tid == 0) {
+            *stop_s = 0;
+            *bad_s = 0;
+        }
         workers_sync();
         if (routed && tid < 4 * T) {
             const int t = tid >> 2, r = tid & 3, e = cta + r * G;
@@ -475,150 +471,57 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < kMtWarps; ++w) v += red[(w * 32 + t) * 4 + r];
-                __stcg(a.raw + (size_t)t * E + e, v);
+                __stcg(a.raw + t * 512 + e, v);
             }
         }
-        ok = *hold_s - 1 != cta;  // test knob: this CTA leaves before its arrival
-        if (ok) ok = workers_grid_sync(a.ctr, target, ok_s, a.ctrl, *cap_s);
-        if (!ok && tid == 0) *stop_s = 1;
-        // S: selection.  Keys of every (token, expert) into shared memory, then one warp per token.
-        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
-        if (ok) {
-            if (tid < T) rs_s[tid] = __ldcg(a.rs + tid);
-            if (routed) {
-#pragma unroll 2
-                for (int i = tid; i < 512 * T; i += kMtWork) {
-                    const int t = i >> 9, e = i & 511;
-                    uint32_t k = 0u;
-                    if (e < E) {
-                        const float v = __ldcg(a.rs + t) * __ldcg(a.raw + (size_t)t * E + e) + (a.bias ? a.bias[e] : 0.f);
-                        if (v != v) atomicOr(bad_s, 8);
-                        k = order_key(v);
-                        if (a.logits_out && cta == 0) a.logits_out[(size_t)t * E + e] = v;
-                    }
-                    keys[i] = k;
-                }
-            }
+        if ((int)knob.y - 1 == cta) {  // test knob: this CTA leaves before its arrival
+            if (tid == 0) *stop_s = 1;
+            cta_sync();
+            return;
         }
-        workers_sync();
-        if (ok && warp < kMtWarps) {
+        grid_arrive(a.ctr, target);
+        // while the others arrive: the barriers, the expert tables, the codebook table
+        if (tid == 32) {
 #pragma unroll 1
-            for (int t = warp; t < T; t += kMtWarps) {
-                int my_id = 0;
-                float my_val = 0.f;
-                uint64_t slot = 1;
-                if (routed) {
-                    warp_topk_smem(keys + 512 * t, E, K, smem + kMtOSel + warp * 448, my_id, my_val);
-                    if (lane < K) slot = slot_s[my_id];
-                } else if (lane < K) {
-                    my_id = a.ids[t * K + lane];
-                    my_val = a.weights[t * K + lane];
-                    slot = a.slots[t * K + lane];
-                    if (my_id < 0 || my_id >= E) {
-                        atomicOr(bad_s, 4);
-                        my_id = 0;
-                    }
-                    slot_s[my_id] = slot;
-                }
-                __syncwarp();
-                if (lane < K) {
-                    id_s[t * K + lane] = my_id;
-                    w_s[t * K + lane] = my_val;
-                    atomicOr(mask_s + my_id, 1u << t);
-                    if (slot == 0) atomicOr(bad_s, 1);
-                    if (slot & 15) atomicOr(bad_s, 2);
-                }
-                __syncwarp();
+            for (int s = 0; s < a.stages; ++s) {
+                mbar_init(full + s, 1);
+                mbar_init(empty + s, kMtWarps);
             }
-        }
-        fence_proxy_async_smem();  // the ring's copies come after the keys
-    }
-    cta_sync();
-    if (*stop_s) return;
-    const int bad = *bad_s;
-    if (routed && cta == 0 && warp < kMtWarps) {  // the outputs of the selection
 #pragma unroll 1
-        for (int t = warp; t < T; t += kMtWarps) {
-            const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
-            uint64_t slot = 1;
-            if (lane < K) {
-                const int e = id_s[t * K + lane];
-                slot = slot_s[e];
-                a.ids[t * K + lane] = e;
-                a.weights[t * K + lane] = w;
-                a.slots[t * K + lane] = slot;
+            for (int s = 0; s < kMtRed; ++s) {
+                mbar_init(redfull + s, kMtWarps);
+                mbar_init(redempty + s, 1);
             }
-            const int nmiss = __popc(__ballot_sync(kFull, lane < K && slot == 0));
-            if (lane == 0 && nmiss > 0) {
-                atomicAdd(a.miss, (uint32_t)nmiss);
-                atomicMin(a.ctrl, a.layer);
-            }
-            __syncwarp();
+            fence_mbar_init();
         }
-    }
-    if (bad) {
-        if (tid == 0 && cta == 0) {
-            const int bits = ((bad & 1) && !routed ? RL_DEVERR_MISSING : 0) | (bad & 2 ? RL_DEVERR_SLOT_ALIGN : 0) |
-                             (bad & 4 ? RL_DEVERR_BAD_ID : 0) | (bad & 8 ? RL_DEVERR_NAN : 0);
-            if (bits) dev_error(a.ctrl, bits);
-        }
-        if (bad & 7) return;
-    }
-    // The list of distinct experts in index order: thread e holds expert e; its pairs (expert, token)
-    // are numbered in token order from `off`, and `before` is the weight of the experts before it.
-    if (tid < kMtWork) {
-        int *scan = reinterpret_cast<int *>(red);  // [16 warps][4]
-        const uint32_t m = tid < 512 ? mask_s[tid] : 0u;
-        const int cnt = __popc(m);
-        uint32_t incl = (uint32_t)cnt | (uint32_t)((cnt + 1) >> 1) << 16;  // pairs | weight
+        if (tid >= 64 && tid < 320) {
+            const int e = tid - 64;
+            const uint2 q = reinterpret_cast<const uint2 *>(a.codebook)[e];
+            uint32_t w[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const unsigned has = __ballot_sync(kFull, m != 0u);
-        if (lane == 31 && warp < kMtWarps) {
-            scan[2 * warp] = __popc(has);
-            scan[2 * warp + 1] = (int)incl;
-        }
-        __syncwarp();
-        workers_sync();
-        int at = 0;
-        uint32_t base = 0u;
-#pragma unroll 4
-        for (int w = 0; w < kMtWarps; ++w) {
-            if (w < warp) {
-                at += scan[2 * w];
-                base += (uint32_t)scan[2 * w + 1];
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t two = (p < 2 ? q.x : q.y) >> (16 * (p & 1));
+                w[p] = bf16_bits((int8_t)(two & 0xffu)) | (bf16_bits((int8_t)((two >> 8) & 0xffu)) << 16);
+            }
+#pragma unroll
+            for (int c = 0; c < kTabCopies; ++c)  // rotated so one store instruction hits 8 bank quads
+                tab[e * kTabCopies + ((c + tid) & (kTabCopies - 1))] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (tid >= 352) {
+            for (int e = tid - 352; e < 512; e += 256) {
+                mask_s[e] = 0u;
+                if (routed && e < E) slot_s[e] = a.table[e];
             }
         }
-        if (tid == kMtWarps * 32 - 1) {  // the last expert's thread knows the totals
-            *nd_s = at + __popc(has);
-            scan_s[0] = (int)((base + incl) >> 16);
-        }
-        if (m) {
-            at += __popc(has & ((1u << lane) - 1u));
-            const uint32_t ex = base + incl - ((uint32_t)cnt | (uint32_t)((cnt + 1) >> 1) << 16);
-            list[at] = make_int4(tid, (int)(ex & 0xffffu), (int)m, (int)(ex >> 16));
-            uint32_t left = m;
-#pragma unroll 1
-            for (int i = (int)(ex & 0xffffu); left; ++i, left &= left - 1u) ptok_s[i] = (uint8_t)(__ffs(left) - 1);
-        }
         __syncwarp();
-        workers_sync();
-        const int lgG = 31 - __clz(I >> 4);                      // gate/up tiles of 16 rows per expert
-        const int lgD = 31 - __clz((H >> 4) * (I > 256 ? I >> 8 : 1) >> 4);  // down tiles of 16 units
-        if (tid < 4) run_s[tid] = run_start(list, *nd_s, scan_s[0], tid < 2 ? lgG : lgD, cta + (tid & 1), G);
-    }
-    cta_sync();
-    // Tiles.  G: 16 rows of gate and up, 2 nb units; tpr of them per round.  D: 16 units, upe per row.
-    const int nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb, lgnb = 31 - __clz(nb);
-    const int lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, lgu = 31 - __clz(upe), lgD = 31 - __clz((H * upe) >> 8);
-    const int dbytes = I >= 256 ? kMtStage : kMtStage / 2;  // bytes of a down tile
-    const int g0 = run_s[0], g1 = run_s[1], d0 = run_s[2], d1 = run_s[3];
-    const int gr = (g1 - g0 + tpr - 1) / tpr, dr = d1 - d0;
-
-    if (tid >= kMtWork) {  // the copying warp
+    } else {
+        // the copying warp
+        cta_sync();
+        if (*stop_s || (*bad_s & 7)) return;
+        cta_sync();
+        const int nD = *nd_s, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb;
+        const int lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, epr = kMtWarps / upe, dnb = I * kBlockBytes / 16;
+        const int g0 = run_s[0], g1 = run_s[1];
+        const int gr = (g1 - g0 + tpr - 1) / tpr, dr = cta < H / 16 ? (nD + epr - 1) / epr : 0;
         const size_t mat = (size_t)I * rowb;
         int slot = 0, turn = 0, issued = 0;
 #pragma unroll 1
@@ -638,11 +541,14 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                     bulk_g2s(dst + (lane >> 1) * tileb + (lane & 1) * 16 * rowb,
                              rec + (lane & 1) * mat + (size_t)(tile & ((1 << lgG) - 1)) * 16 * rowb, 16 * rowb, full + slot);
                 }
-            } else if (lane == 0) {
-                const int tile = d0 + r - gr;
-                const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[tile >> lgD].x]);
-                mbar_arrive_expect_tx(full + slot, dbytes);
-                bulk_g2s(dst, rec + 2 * mat + (size_t)(tile & ((1 << lgD) - 1)) * dbytes, dbytes, full + slot);
+            } else {
+                const int e0 = (r - gr) * epr, n = min(epr, nD - e0);
+                if (lane == 0) mbar_arrive_expect_tx(full + slot, n * dnb);
+                __syncwarp();
+                if (lane < n) {
+                    const uint8_t *rec = reinterpret_cast<const uint8_t *>(slot_s[list[e0 + lane].x]);
+                    bulk_g2s(dst + lane * dnb, rec + 2 * mat + (size_t)cta * dnb, dnb, full + slot);
+                }
             }
             __syncwarp();
             ++issued;
@@ -654,42 +560,221 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         return;
     }
 
-    const int g = lane >> 2, t4 = lane & 3;
+    const int g = lane >> 2, t4 = lane & 3, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb;
+    const int lgnb = 31 - __clz(nb), lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, lgu = 31 - __clz(upe);
+    const int epr = kMtWarps >> lgu, dnb = I * kBlockBytes / 16;
     const uint4 *tabc = tab + (lane & (kTabCopies - 1));
-    // D's units take every `stride`-th row of a tile, so that the rows of a unit lie 132 words apart and
-    // their lanes meet different banks
-    const int lgs = I >= 512 ? 11 - (31 - __clz(I)) : 0;
-    int slot = 0, turn = 0, s = 0;
+    int slot = 0, turn = 0, s = 0, g0 = 0, g1 = 1, nD = 1;
     uint4 b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int ph = 0; ph < 2; ++ph) {
-        const bool down = ph == 1;
-        const int r0 = down ? d0 : g0, r1 = down ? d1 : g1, per = down ? 1 : tpr, lgt = down ? lgD : lgG;
-        const int rounds = down ? dr : gr;
-        // a round's passes (two tokens each): as many as its most shared expert needs
+    for (int ph = -1; ph < 2; ++ph) {  // -1: the dry run, 0: S and G, 1: D
+        const bool dry = ph < 0, down = ph == 1;
+        if (ph == 0) {
+            ok = grid_wait(a.ctr, target, stop_s, a.ctrl, cap);
+            // S: selection.  Keys of every (token, expert) into shared memory, then one warp per token.
+            uint32_t *keys = reinterpret_cast<uint32_t *>(smem + kMtOPart + kMtSelB);
+            if (ok) {
+                if (tid < T) rs_s[tid] = __ldcg(a.rs + tid);
+                if (routed) {
+#pragma unroll 4
+                    for (int i = tid; i < 128 * T; i += kMtWork) {
+                        const int t = i >> 7, e = (i & 127) * 4;
+                        const float rs = __ldcg(a.rs + t);
+                        const float4 r = __ldcg(reinterpret_cast<const float4 *>(a.raw + t * 512 + e));
+                        float v[4] = {rs * r.x, rs * r.y, rs * r.z, rs * r.w};
+                        uint32_t k[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            k[c] = 0u;
+                            if (e + c < E) {
+                                if (a.bias) v[c] += a.bias[e + c];
+                                if (v[c] != v[c]) atomicOr(bad_s, 8);
+                                k[c] = order_key(v[c]);
+                                if (a.logits_out && cta == 0) a.logits_out[(size_t)t * E + e + c] = v[c];
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(keys + t * 512 + e) = make_uint4(k[0], k[1], k[2], k[3]);
+                    }
+                }
+            }
+            workers_sync();
+            if (ok && warp < kMtWarps) {
+#pragma unroll 1
+                for (int t = warp; t < T; t += kMtWarps) {
+                    int my_id = 0;
+                    float my_val = 0.f;
+                    uint64_t at = 1;
+                    if (routed) {
+                        warp_topk_smem(keys + 512 * t, E, K, smem + kMtOPart + warp * 448, my_id, my_val);
+                        if (lane < K) at = slot_s[my_id];
+                    } else if (lane < K) {
+                        my_id = a.ids[t * K + lane];
+                        my_val = a.weights[t * K + lane];
+                        at = a.slots[t * K + lane];
+                        if (my_id < 0 || my_id >= E) {
+                            atomicOr(bad_s, 4);
+                            my_id = 0;
+                        }
+                        slot_s[my_id] = at;
+                    }
+                    __syncwarp();
+                    if (lane < K) {
+                        id_s[t * K + lane] = my_id;
+                        w_s[t * K + lane] = my_val;
+                        atomicOr(mask_s + my_id, 1u << t);
+                        if (at == 0) atomicOr(bad_s, 1);
+                        if (at & 15) atomicOr(bad_s, 2);
+                    }
+                    __syncwarp();
+                }
+            }
+            fence_proxy_async_smem();  // the ring's copies come after the keys
+            cta_sync();
+            if (*stop_s) return;
+            const int bad = *bad_s;
+            if (!(bad & 7)) {
+                // The list of distinct experts in index order: thread e holds expert e; its pairs (expert,
+                // token) are numbered in token order, and `w` is the weight of the experts before it.
+                int *scan = reinterpret_cast<int *>(red);  // [16 warps][2]
+                const uint32_t m = tid < 512 ? mask_s[tid] : 0u;
+                const uint32_t own = (uint32_t)__popc(m) | (uint32_t)((__popc(m) + 1) >> 1) << 16;  // pairs | weight
+                uint32_t incl = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t v = __shfl_up_sync(kFull, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                const unsigned has = __ballot_sync(kFull, m != 0u);
+                if (lane == 31 && warp < kMtWarps) {
+                    scan[2 * warp] = __popc(has);
+                    scan[2 * warp + 1] = (int)incl;
+                }
+                __syncwarp();
+                workers_sync();
+                int at = 0;
+                uint32_t before = 0u;
+#pragma unroll 4
+                for (int w = 0; w < kMtWarps; ++w)
+                    if (w < warp) {
+                        at += scan[2 * w];
+                        before += (uint32_t)scan[2 * w + 1];
+                    }
+                if (tid == kMtWarps * 32 - 1) {  // the last expert's thread knows the totals
+                    *nd_s = at + __popc(has);
+                    *weight_s = (int)((before + incl) >> 16);
+                }
+                if (m) {
+                    at += __popc(has & ((1u << lane) - 1u));
+                    before += incl - own;
+                    list[at] = make_int4(tid, (int)(before & 0xffffu), (int)m, (int)(before >> 16));
+                    uint32_t left = m;
+#pragma unroll 1
+                    for (int i = (int)(before & 0xffffu); left; ++i, left &= left - 1u) ptok_s[i] = (uint8_t)(__ffs(left) - 1);
+                }
+                __syncwarp();
+                workers_sync();
+                if (tid < 2) run_s[tid] = run_start(list, *nd_s, *weight_s, lgG, cta + tid, G);
+                __syncwarp();
+                cta_sync();
+                nD = *nd_s;
+                g0 = run_s[0];
+                g1 = run_s[1];
+            }
+            // the outputs of the selection, by the finishing warps of CTA 0
+            if (routed && cta == 0 && warp >= kMtWarps) {
+#pragma unroll 1
+                for (int t = warp - kMtWarps; t < T; t += kMtFin) {
+                    const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
+                    uint64_t at = 1;
+                    if (lane < K) {
+                        const int e = id_s[t * K + lane];
+                        at = slot_s[e];
+                        a.ids[t * K + lane] = e;
+                        a.weights[t * K + lane] = w;
+                        a.slots[t * K + lane] = at;
+                    }
+                    const int nmiss = __popc(__ballot_sync(kFull, lane < K && at == 0));
+                    if (lane == 0 && nmiss > 0) {
+                        atomicAdd(a.miss, (uint32_t)nmiss);
+                        atomicMin(a.ctrl, a.layer);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (bad && tid == 0 && cta == 0) {
+                const int bits = ((bad & 1) && !routed ? RL_DEVERR_MISSING : 0) | (bad & 2 ? RL_DEVERR_SLOT_ALIGN : 0) |
+                                 (bad & 4 ? RL_DEVERR_BAD_ID : 0) | (bad & 8 ? RL_DEVERR_NAN : 0);
+                if (bits) dev_error(a.ctrl, bits);
+            }
+            if (bad & 7) return;
+        }
+        const int gr = (g1 - g0 + tpr - 1) / tpr, dr = cta < H / 16 ? (nD + epr - 1) >> (4 - lgu) : 0;
+        const int rounds = down ? dr : dry && warp == 0 ? 0 : gr;  // (warp 0 waits for the grid)
+        // passes (two tokens each) of a G round: as many as its most shared expert needs
         auto passes_of = [&](int r) {
             int n = 1;
 #pragma unroll 1
-            for (int i = 0; i < per; ++i) {
-                const int tile = r0 + r * per + i;
-                if (tile < r1) n = max(n, (__popc((uint32_t)list[tile >> lgt].z) + 1) >> 1);
+            for (int i = 0; i < tpr; ++i) {
+                const int tile = g0 + r * tpr + i;
+                if (tile < g1) n = max(n, (__popc((uint32_t)list[tile >> lgG].z) + 1) >> 1);
             }
             return n;
         };
         if (warp >= kMtWarps) {
-            if (!down && routed) {  // renormalised weights, for the combine
+            // finishing warps: h of every third pass of G
 #pragma unroll 1
-                for (int t = warp - kMtWarps; t < T; t += kMtFin) {
+            for (int r = 0; r < (down ? 0 : rounds) && ok; ++r) {
+                const int passes = dry ? 1 : passes_of(r);
+#pragma unroll 1
+                for (int p = 0; p < passes && ok; ++p, ++s) {
+                    if (!dry && s % kMtFin != warp - kMtWarps) continue;
+                    const int buf = s % kMtRed;
+                    if (!dry) ok = wait_or_stop(redfull + buf, (s / kMtRed) & 1, stop_s);
+                    if (!ok) break;
+                    const int row = lane & 15, tk = 2 * p + (lane >> 4);  // lane = 16 token + row
+#pragma unroll 1
+                    for (int i = 0; i < tpr; ++i) {
+                        const int tl = g0 + r * tpr + i;
+                        if (tl >= g1) break;
+                        const int4 q = dry ? make_int4(0, 0, 1, 0) : list[tl >> lgG];
+                        if (tk < __popc((uint32_t)q.z)) {
+                            const float *v = red + (buf * kMtWarps + i * 2 * nb) * 32 + lane;
+                            float gv = 0.f, uv = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (k < nb) {
+                                    gv += v[k * 32];
+                                    uv += v[(nb + k) * 32];
+                                }
+                            const float rs = dry ? 1.f : rs_s[ptok_s[q.y + tk]];
+                            uint32_t h3[3];
+                            split3(silu(rs * gv) * (rs * uv), h3);
+                            uint16_t *h = a.hs + (size_t)(q.y + tk) * 3 * I + ((tl & ((1 << lgG) - 1)) << 4) + row;
+                            if (!dry)
+#pragma unroll
+                                for (int k = 0; k < 3; ++k)
+                                    __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!dry && lane == 0) mbar_arrive(redempty + buf);
+                    __syncwarp();
+                }
+            }
+            if (dry) s = 0;
+            if (down || dry) {  // (the dry run only passes by) weights and pair numbers, for the combine
+#pragma unroll 1
+                for (int t = warp - kMtWarps; t < (dry || !routed ? 0 : T); t += kMtFin) {
                     const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
                     if (lane < K) w_s[t * K + lane] = w;
                     __syncwarp();
                 }
-            }
-            if (!down) {  // pair numbers of (t, k)
 #pragma unroll 1
-                for (int i = tid - kMtWarps * 32; i < T * K; i += kMtFin * 32) {
+                for (int i = tid - kMtWarps * 32; i < (dry ? 0 : T * K); i += kMtFin * 32) {
                     const int e = id_s[i];
-                    int at = 0, n = *nd_s;  // position of e in the list (sorted by expert)
+                    int at = 0, n = nD;  // position of e in the list (sorted by expert)
                     while (n > 1) {
                         const int h = n >> 1;
                         if (list[at + h].x <= e) at += h, n -= h;
@@ -699,65 +784,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 }
                 __syncwarp();
             }
-#pragma unroll 1
-            for (int r = 0; r < rounds && ok; ++r) {
-                const int passes = passes_of(r);
-#pragma unroll 1
-                for (int p = 0; p < passes && ok; ++p, ++s) {
-                    if (s % kMtFin != warp - kMtWarps) continue;
-                    const int buf = s % kMtRed;
-                    ok = wait_or_stop(redfull + buf, (s / kMtRed) & 1, stop_s);
-                    if (!ok) break;
-                    const float *rb = red + buf * kMtWarps * 32;
-                    if (!down) {  // lane = 16 token + row
-                        const int row = lane & 15, tk = 2 * p + (lane >> 4);
-#pragma unroll 1
-                        for (int i = 0; i < per; ++i) {
-                            const int tl = g0 + r * per + i;
-                            if (tl >= g1) break;
-                            const int4 q = list[tl >> lgG];
-                            if (tk < __popc((uint32_t)q.z)) {
-                                const float *v = rb + i * 2 * nb * 32 + lane;
-                                float gv = 0.f, uv = 0.f;
-#pragma unroll 1
-                                for (int k = 0; k < nb; ++k) {
-                                    gv += v[k * 32];
-                                    uv += v[(nb + k) * 32];
-                                }
-                                const float rs = rs_s[ptok_s[q.y + tk]];
-                                uint32_t h3[3];
-                                split3(silu(rs * gv) * (rs * uv), h3);
-                                uint16_t *h = a.hs + (size_t)(q.y + tk) * 3 * I + ((tl & ((1 << lgG) - 1)) << 4) + row;
-#pragma unroll
-                                for (int k = 0; k < 3; ++k)
-                                    __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
-                            }
-                            __syncwarp();
-                        }
-                    } else {
-                        const int tl = d0 + r, rows = 256 >> lgu;
-                        const int4 q = list[tl >> lgD];
-                        const int left = __popc((uint32_t)q.z) - 2 * p;
-                        float *o = a.o + (size_t)(q.y + 2 * p) * H + (tl & ((1 << lgD) - 1)) * rows;
-#pragma unroll 1
-                        for (int i = lane; i < rows * (left > 1 ? 2 : 1); i += 32) {
-                            const int tk = i >= rows ? 1 : 0, row = i - tk * rows;
-                            // row = 16 stride (rg / stride) + stride i + rg % stride of row group rg
-                            const int rg = ((row >> (4 + lgs)) << lgs) + (row & ((1 << lgs) - 1)), ri = (row >> lgs) & 15;
-                            float v = 0.f;
-#pragma unroll 1
-                            for (int k = 0; k < upe; ++k) v += rb[((rg << lgu) + k) * 32 + tk * 16 + ri];
-                            __stcg(o + (size_t)tk * H + row, v);
-                        }
-                        __syncwarp();
-                    }
-                    if (lane == 0) mbar_arrive(redempty + buf);
-                    __syncwarp();
-                }
-            }
         } else {
-            // this warp's unit: G (tile ti of the round, gate or up, block blk), D (row group, block)
-            const int ti = down ? 0 : warp >> (lgnb + 1), blk = down ? warp & (upe - 1) : warp & (nb - 1);
+            // this warp's unit: G (tile ti of the round, gate or up, block blk), D (expert ti of the round, block)
+            const int ti = down ? warp >> lgu : warp >> (lgnb + 1), blk = down ? warp & (upe - 1) : warp & (nb - 1);
             const int width = down ? I : H, steps = down && I < 256 ? 4 : 8, go = down && I < 256 ? 32 * (g & 1) : 0;
             const bool even = (blk & 1) == 0;
             int off, off8;  // bytes of rows g and g + 8 in the stage
@@ -765,21 +794,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 off = ti * tileb + (((warp >> lgnb) & 1) * 16 + g) * rowb + blk * kBlockBytes;
                 off8 = off + 8 * rowb;
             } else {
-                const int rg = warp >> lgu, row = ((rg >> lgs) << (4 + lgs)) + (rg & ((1 << lgs) - 1));
                 // a row of 128 values is half a block: rows 2 i and 2 i + 1 share block i
-                off = I >= 256 ? ((row + (g << lgs)) << lgu) * kBlockBytes + blk * kBlockBytes
-                               : ((row + g) >> 1) * kBlockBytes;
-                off8 = off + (I >= 256 ? (8 << lgs) << lgu : 4) * kBlockBytes;
+                off = ti * dnb + (I >= 256 ? (g << lgu) + blk : g >> 1) * kBlockBytes;
+                off8 = off + (I >= 256 ? 8 << lgu : 4) * kBlockBytes;
             }
             // The B fragments of the next pass are loaded as soon as the present ones have been
-            // used; they stay while the rows do.
-            int haveA = -1, haveB = -1;
-            auto fetch = [&](int r, int p) {
-                const int tile = r0 + r * per + ti;
-                if (r >= rounds || tile >= r1) return;
-                const int4 l = list[tile >> lgt];
-                const int ntok = __popc((uint32_t)l.z), at = l.y + 2 * p;
+            // used; in G they stay while the tokens do.
+            int haveA = -1, haveB = -1, ntok = dry ? 1 : 0, first = 0;  // of the present round: tokens, first pair
+            auto find = [&](int r) {  // the entry of this warp's unit in round r
+                const int at = down ? r * epr + ti : (g0 + r * tpr + ti) >> lgG;
+                const bool in = down ? at < nD : g0 + r * tpr + ti < g1;
+                ntok = 0;
+                if (r < rounds && in) {
+                    const int4 l = list[at];
+                    ntok = __popc((uint32_t)l.z);
+                    first = l.y;
+                }
+            };
+            auto fetch = [&](int p) {
                 if (2 * p >= ntok) return;
+                const int at = first + 2 * p;
                 const int rA = down ? at : ptok_s[at], rB = 2 * p + 1 < ntok ? (down ? at + 1 : ptok_s[at + 1]) : -1;
                 if (rA == haveA && rB == haveB) return;
                 const uint16_t *src = down ? a.hs : a.xs;
@@ -788,78 +822,87 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 haveA = rA;
                 haveB = rB;
             };
-            fetch(0, 0);
+            if (!dry) {
+                find(0);
+                fetch(0);
+            }
 #pragma unroll 1
             for (int r = 0; r < rounds && ok; ++r) {
-                const int tile = r0 + r * per + ti, passes = passes_of(r);
-                const int ntok = tile < r1 ? __popc((uint32_t)list[tile >> lgt].z) : 0;
+                const int n = ntok, pair = first;
+                const int passes = down || tpr == 1 ? max(1, (n + 1) >> 1) : dry ? 1 : passes_of(r);
                 const uint8_t *st = ring + slot * kMtStage;
-                ok = wait_or_stop(full + slot, turn & 1, stop_s);
+                if (!dry) ok = wait_or_stop(full + slot, turn & 1, stop_s);
 #pragma unroll 1
-                for (int p = 0; p < passes && ok; ++p, ++s) {
-                    const int buf = s % kMtRed;
+                for (int p = 0; p < passes && ok; ++p) {
                     float v0 = 0.f, v1 = 0.f;
-                    if (2 * p < ntok) unit_dot<WIDE>(st + off, st + off8, go, steps, even, b, tabc, v0, v1);
+                    if (2 * p < n) unit_dot<WIDE>(st + off, st + off8, go, steps, even, b, tabc, v0, v1);
                     const bool last = p == passes - 1;
-                    if (last) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty + slot);
+                    if (!dry) {
+                        if (last) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(empty + slot);
+                            find(r + 1);
+                        }
+                        fetch(last ? 0 : p + 1);
                     }
-                    fetch(last ? r + 1 : r, last ? 0 : p + 1);
-                    if (s >= kMtRed) ok = wait_or_stop(redempty + buf, (s / kMtRed - 1) & 1, stop_s);
-                    if (t4 < 2 && 2 * p < ntok) {
-                        float *v = red + (buf * kMtWarps + warp) * 32 + t4 * 16;
+                    if (!down) {
+                        const int buf = s % kMtRed;
+                        if (!dry && s >= kMtRed) ok = wait_or_stop(redempty + buf, (s / kMtRed - 1) & 1, stop_s);
+                        if (!dry && t4 < 2 && 2 * p < n) {
+                            float *v = red + (buf * kMtWarps + warp) * 32 + t4 * 16;
+                            v[g] = v0;
+                            v[g + 8] = v1;
+                        }
+                        __syncwarp();
+                        if (!dry) {
+                            if (lane == 0) mbar_arrive(redfull + buf);
+                            ++s;
+                        }
+                    } else if (t4 < 2 && 2 * p + t4 < n) {
+                        float *v = part + (((pair + 2 * p + t4) << lgu) + blk) * 16;
                         v[g] = v0;
                         v[g + 8] = v1;
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(redfull + buf);
                 }
-                if (++slot == a.stages) slot = 0, ++turn;
+                if (!dry && ++slot == a.stages) slot = 0, ++turn;
             }
         }
+        if (dry) continue;
         if (!ok && lane == 0) {
             dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
             *stop_s = 1;
         }
         __syncwarp();
         if (workers_sync_or(!ok)) return;
-        if (!workers_grid_sync(a.ctr, target, ok_s, a.ctrl, *cap_s)) {
-            if (tid == 0) *stop_s = 1;
-            return;
-        }
+        if (down) break;
+        grid_arrive(a.ctr, target);
+        if (!grid_wait(a.ctr, target, stop_s, a.ctrl, cap)) return;
     }
-    // C: four outputs per thread over the whole grid
-#pragma unroll 1
-    for (int i = cta * kMtWork + tid; i < T * H / 4; i += G * kMtWork) {
-        const int t = i >> (lgH - 2), h = (i << 2) & (H - 1);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    if (cta >= H / 16) return;
+    for (int i = tid; i < 16 * T; i += kMtWork) {
+        const int t = i >> 4, row = i & 15;
+        float acc = 0.f;
+#pragma unroll 2
         for (int k = 0; k < K; ++k) {
-            const float w = w_s[t * K + k];
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o + (size_t)pair_s[t * K + k] * H + h));
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+            const float *o = part + ((int)pair_s[t * K + k] << lgu) * 16 + row;
+            float v = 0.f;
+            for (int j = 0; j < upe; ++j) v += o[j * 16];
+            acc = fmaf(w_s[t * K + k], v, acc);
         }
-        float *y = a.y + (size_t)t * H + h;
-        y[0] = a.accumulate ? y[0] + acc.x : acc.x;
-        y[1] = a.accumulate ? y[1] + acc.y : acc.y;
-        y[2] = a.accumulate ? y[2] + acc.z : acc.z;
-        y[3] = a.accumulate ? y[3] + acc.w : acc.w;
+        float *y = a.y + (size_t)t * H + cta * 16 + row;
+        *y = a.accumulate ? *y + acc : acc;
     }
 }
 
-size_t mt_raw_bytes(int T, int E) { return align_up((size_t)T * E * sizeof(float), 256); }
+size_t mt_raw_bytes(int T) { return (size_t)T * 512 * sizeof(float); }
 size_t mt_x_bytes(int T, int H) { return align_up((size_t)T * 3 * H * sizeof(uint16_t), 256); }
 
 }  // namespace
 
 extern "C" size_t moe_decode_tokens_workspace_bytes(const rl_moe_shape *shp, int32_t T) {
     if (check_shape(shp) != RL_OK || T <= 0 || T > kMtMaxT) return 0;
-    return kMtHdr + mt_raw_bytes(T, shp->n_experts) + mt_x_bytes(T, shp->hidden) +
-           mt_x_bytes(T * shp->top_k, shp->inter) + (size_t)T * shp->top_k * shp->hidden * sizeof(float);
+    return kMtHdr + mt_raw_bytes(T) + mt_x_bytes(T, shp->hidden) +
+           mt_x_bytes(T * shp->top_k, shp->inter);
 }
 
 extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, int32_t T, const float *x,
@@ -900,9 +943,8 @@ extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, i
     a.ctr = reinterpret_cast<unsigned long long *>(w8);
     a.rs = reinterpret_cast<float *>(w8 + 128);
     a.raw = reinterpret_cast<float *>(w8 + kMtHdr);
-    a.xs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T, shp->n_experts));
-    a.hs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T, shp->n_experts) + mt_x_bytes(T, shp->hidden));
-    a.o = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.hs) + mt_x_bytes(T * shp->top_k, shp->inter));
+    a.xs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T));
+    a.hs = reinterpret_cast<uint16_t *>(w8 + kMtHdr + mt_raw_bytes(T) + mt_x_bytes(T, shp->hidden));
     a.eps = norm_eps;
     a.layer = layer;
     a.T = T;
@@ -911,8 +953,9 @@ extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, i
     a.K = shp->top_k;
     a.I = shp->inter;
     a.accumulate = accumulate != 0;
-    a.stages = (227 * 1024 - kMtORing) / kMtStage < kMtMaxStages ? (227 * 1024 - kMtORing) / kMtStage : kMtMaxStages;
-    const size_t smem = kMtORing + (size_t)a.stages * kMtStage;
+    const int ring = mt_ring(T, a.K, a.I), most = (227 * 1024 - ring) / kMtStage;
+    a.stages = most < kMtMaxStages ? most : kMtMaxStages;
+    const size_t smem = ring + (size_t)a.stages * kMtStage;
     const int G = sm_count();
     if (G < 128) return fail(RL_ERR_UNSUPPORTED, "moe_decode_tokens: needs a GPU of 128 SMs or more");
     // 32-bit reads of the group bytes need two blocks or more per matrix row

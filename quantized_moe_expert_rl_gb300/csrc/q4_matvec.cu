@@ -163,11 +163,22 @@ __device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *
     }
 }
 
+// The masks and constants of the conversion, held in registers: with immediates the AND-OR would take
+// two instructions.
+struct Q4Const {
+    uint32_t lo, hi, bias;
+};
+__device__ __forceinline__ Q4Const q4_const() {
+    Q4Const c;
+    asm volatile("mov.b32 %0, 0x000f000f;\n\tmov.b32 %1, 0x00f000f0;\n\tmov.b32 %2, 0x64006400;"
+                 : "=r"(c.lo), "=r"(c.hi), "=r"(c.bias));
+    return c;
+}
 // q - 8 for the nibbles at bits 0-3 (LO) or 4-7 of both 16-bit halves of w, as a pair of halves
 template <bool LO>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-    constexpr uint32_t m = LO ? 0x000f000fu : 0x00f000f0u;
-    const uint32_t biased = (w & m) | 0x64006400u;
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, const Q4Const &c) {
+    uint32_t biased;  // (w & mask) | bias
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(biased) : "r"(w), "r"(LO ? c.lo : c.hi), "r"(c.bias));
     const __half2 h = *reinterpret_cast<const __half2 *>(&biased);
     const __half2 r = LO ? __hadd2(h, __floats2half2_rn(-1032.f, -1032.f))
                          : __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-72.f, -72.f));
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
     // ldmatrix: lane l addresses row (l & 7) + 8 (bit 3 of l) of 16-byte piece 2 jj + (l >> 4)
     const int lr = (lane & 7) + ((lane >> 3) & 1) * 8, lp = lane >> 4;
     const uint32_t lrow = smem_addr(ring) + lr * 128, x0 = (lp ^ (lr & 7)) << 4, x1 = x0 ^ 32, x2 = x0 ^ 64, x3 = x0 ^ 96;
+    const Q4Const kc = q4_const();
     int slot = 0, parity = 0;
     for (int tile = first; tile < tiles; tile += step) {
         float y[NT][YV];
@@ -307,9 +319,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
                             for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
                     }
                     const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1], v0 = w0 >> 8, v1 = w1 >> 8;
-                    const uint32_t a0 = q4_pair<true>(w0), a1 = q4_pair<true>(w1), a2 = q4_pair<false>(w0),
-                                   a3 = q4_pair<false>(w1), a4 = q4_pair<true>(v0), a5 = q4_pair<true>(v1),
-                                   a6 = q4_pair<false>(v0), a7 = q4_pair<false>(v1);
+                    const uint32_t a0 = q4_pair<true>(w0, kc), a1 = q4_pair<true>(w1, kc), a2 = q4_pair<false>(w0, kc),
+                                   a3 = q4_pair<false>(w1, kc), a4 = q4_pair<true>(v0, kc), a5 = q4_pair<true>(v1, kc),
+                                   a6 = q4_pair<false>(v0, kc), a7 = q4_pair<false>(v1, kc);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint4 b = bst[(c * NT + n) * 32];
