@@ -15,9 +15,9 @@
 //   D  down: CTA b has output rows 16 b .. 16 b + 15 of every expert, so that the sum over k in
 //      selection order needs no further exchange.  (Tiles of 128 rows spread over all SMs, with the
 //      outputs exchanged through a third grid barrier, were no faster at 32 tokens and 3 us slower at 1.)
-// G and D run the same code on rounds of 16 units, one per computing warp: 16 weight rows x 256
-// values (one block of every row).  In G a round's block sums go through one of four buffers to a
-// finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
+// Work comes in rounds of units, a unit being 16 weight rows x 256 values (one block of every row).  In G
+// a computing warp has two units of a round, gate and up of the same rows and block, which share
+// the activations; in D it has one.  A G round's block sums go through one of four buffers to a finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
 // CTA takes a run of consecutive G tiles of equal weight, where a tile weighs one per two tokens of its
 // expert; an expert's activations then stay in registers over its tiles.
 // For one token the launch is a chain of latencies, much of it the first fetch of each phase's code.
@@ -45,8 +45,8 @@ constexpr int kMtWork = (kMtWarps + kMtFin) * 32;   // threads that meet at the 
 constexpr int kMtThreads = kMtWork + 32;            // and the copying warp
 constexpr int kMtRed = 4;                           // buffers between computing and finishing warps
 constexpr int kMtMaxT = 32;
-constexpr int kMtStage = 16896;    // one round of weights: 16 units of 16 rows x 256 values
-constexpr int kMtMaxStages = 8;
+constexpr int kMtUnits = 16896;    // bytes of 16 units of 16 rows x 256 values
+constexpr int kMtMaxStages = 4;
 constexpr int kMtHdr = 256;        // workspace: barrier counter, test knobs (64..71), RMS scales (128..255)
 
 struct MtArgs {
@@ -63,11 +63,11 @@ struct MtArgs {
     float *rs, *raw;       // [32] RMS scales, [T][512] router dots
     uint16_t *xs, *hs;     // [T][3][H], [T K][3][I] bf16 parts
     float eps;
-    int layer, T, H, E, K, I, accumulate, stages;
+    int layer, T, H, E, K, I, accumulate, stages, halves;  // ring slots, and 16-unit halves of one (2, or 1)
 };
 
 // shared memory: the header (barriers, scalars), the codebook table, then
-constexpr int kMtRedB = kMtRed * kMtWarps * 32 * 4;  // [kMtRed][16 units][2 tokens][16 rows] f32
+constexpr int kMtRedB = kMtRed * kMtWarps * 64 * 4;  // [kMtRed][16 warps][gate, up][2 tokens][16 rows] f32
 constexpr int kMtORed = 512 + kTabBytes;
 constexpr int kMtOList = kMtORed + kMtRedB;          // [512] (expert, first pair, token mask, weight before it)
 constexpr int kMtOMask = kMtOList + 512 * 16;        // [512] u32 token masks by expert
@@ -137,7 +137,10 @@ __device__ __forceinline__ bool grid_wait(unsigned long long *ctr, unsigned long
     return *stop == 0;
 }
 
-// Bounded wait of a whole warp for phase `parity` of an mbarrier, given up once *stop is set.
+// Bounded wait of a whole warp for phase `parity` of an mbarrier, given up once *stop is set.  The
+// warps that mostly wait (SLEEP) sleep between their polls, so that they leave the issue slots to
+// the computing warps.
+template <bool SLEEP>
 __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, const volatile int *stop) {
     if (__all_sync(kFull, mbar_test_wait(bar, parity))) return true;
     int ok = 0;
@@ -149,6 +152,7 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, con
                 break;
             }
             if (*stop) break;
+            if (SLEEP) __nanosleep(40);
         }
     }
     __syncwarp();  // rejoin the warp (see cta_sync)
@@ -196,69 +200,90 @@ __device__ __forceinline__ int lane_group(int j, int t, bool even) {
     return g < 0 ? 31 : g;
 }
 
-// One unit against two tokens: d * sums of rows g (v0) and g + 8 (v1) for token t in lanes t = 0, 1.
-// p0, p1: the block's first byte in this lane's two rows (plus, for half blocks, 16 groups in `go`).
+// What the activations of a unit come from: this lane's column of B (16-byte pieces of one bf16 part
+// of one row), or NULL for a column that is not used.
+struct BColumn {
+    const uint4 *p;
+};
+// B fragments of two rows of bf16 parts (rowA, rowB: [3][width], rowB may be NULL), values from `at` on:
+// lane (n, t) holds its groups of column n.
+__device__ __forceinline__ BColumn b_column(const uint16_t *rowA, const uint16_t *rowB, int width, int at) {
+    const int n = (threadIdx.x >> 2) & 7;
+    const uint16_t *row = (n == 2 || n == 3 || n == 5) ? rowB : rowA;
+    const int part = n >= 4 ? 2 : n & 1;
+    BColumn c;
+    c.p = n < 6 && row != nullptr ? reinterpret_cast<const uint4 *>(row + part * width + at) : nullptr;
+    return c;
+}
 template <bool WIDE>
-__device__ __forceinline__ void unit_dot(const uint8_t *p0, const uint8_t *p1, int go, int steps, bool even,
-                                         const uint4 (&b)[8], const uint4 *tabc, float &v0, float &v1) {
+__device__ __forceinline__ void load_b(uint4 (&b)[8], BColumn c, int steps, bool even) {
     const int t = threadIdx.x & 3;
-    float c[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-    if (WIDE) {
-        const uint8_t *w0 = p0 + (even ? 0 : 2) + 4 * t, *w1 = p1 + (even ? 0 : 2) + 4 * t;
-        uint32_t w[4], v[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            w[m] = *reinterpret_cast<const uint32_t *>(w0 + 16 * m);
-            v[m] = *reinterpret_cast<const uint32_t *>(w1 + 16 * m);
-        }
-        if (even && t == 0) {
-            w[0] = (w[0] & 0xffff0000u) | lds_half(p0 + 64);
-            v[0] = (v[0] & 0xffff0000u) | lds_half(p1 + 64);
-        }
+    for (int j = 0; j < 8; ++j)
+        b[j] = c.p != nullptr && (WIDE || j < steps) ? __ldcg(c.p + lane_group<WIDE>(j, t, even)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// NU units against two tokens: d * sums of rows g (v[u][0]) and g + 8 (v[u][1]) for token t in lanes t = 0,
+// 1.  p[u]: the block's first byte in row g of unit u, `r8` bytes before row g + 8's (`go`: bytes of the
+// groups before this lane's, for half blocks).  One straight piece of code: a branch in it (say, to refill
+// B half-way) keeps the compiler from overlapping the steps and cost 40% in D.
+template <bool WIDE, int NU>
+__device__ __forceinline__ void unit_dot(const uint8_t *const (&p)[NU], int r8, int go, int steps, bool even,
+                                         const uint4 (&b)[8], const uint4 *tabc, float (&v)[NU][2]) {
+    const int t = threadIdx.x & 3;
+    float c[NU][2][4] = {};
+    auto step = [&](int j, uint32_t (&x)[NU][2]) {  // x: index | sign << 8 in the half (j & 1) of a word
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t x = w[j >> 1], y = v[j >> 1];
-            uint4 q = tabc[((j & 1) ? __byte_perm(x, 0, 0x4442) : x & 0xffu) * kTabCopies];
-            uint4 r = tabc[((j & 1) ? __byte_perm(y, 0, 0x4442) : y & 0xffu) * kTabCopies];
-            flip_signs(q, (j & 1) ? x >> 24 : __byte_perm(x, 0, 0x4441));
-            flip_signs(r, (j & 1) ? y >> 24 : __byte_perm(y, 0, 0x4441));
-            mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
-            mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
+        for (int u = 0; u < NU; ++u) {
+            const bool hi = WIDE && (j & 1);
+            uint4 q = tabc[(hi ? __byte_perm(x[u][0], 0, 0x4442) : x[u][0] & 0xffu) * kTabCopies];
+            uint4 r = tabc[(hi ? __byte_perm(x[u][1], 0, 0x4442) : x[u][1] & 0xffu) * kTabCopies];
+            flip_signs(q, hi ? x[u][0] >> 24 : __byte_perm(x[u][0], 0, 0x4441));
+            flip_signs(r, hi ? x[u][1] >> 24 : __byte_perm(x[u][1], 0, 0x4441));
+            mma_bf16(c[u][0], q.x, r.x, q.y, r.y, b[j].x, b[j].y);
+            mma_bf16(c[u][1], q.z, r.z, q.w, r.w, b[j].z, b[j].w);
         }
-    } else {
+    };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= steps) break;
-            const uint32_t gw = lds_half(p0 + go + 2 + 8 * j + 2 * t), gv = lds_half(p1 + go + 2 + 8 * j + 2 * t);
-            uint4 q = tabc[(gw & 0xffu) * kTabCopies], r = tabc[(gv & 0xffu) * kTabCopies];
-            flip_signs(q, gw >> 8);
-            flip_signs(r, gv >> 8);
-            mma_bf16(c, q.x, r.x, q.y, r.y, b[j].x, b[j].y);
-            mma_bf16(e, q.z, r.z, q.w, r.w, b[j].z, b[j].w);
+    for (int m = 0; m < 4; ++m) {
+        uint32_t x[NU][2];
+        if (WIDE) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *row = p[u] + h * r8;
+                    x[u][h] = *reinterpret_cast<const uint32_t *>(row + (even ? 0 : 2) + 4 * t + 16 * m);
+                    if (m == 0) {
+                        const uint32_t g31 = lds_half(row + 64);
+                        x[u][h] = even && t == 0 ? __byte_perm(x[u][h], g31, 0x3254) : x[u][h];
+                    }
+                }
+            step(2 * m, x);
+            step(2 * m + 1, x);
+        } else {
+#pragma unroll
+            for (int j = 2 * m; j < 2 * m + 2; ++j)
+                if (j < steps) {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) x[u][h] = lds_half(p[u] + h * r8 + go + 2 + 8 * j + 2 * t);
+                    step(j, x);
+                }
         }
     }
     // columns 0, 1: token 0 leading and middle parts; 2, 3: token 1; 4: token 0 last part; 5: token 1
     const int src = (threadIdx.x & 28) | 2;
-    const float c0 = c[0] + e[0], c1 = c[1] + e[1], c2 = c[2] + e[2], c3 = c[3] + e[3];
-    const float l0 = __shfl_sync(kFull, c0, src), l1 = __shfl_sync(kFull, c1, src);
-    const float l2 = __shfl_sync(kFull, c2, src), l3 = __shfl_sync(kFull, c3, src);
-    v0 = fp16_bits_to_float(lds_half(p0)) * ((c0 + c1) + (t == 0 ? l0 : l1));
-    v1 = fp16_bits_to_float(lds_half(p1)) * ((c2 + c3) + (t == 0 ? l2 : l3));
-}
-
-// B fragments of two rows of bf16 parts (rowA, rowB: [3][width], rowB may be NULL), values from
-// `at` on: lane (n, t) holds its groups of column n.
-template <bool WIDE>
-__device__ __forceinline__ void load_b(uint4 (&b)[8], const uint16_t *rowA, const uint16_t *rowB, int width, int at,
-                                       int steps, bool even) {
-    const int n = (threadIdx.x >> 2) & 7, t = threadIdx.x & 3;
-    const uint16_t *row = (n == 2 || n == 3 || n == 5) ? rowB : rowA;
-    const int part = n >= 4 ? 2 : n & 1;
-    const bool in = n < 6 && row != nullptr;
-    const uint4 *p = reinterpret_cast<const uint4 *>(row + part * width + at);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        b[j] = in && (WIDE || j < steps) ? __ldcg(p + lane_group<WIDE>(j, t, even)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < NU; ++u) {
+        const float c0 = c[u][0][0] + c[u][1][0], c1 = c[u][0][1] + c[u][1][1];
+        const float c2 = c[u][0][2] + c[u][1][2], c3 = c[u][0][3] + c[u][1][3];
+        const float l0 = __shfl_sync(kFull, c0, src), l1 = __shfl_sync(kFull, c1, src);
+        const float l2 = __shfl_sync(kFull, c2, src), l3 = __shfl_sync(kFull, c3, src);
+        v[u][0] = fp16_bits_to_float(lds_half(p[u])) * ((c0 + c1) + (t == 0 ? l0 : l1));
+        v[u][1] = fp16_bits_to_float(lds_half(p[u] + r8)) * ((c2 + c3) + (t == 0 ? l2 : l3));
+    }
 }
 
 // The K best of the E keys in shared memory (key, then lower index; E <= 512, key[e] = 0 from E on) by
@@ -518,7 +543,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         cta_sync();
         if (*stop_s || (*bad_s & 7)) return;
         cta_sync();
-        const int nD = *nd_s, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb;
+        const int nD = *nd_s, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 * a.halves / nb, tileb = 32 * rowb;
         const int lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, epr = kMtWarps / upe, dnb = I * kBlockBytes / 16;
         const int g0 = run_s[0], g1 = run_s[1];
         const int gr = (g1 - g0 + tpr - 1) / tpr, dr = cta < H / 16 ? (nD + epr - 1) / epr : 0;
@@ -526,11 +551,11 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         int slot = 0, turn = 0, issued = 0;
 #pragma unroll 1
         for (int r = 0; r < gr + dr; ++r) {
-            if (turn > 0 && !wait_or_stop(empty + slot, (turn - 1) & 1, stop_s)) {
+            if (turn > 0 && !wait_or_stop<true>(empty + slot, (turn - 1) & 1, stop_s)) {
                 if (lane == 0) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
                 break;
             }
-            uint8_t *dst = ring + slot * kMtStage;
+            uint8_t *dst = ring + slot * a.halves * kMtUnits;
             if (r < gr) {
                 const int n = min(tpr, g1 - g0 - r * tpr);
                 if (lane == 0) mbar_arrive_expect_tx(full + slot, n * tileb);
@@ -560,7 +585,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         return;
     }
 
-    const int g = lane >> 2, t4 = lane & 3, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 / nb, tileb = 32 * rowb;
+    const int g = lane >> 2, t4 = lane & 3, nb = H >> 8, rowb = nb * kBlockBytes, tpr = 8 * a.halves / nb, tileb = 32 * rowb;
     const int lgnb = 31 - __clz(nb), lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, lgu = 31 - __clz(upe);
     const int epr = kMtWarps >> lgu, dnb = I * kBlockBytes / 16;
     const uint4 *tabc = tab + (lane & (kTabCopies - 1));
@@ -569,7 +594,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int ph = -1; ph < 2; ++ph) {  // -1: the dry run, 0: S and G, 1: D
+    for (int ph = -1; ph < 2; ++ph) {  // -1: the dry run (of G's code), 0: S and G, 1: D
         const bool dry = ph < 0, down = ph == 1;
         if (ph == 0) {
             ok = grid_wait(a.ctr, target, stop_s, a.ctrl, cap);
@@ -711,7 +736,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
             if (bad & 7) return;
         }
         const int gr = (g1 - g0 + tpr - 1) / tpr, dr = cta < H / 16 ? (nD + epr - 1) >> (4 - lgu) : 0;
-        const int rounds = down ? dr : dry && warp == 0 ? 0 : gr;  // (warp 0 waits for the grid)
+        const int rounds = dry ? (warp == 0 ? 0 : 1) : down ? dr : gr;  // (warp 0 waits for the grid)
         // passes (two tokens each) of a G round: as many as its most shared expert needs
         auto passes_of = [&](int r) {
             int n = 1;
@@ -731,7 +756,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 for (int p = 0; p < passes && ok; ++p, ++s) {
                     if (!dry && s % kMtFin != warp - kMtWarps) continue;
                     const int buf = s % kMtRed;
-                    if (!dry) ok = wait_or_stop(redfull + buf, (s / kMtRed) & 1, stop_s);
+                    if (!dry) ok = wait_or_stop<true>(redfull + buf, (s / kMtRed) & 1, stop_s);
                     if (!ok) break;
                     const int row = lane & 15, tk = 2 * p + (lane >> 4);  // lane = 16 token + row
 #pragma unroll 1
@@ -740,13 +765,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                         if (tl >= g1) break;
                         const int4 q = dry ? make_int4(0, 0, 1, 0) : list[tl >> lgG];
                         if (tk < __popc((uint32_t)q.z)) {
-                            const float *v = red + (buf * kMtWarps + i * 2 * nb) * 32 + lane;
+                            const float *v = red + (buf * kMtWarps + i * nb) * 64 + lane;
                             float gv = 0.f, uv = 0.f;
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 if (k < nb) {
-                                    gv += v[k * 32];
-                                    uv += v[(nb + k) * 32];
+                                    gv += v[k * 64];
+                                    uv += v[k * 64 + 32];
                                 }
                             const float rs = dry ? 1.f : rs_s[ptok_s[q.y + tk]];
                             uint32_t h3[3];
@@ -785,83 +810,86 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 __syncwarp();
             }
         } else {
-            // this warp's unit: G (tile ti of the round, gate or up, block blk), D (expert ti of the round, block)
-            const int ti = down ? warp >> lgu : warp >> (lgnb + 1), blk = down ? warp & (upe - 1) : warp & (nb - 1);
+            // this warp's units: G (gate and up of tile ti of the round, block blk), D (expert ti, block)
+            const int ti = down ? warp >> lgu : warp >> lgnb, blk = down ? warp & (upe - 1) : warp & (nb - 1);
             const int width = down ? I : H, steps = down && I < 256 ? 4 : 8, go = down && I < 256 ? 32 * (g & 1) : 0;
             const bool even = (blk & 1) == 0;
-            int off, off8;  // bytes of rows g and g + 8 in the stage
-            if (!down) {
-                off = ti * tileb + (((warp >> lgnb) & 1) * 16 + g) * rowb + blk * kBlockBytes;
-                off8 = off + 8 * rowb;
-            } else {
-                // a row of 128 values is half a block: rows 2 i and 2 i + 1 share block i
-                off = ti * dnb + (I >= 256 ? (g << lgu) + blk : g >> 1) * kBlockBytes;
-                off8 = off + (I >= 256 ? 8 << lgu : 4) * kBlockBytes;
-            }
-            // The B fragments of the next pass are loaded as soon as the present ones have been
-            // used; in G they stay while the tokens do.
-            int haveA = -1, haveB = -1, ntok = dry ? 1 : 0, first = 0;  // of the present round: tokens, first pair
-            auto find = [&](int r) {  // the entry of this warp's unit in round r
+            // byte of row g in the slot, and from there to row g + 8; a row of 128 values is half a block (rows
+            // 2 i and 2 i + 1 share block i)
+            const int off = !down ? ti * tileb + g * rowb + blk * kBlockBytes
+                                  : ti * dnb + (I >= 256 ? (g << lgu) + blk : g >> 1) * kBlockBytes;
+            const int r8 = !down ? 8 * rowb : (I >= 256 ? 8 << lgu : 4) * kBlockBytes;
+            int haveA = -1, haveB = -1, ntok = 0, first = 0;  // B's rows; tokens and first pair of the round's expert
+            auto find = [&](int r) {
                 const int at = down ? r * epr + ti : (g0 + r * tpr + ti) >> lgG;
-                const bool in = down ? at < nD : g0 + r * tpr + ti < g1;
-                ntok = 0;
-                if (r < rounds && in) {
-                    const int4 l = list[at];
-                    ntok = __popc((uint32_t)l.z);
-                    first = l.y;
-                }
+                const bool in = r < rounds && (down ? at < nD : ti < tpr && g0 + r * tpr + ti < g1);
+                const int4 l = list[in ? at : 0];
+                ntok = dry ? (down || ti < tpr ? 1 : 0) : in ? __popc((uint32_t)l.z) : 0;  // (no unit past the slot)
+                first = dry ? 0 : l.y;
             };
-            auto fetch = [&](int p) {
-                if (2 * p >= ntok) return;
+            // the columns of pass p of the round found last; false where B stays as it is
+            auto columns = [&](int p, BColumn &c) {
+                if (2 * p >= ntok) return false;
                 const int at = first + 2 * p;
-                const int rA = down ? at : ptok_s[at], rB = 2 * p + 1 < ntok ? (down ? at + 1 : ptok_s[at + 1]) : -1;
-                if (rA == haveA && rB == haveB) return;
+                const int rA = dry ? 0 : down ? at : ptok_s[at];
+                const int rB = dry || 2 * p + 1 >= ntok ? -1 : down ? at + 1 : ptok_s[at + 1];
+                if (rA == haveA && rB == haveB) return false;
                 const uint16_t *src = down ? a.hs : a.xs;
-                load_b<WIDE>(b, src + (size_t)rA * 3 * width, rB < 0 ? nullptr : src + (size_t)rB * 3 * width, width,
-                             blk * 256, steps, even);
+                c = b_column(src + (size_t)rA * 3 * width, rB < 0 ? nullptr : src + (size_t)rB * 3 * width, width, blk * 256);
                 haveA = rA;
                 haveB = rB;
+                return true;
             };
-            if (!dry) {
-                find(0);
-                fetch(0);
-            }
+            BColumn next = {nullptr};
+            find(0);
+            if (columns(0, next) && !dry) load_b<WIDE>(b, next, steps, even);
 #pragma unroll 1
             for (int r = 0; r < rounds && ok; ++r) {
                 const int n = ntok, pair = first;
-                const int passes = down || tpr == 1 ? max(1, (n + 1) >> 1) : dry ? 1 : passes_of(r);
-                const uint8_t *st = ring + slot * kMtStage;
-                if (!dry) ok = wait_or_stop(full + slot, turn & 1, stop_s);
+                const int passes = dry ? 1 : down ? max(1, (n + 1) >> 1) : passes_of(r);
+                const uint8_t *st = ring + slot * a.halves * kMtUnits + off;
+                if (!dry) ok = wait_or_stop<false>(full + slot, turn & 1, stop_s);
 #pragma unroll 1
                 for (int p = 0; p < passes && ok; ++p) {
-                    float v0 = 0.f, v1 = 0.f;
-                    if (2 * p < n) unit_dot<WIDE>(st + off, st + off8, go, steps, even, b, tabc, v0, v1);
                     const bool last = p == passes - 1;
-                    if (!dry) {
-                        if (last) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(empty + slot);
-                            find(r + 1);
-                        }
-                        fetch(last ? 0 : p + 1);
-                    }
                     if (!down) {
+                        float v[2][2] = {};
+                        if (2 * p < n) {
+                            const uint8_t *const rows[2] = {st, st + 16 * rowb};
+                            unit_dot<WIDE, 2>(rows, r8, 0, 8, even, b, tabc, v);
+                        }
+                        if (dry) continue;
+                        __syncwarp();
+                        if (last && lane == 0) mbar_arrive(empty + slot);
+                        if (last) find(r + 1);
+                        if (columns(last ? 0 : p + 1, next)) load_b<WIDE>(b, next, steps, even);
                         const int buf = s % kMtRed;
-                        if (!dry && s >= kMtRed) ok = wait_or_stop(redempty + buf, (s / kMtRed - 1) & 1, stop_s);
-                        if (!dry && t4 < 2 && 2 * p < n) {
-                            float *v = red + (buf * kMtWarps + warp) * 32 + t4 * 16;
-                            v[g] = v0;
-                            v[g + 8] = v1;
+                        if (s >= kMtRed) ok = wait_or_stop<false>(redempty + buf, (s / kMtRed - 1) & 1, stop_s);
+                        if (t4 < 2 && 2 * p < n) {
+                            float *o = red + (buf * kMtWarps + warp) * 64 + t4 * 16 + g;
+                            o[0] = v[0][0];
+                            o[8] = v[0][1];
+                            o[32] = v[1][0];
+                            o[40] = v[1][1];
                         }
                         __syncwarp();
-                        if (!dry) {
-                            if (lane == 0) mbar_arrive(redfull + buf);
-                            ++s;
+                        if (lane == 0) mbar_arrive(redfull + buf);
+                        ++s;
+                    } else {
+                        float v[1][2] = {};
+                        if (2 * p < n) {
+                            const uint8_t *const rows[1] = {st};
+                            unit_dot<WIDE, 1>(rows, r8, go, steps, even, b, tabc, v);
                         }
-                    } else if (t4 < 2 && 2 * p + t4 < n) {
-                        float *v = part + (((pair + 2 * p + t4) << lgu) + blk) * 16;
-                        v[g] = v0;
-                        v[g + 8] = v1;
+                        __syncwarp();
+                        if (last && lane == 0) mbar_arrive(empty + slot);
+                        if (last) find(r + 1);
+                        if (columns(last ? 0 : p + 1, next)) load_b<WIDE>(b, next, steps, even);
+                        if (t4 < 2 && 2 * p + t4 < n) {
+                            float *o = part + (((pair + 2 * p + t4) << lgu) + blk) * 16 + g;
+                            o[0] = v[0][0];
+                            o[8] = v[0][1];
+                        }
                     }
                 }
                 if (!dry && ++slot == a.stages) slot = 0, ++turn;
@@ -953,9 +981,12 @@ extern "C" rl_status moe_decode_tokens(const rl_moe_shape *shp, int32_t layer, i
     a.K = shp->top_k;
     a.I = shp->inter;
     a.accumulate = accumulate != 0;
-    const int ring = mt_ring(T, a.K, a.I), most = (227 * 1024 - ring) / kMtStage;
-    a.stages = most < kMtMaxStages ? most : kMtMaxStages;
-    const size_t smem = ring + (size_t)a.stages * kMtStage;
+    // two 16-unit halves per ring slot, one where the partial outputs leave too little room
+    const int ring = mt_ring(T, a.K, a.I), room = (227 * 1024 - ring) / kMtUnits;
+    a.halves = room >= 4 ? 2 : 1;
+    a.stages = room / a.halves < kMtMaxStages ? room / a.halves : kMtMaxStages;
+    const size_t smem = ring + (size_t)a.stages * a.halves * kMtUnits;
+    if (a.stages < 1) return fail(RL_ERR_UNSUPPORTED, "moe_decode_tokens: T=%d top_k=%d inter=%d does not fit", T, a.K, a.I);
     const int G = sm_count();
     if (G < 128) return fail(RL_ERR_UNSUPPORTED, "moe_decode_tokens: needs a GPU of 128 SMs or more");
     // 32-bit reads of the group bytes need two blocks or more per matrix row
