@@ -20,9 +20,11 @@
 // the activations; in D it has one.  A G round's block sums go through one of four buffers to a finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
 // CTA takes a run of consecutive G tiles of equal weight, where a tile weighs one per two tokens of its
 // expert; an expert's activations then stay in registers over its tiles.
-// For one token the launch is a chain of latencies, much of it the first fetch of each phase's code.
-// So the codebook table is built, and the unit loop run once on whatever the ring holds (with
-// its waits and stores turned off), while the first grid barrier is pending.
+// For few tokens the launch is a chain of latencies, much of them the first fetch of straight code: a
+// combine unrolled to 16 experts took 8.5k cycles where the rolled loop takes 1.2k.  So what runs once
+// stays in rolled loops, and the codebook table and the expert tables are built while the first grid
+// barrier is pending.  (Running the unit code dry there, to fetch it early, delayed the barrier by as
+// much as it saved; one copy of the unit code for both phases cost 2 us at 1 token and 15 at 32.)
 //
 // The matrix arithmetic.  A weight is d * (codebook value) * (sign): the codebook value is an
 // 8-bit integer, exact in bf16, so a group's 8 values are one 16-byte table entry whose signs are
@@ -589,13 +591,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
     const int lgnb = 31 - __clz(nb), lgG = 31 - __clz(I >> 4), upe = I > 256 ? I >> 8 : 1, lgu = 31 - __clz(upe);
     const int epr = kMtWarps >> lgu, dnb = I * kBlockBytes / 16;
     const uint4 *tabc = tab + (lane & (kTabCopies - 1));
-    int slot = 0, turn = 0, s = 0, g0 = 0, g1 = 1, nD = 1;
+    int slot = 0, turn = 0, s = 0, g0 = 0, g1 = 0, nD = 0;
     uint4 b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int ph = -1; ph < 2; ++ph) {  // -1: the dry run (of G's code), 0: S and G, 1: D
-        const bool dry = ph < 0, down = ph == 1;
+    for (int ph = 0; ph < 2; ++ph) {  // 0: S and G, 1: D
+        const bool down = ph == 1;
         if (ph == 0) {
             ok = grid_wait(a.ctr, target, stop_s, a.ctrl, cap);
             // S: selection.  Keys of every (token, expert) into shared memory, then one warp per token.
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
             if (bad & 7) return;
         }
         const int gr = (g1 - g0 + tpr - 1) / tpr, dr = cta < H / 16 ? (nD + epr - 1) >> (4 - lgu) : 0;
-        const int rounds = dry ? (warp == 0 ? 0 : 1) : down ? dr : gr;  // (warp 0 waits for the grid)
+        const int rounds = down ? dr : gr;
         // passes (two tokens each) of a G round: as many as its most shared expert needs
         auto passes_of = [&](int r) {
             int n = 1;
@@ -751,19 +753,19 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
             // finishing warps: h of every third pass of G
 #pragma unroll 1
             for (int r = 0; r < (down ? 0 : rounds) && ok; ++r) {
-                const int passes = dry ? 1 : passes_of(r);
+                const int passes = passes_of(r);
 #pragma unroll 1
                 for (int p = 0; p < passes && ok; ++p, ++s) {
-                    if (!dry && s % kMtFin != warp - kMtWarps) continue;
+                    if (s % kMtFin != warp - kMtWarps) continue;
                     const int buf = s % kMtRed;
-                    if (!dry) ok = wait_or_stop<true>(redfull + buf, (s / kMtRed) & 1, stop_s);
+                    ok = wait_or_stop<true>(redfull + buf, (s / kMtRed) & 1, stop_s);
                     if (!ok) break;
                     const int row = lane & 15, tk = 2 * p + (lane >> 4);  // lane = 16 token + row
 #pragma unroll 1
                     for (int i = 0; i < tpr; ++i) {
                         const int tl = g0 + r * tpr + i;
                         if (tl >= g1) break;
-                        const int4 q = dry ? make_int4(0, 0, 1, 0) : list[tl >> lgG];
+                        const int4 q = list[tl >> lgG];
                         if (tk < __popc((uint32_t)q.z)) {
                             const float *v = red + (buf * kMtWarps + i * nb) * 64 + lane;
                             float gv = 0.f, uv = 0.f;
@@ -773,31 +775,29 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                                     gv += v[k * 64];
                                     uv += v[k * 64 + 32];
                                 }
-                            const float rs = dry ? 1.f : rs_s[ptok_s[q.y + tk]];
+                            const float rs = rs_s[ptok_s[q.y + tk]];
                             uint32_t h3[3];
                             split3(silu(rs * gv) * (rs * uv), h3);
                             uint16_t *h = a.hs + (size_t)(q.y + tk) * 3 * I + ((tl & ((1 << lgG) - 1)) << 4) + row;
-                            if (!dry)
 #pragma unroll
-                                for (int k = 0; k < 3; ++k)
-                                    __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
+                            for (int k = 0; k < 3; ++k)
+                                __stcg(reinterpret_cast<unsigned short *>(h + (size_t)k * I), (unsigned short)h3[k]);
                         }
                         __syncwarp();
                     }
-                    if (!dry && lane == 0) mbar_arrive(redempty + buf);
+                    if (lane == 0) mbar_arrive(redempty + buf);
                     __syncwarp();
                 }
             }
-            if (dry) s = 0;
-            if (down || dry) {  // (the dry run only passes by) weights and pair numbers, for the combine
+            if (down) {  // weights and pair numbers, for the combine
 #pragma unroll 1
-                for (int t = warp - kMtWarps; t < (dry || !routed ? 0 : T); t += kMtFin) {
+                for (int t = warp - kMtWarps; t < (routed ? T : 0); t += kMtFin) {
                     const float w = topk_weight(lane < K ? w_s[t * K + lane] : 0.f, K);
                     if (lane < K) w_s[t * K + lane] = w;
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int i = tid - kMtWarps * 32; i < (dry ? 0 : T * K); i += kMtFin * 32) {
+                for (int i = tid - kMtWarps * 32; i < T * K; i += kMtFin * 32) {
                     const int e = id_s[i];
                     int at = 0, n = nD;  // position of e in the list (sorted by expert)
                     while (n > 1) {
@@ -824,15 +824,15 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                 const int at = down ? r * epr + ti : (g0 + r * tpr + ti) >> lgG;
                 const bool in = r < rounds && (down ? at < nD : ti < tpr && g0 + r * tpr + ti < g1);
                 const int4 l = list[in ? at : 0];
-                ntok = dry ? (down || ti < tpr ? 1 : 0) : in ? __popc((uint32_t)l.z) : 0;  // (no unit past the slot)
-                first = dry ? 0 : l.y;
+                ntok = in ? __popc((uint32_t)l.z) : 0;
+                first = l.y;
             };
             // the columns of pass p of the round found last; false where B stays as it is
             auto columns = [&](int p, BColumn &c) {
                 if (2 * p >= ntok) return false;
                 const int at = first + 2 * p;
-                const int rA = dry ? 0 : down ? at : ptok_s[at];
-                const int rB = dry || 2 * p + 1 >= ntok ? -1 : down ? at + 1 : ptok_s[at + 1];
+                const int rA = down ? at : ptok_s[at];
+                const int rB = 2 * p + 1 >= ntok ? -1 : down ? at + 1 : ptok_s[at + 1];
                 if (rA == haveA && rB == haveB) return false;
                 const uint16_t *src = down ? a.hs : a.xs;
                 c = b_column(src + (size_t)rA * 3 * width, rB < 0 ? nullptr : src + (size_t)rB * 3 * width, width, blk * 256);
@@ -842,13 +842,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
             };
             BColumn next = {nullptr};
             find(0);
-            if (columns(0, next) && !dry) load_b<WIDE>(b, next, steps, even);
+            if (columns(0, next)) load_b<WIDE>(b, next, steps, even);
 #pragma unroll 1
             for (int r = 0; r < rounds && ok; ++r) {
                 const int n = ntok, pair = first;
-                const int passes = dry ? 1 : down ? max(1, (n + 1) >> 1) : passes_of(r);
+                const int passes = down ? max(1, (n + 1) >> 1) : passes_of(r);
                 const uint8_t *st = ring + slot * a.halves * kMtUnits + off;
-                if (!dry) ok = wait_or_stop<false>(full + slot, turn & 1, stop_s);
+                ok = wait_or_stop<false>(full + slot, turn & 1, stop_s);
 #pragma unroll 1
                 for (int p = 0; p < passes && ok; ++p) {
                     const bool last = p == passes - 1;
@@ -858,7 +858,6 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                             const uint8_t *const rows[2] = {st, st + 16 * rowb};
                             unit_dot<WIDE, 2>(rows, r8, 0, 8, even, b, tabc, v);
                         }
-                        if (dry) continue;
                         __syncwarp();
                         if (last && lane == 0) mbar_arrive(empty + slot);
                         if (last) find(r + 1);
@@ -892,10 +891,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
                         }
                     }
                 }
-                if (!dry && ++slot == a.stages) slot = 0, ++turn;
+                if (++slot == a.stages) slot = 0, ++turn;
             }
         }
-        if (dry) continue;
         if (!ok && lane == 0) {
             dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
             *stop_s = 1;
@@ -907,18 +905,25 @@ __global__ void __launch_bounds__(kMtThreads, 1) moe_tokens_kernel(const __grid_
         if (!grid_wait(a.ctr, target, stop_s, a.ctrl, cap)) return;
     }
     if (cta >= H / 16) return;
+#pragma unroll 1
     for (int i = tid; i < 16 * T; i += kMtWork) {
         const int t = i >> 4, row = i & 15;
-        float acc = 0.f;
-#pragma unroll 2
-        for (int k = 0; k < K; ++k) {
-            const float *o = part + ((int)pair_s[t * K + k] << lgu) * 16 + row;
-            float v = 0.f;
-            for (int j = 0; j < upe; ++j) v += o[j * 16];
-            acc = fmaf(w_s[t * K + k], v, acc);
-        }
         float *y = a.y + (size_t)t * H + cta * 16 + row;
-        *y = a.accumulate ? *y + acc : acc;
+        const float base = a.accumulate ? *y : 0.f;
+        float acc = 0.f;
+        int at = pair_s[t * K];
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+            const float *v = part + (at << lgu) * 16 + row;
+            at = pair_s[t * K + (k + 1 < K ? k + 1 : k)];
+            const float w = w_s[t * K + k];
+            float o = v[0];
+            if (upe > 1) o += v[16];
+#pragma unroll 1
+            for (int j = 2; j < upe; ++j) o += v[j * 16];
+            acc = fmaf(w, o, acc);
+        }
+        *y = a.accumulate ? base + acc : acc;
     }
 }
 
