@@ -121,14 +121,9 @@ __device__ __noinline__ void lp_sort(LpShared &sh, int cnt, int n, bool keep) {
     }
 }
 
-// Put the keys (0 = none) above the threshold into the buffer, after raising the threshold to the
-// n-th largest of the 64 groups' largest keys.  Whole CTA; the buffer holds at most kLpKeep keys before
-// the call and as many after it.
-template <int M>
-__device__ __forceinline__ void lp_insert(LpShared &sh, const unsigned long long (&key)[M], int n) {
-    unsigned long long m = 0ull;
-#pragma unroll
-    for (int i = 0; i < M; ++i) m = key[i] > m ? key[i] : m;
+// Raise the threshold to just below the n-th largest of the 64 groups' (of 4 threads) largest keys, m
+// being this thread's (0: none).  Whole CTA.
+__device__ __noinline__ void lp_raise(LpShared &sh, unsigned long long m, int n) {
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         const unsigned long long v = __shfl_xor_sync(kFull, m, o);
@@ -138,23 +133,20 @@ __device__ __forceinline__ void lp_insert(LpShared &sh, const unsigned long long
     cta_sync();
     // rank of this group's head, 16 comparisons per lane (equal heads are all 0)
     int rank = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int j = threadIdx.x & 3; j < 64; j += 4) rank += sh.heads[j] > m ? 1 : 0;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
     // one below the n-th head, so that the head itself passes
     if ((threadIdx.x & 3) == 0 && rank == n - 1 && m > 0ull && m - 1ull > sh.thr) sh.thr = m - 1ull;
     cta_sync();
-    const unsigned long long t2 = sh.thr;
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-        if (key[i] > t2) sh.cand[atomicAdd(&sh.count, 1)] = key[i];
+}
+// After insertions by the whole CTA: cut the buffer back to its n best if it holds more than kLpKeep.
+__device__ __forceinline__ void lp_settle(LpShared &sh, int n) {
     cta_sync();
     const int cnt = sh.count;
-    if (cnt > kLpKeep) {
-        cta_sync();
-        lp_sort(sh, cnt, n, true);
-    }
+    cta_sync();  // everybody has read the count
+    if (cnt > kLpKeep) lp_sort(sh, cnt, n, true);
 }
 
 __device__ __forceinline__ unsigned long long lp_key(float v, int idx) {
@@ -209,28 +201,45 @@ struct LpTile {
 // The cold parts are functions of their own, so that the tile loop keeps its registers.
 
 // Tiles t0, t0 + kLpTile, .. t1 into the buffer with the threshold raised tile by tile; from ring slot
-// `slot` (one tile), or 0 for the logits' own memory.  Whole CTA.
+// `slot` (one tile), or 0 for the logits' own memory.  Whole CTA.  Rolled loops: this runs once per
+// piece of a row, and fetching straight code costs more than executing it.
 template <typename E>
 __device__ __noinline__ void lp_robust(LpShared &sh, const E *x, int lo, int hi, int t0, int t1, int n, uint32_t slot) {
     using Tile = LpTile<E>;
+    constexpr int EV = Tile::EV;
 #pragma unroll 1
     for (int tt = t0; tt <= t1; tt += kLpTile) {
-        uint4 q[Tile::NV];
-        float v[kLpEpt];
+        unsigned long long best = 0ull;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {  // this thread's largest key; then the keys above the threshold
+            const unsigned long long thr = sh.thr;
+#pragma unroll 1
+            for (int j = 0; j < Tile::NV; ++j) {
+                const int i0 = tt + (j * kLpThreads + threadIdx.x) * EV;
+                const uint4 q = !(i0 >= lo && i0 + EV <= hi) ? Tile::edge(x, lo, hi, i0)
+                                : slot ? lds128(slot + j * kLpThreads * 16) : *reinterpret_cast<const uint4 *>(x + i0);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int j = 0; j < Tile::NV; ++j) {
-            const int i0 = tt + (j * kLpThreads + threadIdx.x) * Tile::EV;
-            q[j] = !(i0 >= lo && i0 + Tile::EV <= hi) ? Tile::edge(x, lo, hi, i0)
-                   : slot ? lds128(slot + j * kLpThreads * 16) : *reinterpret_cast<const uint4 *>(x + i0);
+                for (int k = 0; k < EV; ++k) {
+                    float v;
+                    if constexpr (sizeof(E) == 4) {
+                        v = __uint_as_float(w[k]);
+                    } else {
+                        const float2 f = unpack2(w[k >> 1], E());
+                        v = k & 1 ? f.y : f.x;
+                    }
+                    const int idx = i0 + k;
+                    const unsigned long long key = lp_key(v, idx);
+                    if (idx >= lo && idx < hi) {
+                        if (pass == 0) best = key > best ? key : best;
+                        else if (key > thr) sh.cand[atomicAdd(&sh.count, 1)] = key;
+                    }
+                }
+            }
+            __syncwarp();
+            if (pass == 0) lp_raise(sh, best, n);
         }
-        Tile::unpack(q, v);
-        unsigned long long key[kLpEpt];
-#pragma unroll
-        for (int i = 0; i < kLpEpt; ++i) {
-            const int idx = tt + ((i / Tile::EV) * kLpThreads + threadIdx.x) * Tile::EV + i % Tile::EV;
-            key[i] = idx >= lo && idx < hi ? lp_key(v[i], idx) : 0ull;
-        }
-        lp_insert(sh, key, n);
+        lp_settle(sh, n);
     }
     cta_sync();
 }
@@ -390,8 +399,15 @@ __device__ __noinline__ void lp_cut_rows(const LpArgs &a, LpShared &sh, int r0, 
                     unsigned long long key[M];
 #pragma unroll
                     for (int i = 0; i < M; ++i) key[i] = at(base + i * kLpThreads + tid);
-                    lp_insert(sh, key, n);
-                    cta_sync();
+                    unsigned long long best = 0ull;
+#pragma unroll
+                    for (int i = 0; i < M; ++i) best = key[i] > best ? key[i] : best;
+                    lp_raise(sh, best, n);
+#pragma unroll
+                    for (int i = 0; i < M; ++i)
+                        if (key[i] > sh.thr) sh.cand[atomicAdd(&sh.count, 1)] = key[i];
+                    __syncwarp();
+                    lp_settle(sh, n);
                 }
             }
             lp_sort(sh, sh.count, n, false);

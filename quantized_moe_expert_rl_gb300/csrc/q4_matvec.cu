@@ -66,13 +66,15 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// d += a (16 x 16, half) * b (16 x 8, half), f32 accumulation
+// d = (ADD ? d : 0) + a (16 x 16, half) * b (16 x 8, half), f32 accumulation
+template <bool ADD>
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(ADD ? d[0] : 0.f), "f"(ADD ? d[1] : 0.f),
+          "f"(ADD ? d[2] : 0.f), "f"(ADD ? d[3] : 0.f));
 }
 
 // 8 activations k = 8 o .. 8 o + 7 of token `tok` as f32; zero outside the matrix
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
     constexpr bool SPLIT = KIND == kQ4Split;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int TOK = NT * (SPLIT ? 4 : 8);
+    constexpr int GS = 8 / GL;         // groups per stage: 8, 4, 2
     constexpr int YV = SPLIT ? 2 : 4;  // outputs per lane and column tile
     float *sc = reinterpret_cast<float *>(smem + lay.o_sc);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -304,6 +307,19 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
             const uint32_t sb = lrow + slot * kQ4Stage;
             const uint4 *bst = bs + st * (8 * NT * 32);
             const uint8_t *wsp = ring + slot * kQ4Stage + 2048 + g * 16;
+            uint32_t sw[2][GS / 2 + (GS & 1)];  // the stage's scales of rows g and g + 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (GS == 8) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(wsp + 128 * h);
+                    sw[h][0] = q.x, sw[h][GS / 8] = q.y, sw[h][GS / 4] = q.z, sw[h][GS / 2 - 1] = q.w;
+                } else if (GS == 4) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(wsp + 128 * h);
+                    sw[h][0] = q.x, sw[h][GS / 2 - 1] = q.y;
+                } else {
+                    sw[h][0] = *reinterpret_cast<const uint32_t *>(wsp + 128 * h);
+                }
+            }
             float acc[NT][4];
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
@@ -312,12 +328,6 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = 2 * jj + h;
-                    if (c % GL == 0) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-                    }
                     const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1], v0 = w0 >> 8, v1 = w1 >> 8;
                     const uint32_t a0 = q4_pair<true>(w0, kc), a1 = q4_pair<true>(w1, kc), a2 = q4_pair<false>(w0, kc),
                                    a3 = q4_pair<false>(w1, kc), a4 = q4_pair<true>(v0, kc), a5 = q4_pair<true>(v1, kc),
@@ -325,13 +335,14 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint4 b = bst[(c * NT + n) * 32];
-                        mma_f16(acc[n], a0, a1, a2, a3, b.x, b.y);
-                        mma_f16(acc[n], a4, a5, a6, a7, b.z, b.w);
+                        if (c % GL == 0) mma_f16<false>(acc[n], a0, a1, a2, a3, b.x, b.y);
+                        else mma_f16<true>(acc[n], a0, a1, a2, a3, b.x, b.y);
+                        mma_f16<true>(acc[n], a4, a5, a6, a7, b.z, b.w);
                     }
                     if (c % GL == GL - 1) {
                         const int gi = c / GL;
-                        const float s0 = __half2float(*reinterpret_cast<const __half *>(wsp + 2 * gi));
-                        const float s1 = __half2float(*reinterpret_cast<const __half *>(wsp + 128 + 2 * gi));
+                        const float2 f0 = unpack2(sw[0][gi >> 1], __half()), f1 = unpack2(sw[1][gi >> 1], __half());
+                        const float s0 = gi & 1 ? f0.y : f0.x, s1 = gi & 1 ? f1.y : f1.x;
                         const float *p = sc + (st * (8 / GL) + gi) * TOK;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
