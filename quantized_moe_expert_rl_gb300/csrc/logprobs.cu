@@ -17,10 +17,11 @@
 // distinct and equal logits go to the lower index.  Only keys above a threshold are kept, in a buffer
 // that is cut back to its n best whenever it holds more than 128, by counting for every key the
 // larger ones.  A row's first tile sets the threshold: the CTA's 64 groups of 4 threads each publish
-// their largest key, and the n-th largest of the 64 bounds the tile's n-th largest from below, which
-// leaves at most n groups x 64 values.  Later tiles put their few survivors straight into the buffer,
-// without a barrier; every fourth tile the CTA meets, cuts the buffer back if need be, and if it
-// overflowed (rising logits) goes through those tiles again the first tile's way.
+// their largest logit, and the n-th largest of the 64 bounds the tile's n-th largest from below.  The
+// survivors (a few more than n) go into the buffer without a barrier; every fourth tile the CTA meets
+// and cuts the buffer back if need be.  If it overflowed (rising logits, masses of equal ones) the CTA
+// goes through those tiles again with the groups' largest keys, which are distinct, so that a tile
+// leaves at most n groups x 64 of them.
 #include <math.h>
 
 #include "qdot.cuh"
@@ -141,6 +142,25 @@ __device__ __noinline__ void lp_raise(LpShared &sh, unsigned long long m, int n)
     if ((threadIdx.x & 3) == 0 && rank == n - 1 && m > 0ull && m - 1ull > sh.thr) sh.thr = m - 1ull;
     cta_sync();
 }
+// The first tile's threshold: just below every key whose logit (as an order-preserving integer) reaches
+// the n-th largest of the groups' largest, m being this thread's.  Whole CTA; true where any thread brought
+// `pred` (nothing is raised then).
+__device__ __forceinline__ bool lp_first(LpShared &sh, uint32_t m, int n, bool pred) {
+    uint32_t *heads = reinterpret_cast<uint32_t *>(sh.heads);
+    m = max(m, __shfl_xor_sync(kFull, m, 1));
+    m = max(m, __shfl_xor_sync(kFull, m, 2));
+    const int group = threadIdx.x >> 2;
+    if ((threadIdx.x & 3) == 0) heads[group] = m;
+    if (cta_sync_or(pred)) return true;
+    int rank = 0;  // among equal heads the lower group comes first; 16 comparisons per lane
+#pragma unroll 4
+    for (int j = threadIdx.x & 3; j < 64; j += 4) rank += heads[j] > m || (heads[j] == m && j < group) ? 1 : 0;
+    rank += __shfl_xor_sync(kFull, rank, 1);
+    rank += __shfl_xor_sync(kFull, rank, 2);
+    if ((threadIdx.x & 3) == 0 && rank == n - 1) sh.thr = ((unsigned long long)m << 32) - 1ull;
+    cta_sync();
+    return false;
+}
 // After insertions by the whole CTA: cut the buffer back to its n best if it holds more than kLpKeep.
 __device__ __forceinline__ void lp_settle(LpShared &sh, int n) {
     cta_sync();
@@ -200,11 +220,10 @@ struct LpTile {
 
 // The cold parts are functions of their own, so that the tile loop keeps its registers.
 
-// Tiles t0, t0 + kLpTile, .. t1 into the buffer with the threshold raised tile by tile; from ring slot
-// `slot` (one tile), or 0 for the logits' own memory.  Whole CTA.  Rolled loops: this runs once per
-// piece of a row, and fetching straight code costs more than executing it.
+// Tiles t0, t0 + kLpTile, .. t1 into the buffer, from the logits' memory, with the threshold raised tile by
+// tile.  Whole CTA.
 template <typename E>
-__device__ __noinline__ void lp_robust(LpShared &sh, const E *x, int lo, int hi, int t0, int t1, int n, uint32_t slot) {
+__device__ __noinline__ void lp_robust(LpShared &sh, const E *x, int lo, int hi, int t0, int t1, int n) {
     using Tile = LpTile<E>;
     constexpr int EV = Tile::EV;
 #pragma unroll 1
@@ -216,8 +235,7 @@ __device__ __noinline__ void lp_robust(LpShared &sh, const E *x, int lo, int hi,
 #pragma unroll 1
             for (int j = 0; j < Tile::NV; ++j) {
                 const int i0 = tt + (j * kLpThreads + threadIdx.x) * EV;
-                const uint4 q = !(i0 >= lo && i0 + EV <= hi) ? Tile::edge(x, lo, hi, i0)
-                                : slot ? lds128(slot + j * kLpThreads * 16) : *reinterpret_cast<const uint4 *>(x + i0);
+                const uint4 q = i0 >= lo && i0 + EV <= hi ? *reinterpret_cast<const uint4 *>(x + i0) : Tile::edge(x, lo, hi, i0);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int k = 0; k < EV; ++k) {
@@ -321,8 +339,6 @@ __device__ __noinline__ void lp_piece_end(const LpArgs &a, LpShared &sh, int row
 // after it up to c1.
 __device__ __noinline__ void lp_cut_rows(const LpArgs &a, LpShared &sh, int r0, int r1) {
     const int tid = threadIdx.x, lane = tid & 31, n = a.n;
-    __threadfence();
-    cta_sync();
     const int k = (tid >> 5) & 1, r = k ? r1 : r0;  // warp 0 takes r0, warp 1 r1
     const long long at = (long long)(r < 0 ? 0 : r) * a.V;
     const int c0 = a.per_row ? r * a.per_row : (int)(at / a.run);
@@ -344,9 +360,11 @@ __device__ __noinline__ void lp_cut_rows(const LpArgs &a, LpShared &sh, int r0, 
     if (tid < 64) {
         int last = 0;
         if (r >= 0 && lane == 0) {
-            last = atomicAdd(a.done + c0, 1u) == (uint32_t)(c1 - c0);
+            // release what the CTA wrote (before its last barrier), acquire what the others did
+            uint32_t old;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.done + c0) : "memory");
+            last = old == (uint32_t)(c1 - c0);
             if (last) a.done[c0] = 0u;
-            __threadfence();
         }
         last = __shfl_sync(kFull, last, 0);
         if (last && total <= 64) {  // few keys: a warp ranks them by itself
@@ -553,7 +571,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const __grid_co
                     }
                 }
             }
-            if (n > 0 && t0 != begin) {
+            bool again = false;  // the first tile, with a NaN in it
+            if (n > 0 && t0 == begin) again = lp_first(sh, order_key(tm), n, nan);
+            if (n > 0 && !again) {
                 const unsigned long long thr = sh.thr;
                 const uint32_t th = (uint32_t)(thr >> 32);
                 if (nan || order_key(tm) >= th) {
@@ -577,24 +597,17 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const __grid_co
                 }
                 __syncwarp();  // rejoin the warp (see cta_sync): here, where every lane comes by
             }
-            if (n > 0 && t0 == begin) lp_robust(sh, x, lo, hi, t0, t0, n, slot);
             slot = slot == ring + (kLpDepth - 1) * kSlot ? ring : slot + kSlot;
             issue();  // into the slot just read
             if (n == 0) continue;
-            if (t0 == begin) {
-                before = sh.count;
-                tb = t0 + kLpTile;
-                cta_sync();
-                continue;
-            }
-            if (++since == kLpTurn || t0 + kLpTile >= hi) {
+            if (++since == kLpTurn || t0 == begin || t0 + kLpTile >= hi) {
                 cta_sync();
                 const int cnt = sh.count;
                 cta_sync();  // everybody has read the count
-                if (cnt > kLpCap) {  // again, from the tiles' memory
+                if (again || cnt > kLpCap) {  // again, from the tiles' memory
                     if (tid == 0) sh.count = before;
                     cta_sync();
-                    lp_robust(sh, x, lo, hi, tb, t0, n, 0u);
+                    lp_robust(sh, x, lo, hi, tb, t0, n);
                 } else if (cnt > kLpKeep) {
                     lp_sort(sh, cnt, n, true);
                 }
