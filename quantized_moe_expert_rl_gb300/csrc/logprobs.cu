@@ -15,7 +15,7 @@
 //
 // Top n.  A candidate is a 64-bit key, order-preserving logit above ~index, so that keys are
 // distinct and equal logits go to the lower index.  Only keys above a threshold are kept, in a buffer
-// that is cut back to its n best whenever it holds more than 128, by counting for every key the
+// that is cut back to its n best whenever it holds more than 64, by counting for every key the
 // larger ones.  A row's first tile sets the threshold: the CTA's 64 groups of 4 threads each publish
 // their largest logit, and the n-th largest of the 64 bounds the tile's n-th largest from below.  The
 // survivors (a few more than n) go into the buffer without a barrier; every fourth tile the CTA meets
@@ -38,7 +38,7 @@ constexpr int kLpMaxCtas = 3 * 152;
 constexpr int kLpMaxPieces = 64;                    // of one row
 constexpr int kLpDepth = 3;                         // tiles on their way
 constexpr int kLpTurn = 4;                          // tiles between two meetings of the CTA
-constexpr int kLpKeep = 128;                        // the buffer is cut back beyond this many
+constexpr int kLpKeep = 64;                         // the buffer is cut back beyond this many
 constexpr int kLpCap = kLpKeep + 64 * kLpMaxN;      // and never holds more than this
 constexpr float kLog2e = 1.4426950408889634f;
 

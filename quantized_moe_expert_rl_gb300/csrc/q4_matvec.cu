@@ -45,6 +45,7 @@ struct Q4Args {
     const float *xs;
     void *y;
     int N, K, T, group, xdt, ydt, acc;
+    uint32_t inv;  // 2^32 / (octets of a padded row), rounded up: i / KO = umulhi(i, inv) for the i that occur
     int KC, W, stages, wide;  // stages of 256 values per row, warps per tile, ring depth, scales by wide copies
 };
 
@@ -118,16 +119,24 @@ __device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *
     if (KIND != kQ4F8) {  // the largest magnitude of every row, as an integer (a NaN or infinity ranks highest)
         if (threadIdx.x < TOK) top[threadIdx.x] = 0u;
         __syncthreads();
-#pragma unroll 2
-        for (int i = threadIdx.x; i < a.T * KO; i += kQ4Threads) {  // KO is a multiple of 32: whole warps
-            const int tok = i / KO, o = i - tok * KO;
-            float v[8];
-            q4_load_x(a, tok, o, v);
-            uint32_t mb = 0u;
+#pragma unroll 1
+        for (int i0 = threadIdx.x; i0 < a.T * KO; i0 += 4 * kQ4Threads) {  // four loads in flight
+            float v[4][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[j]) & 0x7fffffffu);
-            mb = __reduce_max_sync(kFull, mb);
-            if (lane == 0) atomicMax(top + tok, mb);
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kQ4Threads, tok = (int)__umulhi((uint32_t)i, a.inv);
+                q4_load_x(a, tok, i - tok * KO, v[u]);  // (zeros past the last token)
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int tok = (int)__umulhi((uint32_t)(i0 + u * kQ4Threads), a.inv);  // KO is a multiple of 32: one per warp
+                uint32_t mb = 0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(v[u][j]) & 0x7fffffffu);
+                mb = __reduce_max_sync(kFull, mb);
+                if (lane == 0 && tok < a.T) atomicMax(top + tok, mb);
+            }
+            __syncwarp();
         }
         __syncthreads();
         if (threadIdx.x < TOK) {
@@ -137,30 +146,40 @@ __device__ __forceinline__ void q4_stage_x(const Q4Args &a, uint8_t *bs, float *
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < TOK * KO; i += kQ4Threads) {
-        const int tok = i / KO, o = i - tok * KO;
-        float v[8];
-        q4_load_x(a, tok, o, v);
-        uint8_t *at = bs + ((size_t)(o >> 2) * NT * 8 + (KIND == kQ4Split ? 2 * tok : tok)) * 64 + (o & 3) * 16;
-        if (KIND != kQ4F8) {
-            const float mult = 1.0f / sc[tok];  // a power of two: exact
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < TOK * KO; i0 += 4 * kQ4Threads) {
+        float x[4][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= mult;
-        } else if ((8 * o) % a.group == 0) {
-            sc[(8 * o / a.group) * TOK + tok] = tok < a.T && 8 * o < a.K ? a.xs[(size_t)tok * (a.K / a.group) + 8 * o / a.group] : 0.f;
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kQ4Threads, tok = (int)__umulhi((uint32_t)i, a.inv);
+            q4_load_x(a, tok, i - tok * KO, x[u]);
         }
-        if (KIND == kQ4Split) {
-            float lo[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float hi = __half2float(__float2half_rn(v[j]));
-                lo[j] = v[j] - hi;
-                v[j] = hi;
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kQ4Threads, tok = (int)__umulhi((uint32_t)i, a.inv), o = i - tok * KO;
+            if (tok >= TOK) break;
+            float (&v)[8] = x[u];
+            uint8_t *at = bs + ((size_t)(o >> 2) * NT * 8 + (KIND == kQ4Split ? 2 * tok : tok)) * 64 + (o & 3) * 16;
+            if (KIND != kQ4F8) {
+                const float mult = 1.0f / sc[tok];  // a power of two: exact
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= mult;
+            } else if ((8 * o) % a.group == 0) {
+                sc[(8 * o / a.group) * TOK + tok] = tok < a.T && 8 * o < a.K ? a.xs[(size_t)tok * (a.K / a.group) + 8 * o / a.group] : 0.f;
             }
-            *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
-            *reinterpret_cast<uint4 *>(at + 64) = q4_fragment(lo);
-        } else {
-            *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
+            if (KIND == kQ4Split) {
+                float lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float hi = __half2float(__float2half_rn(v[j]));
+                    lo[j] = v[j] - hi;
+                    v[j] = hi;
+                }
+                *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
+                *reinterpret_cast<uint4 *>(at + 64) = q4_fragment(lo);
+            } else {
+                *reinterpret_cast<uint4 *>(at) = q4_fragment(v);
+            }
         }
     }
 }
@@ -476,6 +495,7 @@ extern "C" rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t
         a.ydt = y_dtype;
         a.acc = accumulate != 0;
         a.KC = (K + 255) / 256;
+        a.inv = (uint32_t)(((1ull << 32) + a.KC * 32 - 1) / (a.KC * 32));
         a.W = p.W;
         a.stages = p.stages;
         a.wide = K % 256 == 0;
