@@ -124,6 +124,18 @@ def test_add_rmsnorm_non_finite_stays_in_its_row(L):
     assert s[0].isfinite().all() and s[3].isfinite().all()
 
 
+def test_add_rmsnorm_in_place_of_either_input(L):
+    x, r = randn(9, 1024, seed=1, dtype=torch.bfloat16), randn(9, 1024, seed=2, dtype=torch.bfloat16)
+    xn, xo = torch.empty_like(x), torch.empty_like(x)
+    L.rl_add_rmsnorm(x, 9, 1024, 1e-6, res=r, x_out=xo, xn=xn)
+    a, b = x.clone(), r.clone()
+    L.rl_add_rmsnorm(a, 9, 1024, 1e-6, res=b, x_out=a, xn=b)
+    assert torch.equal(a, xo) and torch.equal(b, xn)
+    a, b = x.clone(), r.clone()
+    L.rl_add_rmsnorm(a, 9, 1024, 1e-6, res=b, x_out=b, xn=a)
+    assert torch.equal(b, xo) and torch.equal(a, xn)
+
+
 # ---- rl_q4_matvec -------------------------------------------------------------------------
 def q4_case(N, K, T, group, xt, seed=0):
     g = torch.Generator().manual_seed(seed)
@@ -307,6 +319,38 @@ def test_logprobs_unaligned_rows_and_shared_workspace(L):
         check_lp(lp_run(L, x, t, n, ws), x, t, n)
 
 
+def test_logprobs_each_output_alone(L):
+    """Any of the outputs may be left out; the others keep their bits."""
+    for T, V in ((3, 9001), (300, 20011)):
+        x = 3 * randn(T, V, seed=V)
+        t = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+        full = lp_run(L, x, t, 5)
+        ws = torch.zeros(L.rl_logprobs_workspace_bytes(T, V, 5), dtype=torch.uint8, device="cuda")
+        lp, en = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        ids, top = torch.empty(T, 5, dtype=torch.int32, device="cuda"), torch.empty(T, 5, device="cuda")
+        L.rl_logprobs(x, T, V, t, lp, None, 0, None, None, ws, ws.numel())
+        L.rl_logprobs(x, T, V, None, None, en, 0, None, None, ws, ws.numel())
+        L.rl_logprobs(x, T, V, None, None, None, 5, ids, top, ws, ws.numel())
+        assert torch.equal(lp, full["logprob"]) and torch.equal(en, full["entropy"])
+        assert torch.equal(ids, full["ids"]) and torch.equal(top, full["top"])
+
+
+def test_logprobs_masked_vocabulary(L):
+    """Most of every row masked, by -inf and by the type's lowest value, in 16 bits too."""
+    T, V, n = 70, 30011, 8
+    for dt in TYPES.values():
+        x = (2 * randn(T, V, seed=8)).to(dt)
+        x[:, 100:] = -math.inf
+        x[1::2, 100:] = torch.finfo(dt).min
+        t = torch.randint(0, 100, (T,), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+        o = lp_run(L, x, t, n)
+        small = lp_run(L, x[:, :100].contiguous(), t, n)
+        assert torch.equal(o["ids"], small["ids"])
+        # the masked values add nothing, so that only the order of the sums differs
+        for k in ("logprob", "entropy", "top"):
+            assert torch.all((o[k] - small[k]).abs() <= 300 * U * (1 + small[k].abs())), k
+
+
 # ---- moe_decode_tokens --------------------------------------------------------------------
 TINY = synth.WORKLOADS["tiny"]
 SHAPES = {
@@ -318,6 +362,8 @@ SHAPES = {
     "wide_inter": replace(TINY, hidden=1024, n_experts=20, top_k=8, inter=2048),
     "most_pairs": replace(TINY, hidden=512, n_experts=40, top_k=16, inter=1024),
     "odd_experts": replace(TINY, n_experts=157, top_k=5, inter=256),
+    "widest": replace(TINY, hidden=2048, n_experts=12, top_k=8, inter=2048),
+    "biased": replace(TINY, n_experts=64, zipf_s=1.1),
 }
 
 
@@ -327,7 +373,7 @@ class Layer:
     def __init__(self, w):
         from quantized_moe_expert_rl_gb300 import engine
         self.engine, self.w = engine, w
-        self.m = engine.Model(w)
+        self.m = engine.Model(w, slot_perm=True)
         self.o = OracleSide(self.m)
 
     def run(self, L, x, stacked, y=None, accumulate=0, eps=None, ws=None):
@@ -349,7 +395,7 @@ class Layer:
         xn = oracle.rmsnorm(xo) if stacked else xo
         rep = {}
         r = check_route(lg.cpu().numpy(), b.ids[0].cpu().numpy(), b.weights[0].cpu().numpy(), u64(b.slots[0]),
-                        oracle.router_logits(xn, self.o.router(0)), self.o.table_row(0), self.w.top_k, 0, rep)
+                        oracle.router_logits(xn, self.o.router(0), self.o.bias(0)), self.o.table_row(0), self.w.top_k, 0, rep)
         assert rep["near_ties"] == 0
         assert rel_l2(y.cpu().numpy(), self.o.experts(xn, r.ids, r.weights, r.slots)) <= REL_F32
         return b, y
@@ -466,6 +512,30 @@ def test_moe_tokens_misses_and_given_routing(L):
         assert torch.all(y == 7.0) and b.ctrl.tolist() == [NO_EARLY_OUT, bit]
         b.ctrl[1] = 0
         at.copy_(keep)
+
+
+def test_moe_tokens_given_routing_may_repeat_an_expert(L, small):
+    """The same expert twice in a token's list, as moe_decode takes it: both weights count."""
+    x = rows(TINY, 3, seed=14)
+    b, _, _ = small.run(L, x, False)
+    b.ids[0, 1, 2] = b.ids[0, 1, 0]
+    b.slots[0, 1, 2] = b.slots[0, 1, 0]
+    y = torch.empty_like(x)
+    small.engine.enqueue_tokens_layer(small.m, b, 0, x, y, stacked=False, routed=False)
+    torch.cuda.synchronize()
+    ref = small.o.experts(x.double().cpu().numpy(), b.ids[0].cpu().numpy(), b.weights[0].double().cpu().numpy(),
+                          u64(b.slots[0]))
+    assert b.ctrl.tolist() == [NO_EARLY_OUT, 0] and rel_l2(y.cpu().numpy(), ref) <= REL_F32
+
+
+def test_moe_tokens_norm_range_is_flagged(L, small):
+    """Beyond the fixed-point range of the RMSNorm's squares the call says so, as rl_route does."""
+    x = rows(TINY, 3, seed=15)
+    x[2] *= 1e4
+    b, _, _ = small.run(L, x, True)
+    assert b.ctrl.tolist() == [NO_EARLY_OUT, L.RL_DEVERR_RANGE]
+    b, _, _ = small.run(L, x, False)
+    assert b.ctrl.tolist() == [NO_EARLY_OUT, 0]
 
 
 def test_moe_tokens_nan_router_is_flagged(L, small):
