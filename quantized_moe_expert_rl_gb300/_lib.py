@@ -133,7 +133,7 @@ def _cuda():
 
 def _stream(s) -> int | None:
     if s is None:
-        device, raw = _cuda()
+        device, raw = _current or _cuda()
         return raw(device()) or None
     if isinstance(s, int):
         return s or None
@@ -262,17 +262,17 @@ def _sized(what: str, t, itemsize: int, numel: int) -> None:
 def _ptrs(*tensors):
     """Raw addresses of device tensors (None: NULL), all dense and on the current device, where the
     call will launch."""
-    device = _cuda()[0]()
+    device = (_current or _cuda())[0]()
     out = []
     for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if not t.is_contiguous():
-            raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
-        if t.get_device() != device:
+        elif t.get_device() != device:
             raise ValueError(f"tensor on {t.device} passed to a call on cuda:{device}")
-        out.append(t.data_ptr() or None)
+        elif not t.is_contiguous():
+            raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+        else:
+            out.append(t.data_ptr())
     return out
 
 

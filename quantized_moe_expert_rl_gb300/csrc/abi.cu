@@ -45,6 +45,7 @@ rl_status check_shape(const rl_moe_shape *shp) {
 // The attribute belongs to the kernel on the current device, so the cache is per device: a
 // process that drives several GPUs sets it once on each.
 rl_status allow_smem(const void *kernel, size_t bytes) {
+    if (bytes == 0) return RL_OK;
     static std::mutex mu;
     static std::map<std::pair<int, const void *>, size_t> done;
     int dev = 0;
