@@ -22,6 +22,12 @@
 // and cuts the buffer back if need be.  If it overflowed (rising logits, masses of equal ones) the CTA
 // goes through those tiles again with the groups' largest keys, which are distinct, so that a tile
 // leaves at most n groups x 64 of them.
+//
+// Measured back to back in a graph: 512 x 131072 f32 (268.5 MB, 39.6 us at the measured copy rate) 72 us
+// with the 20 best tokens, 54 us without any; 912 rows without any 73 us, 6.5 TB/s.  What is left are the
+// rows cut by the runs' ends (with 512 rows every CTA has two: two publications and a merge, about 10
+// us) and the insertions.  One row of 131072 takes 9.6 us, 16 rows of 100003 bf16 11.7 us: a chain of latencies
+// (launch, tile, first threshold, publication, merge).
 #include <math.h>
 
 #include "qdot.cuh"

@@ -17,9 +17,10 @@
 //      outputs exchanged through a third grid barrier, were no faster at 32 tokens and 3 us slower at 1.)
 // Work comes in rounds of units, a unit being 16 weight rows x 256 values (one block of every row).  In G
 // a computing warp has two units of a round, gate and up of the same rows and block, which share
-// the activations; in D it has one.  A G round's block sums go through one of four buffers to a finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
-// CTA takes a run of consecutive G tiles of equal weight, where a tile weighs one per two tokens of its
-// expert; an expert's activations then stay in registers over its tiles.
+// the activations; in D it has one.  A G round's block sums go through one of four buffers to a
+// finishing warp, which adds them and applies SwiGLU, so that no computing warp waits for another.  Every
+// CTA takes a run of consecutive G tiles of equal weight, where a tile weighs one per two tokens of
+// its expert; an expert's activations then stay in registers over its tiles.
 // For few tokens the launch is a chain of latencies, much of them the first fetch of straight code: a
 // combine unrolled to 16 experts took 8.5k cycles where the rolled loop takes 1.2k.  So what runs once
 // stays in rolled loops, and the codebook table and the expert tables are built while the first grid
@@ -34,6 +35,15 @@
 // carry it without loss, two tokens share the 8 columns of one MMA, and the products are exact
 // before the f32 sums.  On the CUDA cores the same dot needs two unpacking instructions and a packed FMA
 // per pair of weights (25 instructions per group against 13 here).
+//
+// Measured at hidden 2048, 512 experts, top-10, intermediate 512, back to back in a graph: 1 token 22.6 us
+// (12.3 MB, 1.8 us at the measured copy rate), 5 drafted tokens with 24 distinct experts 38.3 us
+// (23.8 MB, 3.5 us), 32 independent tokens with 240 distinct experts 153 us (199 MB, 29 us).  DRAM reads are
+// the router and every distinct expert once.  At 1 token two grid barriers take 10k of 42k cycles, router
+// 3k, selection 5k, list and first copies 4k, G 6k, D 5k.  At 32 tokens the table lookups alone (16
+// bytes of shared memory per 8 weights: 51 weights per clock and SM) are a third of the time, and issue
+// slots are 57% used.  For comparison: T calls of moe_decode_layer take 23 us each, the grouped prefill
+// path (half-precision operands) 58, 119, 201 and 306 us at 1, 5, 16 and 32 tokens.
 #include "decode_rows.cuh"
 #include "select.cuh"
 #include "stack_kernel.cuh"
