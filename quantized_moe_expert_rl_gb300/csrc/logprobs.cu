@@ -24,7 +24,7 @@
 // leaves at most n groups x 64 of them.
 //
 // Measured back to back in a graph: 512 x 131072 f32 (268.5 MB, 39.6 us at the measured copy rate) 72 us
-// with the 20 best tokens, 54 us without any; 912 rows without any 73 us, 6.5 TB/s.  What is left are the
+// with the 20 best tokens, 54 to 56 us without any; 912 rows without any 73 us, 6.5 TB/s.  What is left are the
 // rows cut by the runs' ends (with 512 rows every CTA has two: two publications and a merge, about 10
 // us) and the insertions.  One row of 131072 takes 9.6 us, 16 rows of 100003 bf16 11.7 us: a chain of latencies
 // (launch, tile, first threshold, publication, merge).

@@ -24,8 +24,8 @@
 // For few tokens the launch is a chain of latencies, much of them the first fetch of straight code: a
 // combine unrolled to 16 experts took 8.5k cycles where the rolled loop takes 1.2k.  So what runs once
 // stays in rolled loops, and the codebook table and the expert tables are built while the first grid
-// barrier is pending.  (Running the unit code dry there, to fetch it early, delayed the barrier by as
-// much as it saved; one copy of the unit code for both phases cost 2 us at 1 token and 15 at 32.)
+// barrier is pending.  (Running the unit code dry there, to fetch it early, cost 0.7 us at 1 token; one
+// copy of the unit code for both phases cost 2 us at 1 token and 15 at 32.)
 //
 // The matrix arithmetic.  A weight is d * (codebook value) * (sign): the codebook value is an
 // 8-bit integer, exact in bf16, so a group's 8 values are one 16-byte table entry whose signs are
@@ -37,13 +37,14 @@
 // per pair of weights (25 instructions per group against 13 here).
 //
 // Measured at hidden 2048, 512 experts, top-10, intermediate 512, back to back in a graph: 1 token 22.6 us
-// (12.3 MB, 1.8 us at the measured copy rate), 5 drafted tokens with 24 distinct experts 38.3 us
-// (23.8 MB, 3.5 us), 32 independent tokens with 240 distinct experts 153 us (199 MB, 29 us).  DRAM reads are
-// the router and every distinct expert once.  At 1 token two grid barriers take 10k of 42k cycles, router
-// 3k, selection 5k, list and first copies 4k, G 6k, D 5k.  At 32 tokens the table lookups alone (16
-// bytes of shared memory per 8 weights: 51 weights per clock and SM) are a third of the time, and issue
-// slots are 57% used.  For comparison: T calls of moe_decode_layer take 23 us each, the grouped prefill
-// path (half-precision operands) 58, 119, 201 and 306 us at 1, 5, 16 and 32 tokens.
+// (12.3 MB, 1.8 us at the measured copy rate), 5 drafted tokens with 22 to 24 distinct experts 38.3 us
+// (23.8 MB with 24, 3.5 us), 32 independent tokens with 233 to 240 distinct experts 153 us (199 MB with 240,
+// 29 us).  DRAM reads are the router and every distinct expert once.  At 1 token, of 41k cycles (clock64 of
+// one thread, instrumented): router 4k, first barrier 3k, selection 5.5k, list and first copies 5k, G 5.5k,
+// finishing and second barrier 9.5k, D and its first copies 7k, combine 1.4k.  At 32 tokens G takes 121k and
+// D 100k of 285k; shared loads (the table's above all) fill 35% of their pipe's slots, issue slots are 57%
+// used.  For comparison: T calls of moe_decode_layer take 21 to 23 us each, the grouped prefill path
+// (half-precision operands) 58, 119, 201 and 306 us at 1, 5, 16 and 32 tokens.
 #include "decode_rows.cuh"
 #include "select.cuh"
 #include "stack_kernel.cuh"

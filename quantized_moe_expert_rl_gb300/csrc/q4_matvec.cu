@@ -425,7 +425,7 @@ struct Q4Plan {
 
 // NT column tiles: as few as hold the tokens of the launch.  W warps share a tile where the tiles alone do not
 // fill every warp of the GPU (512 rows of 2048: 8 warps per tile); where they do, one warp per tile
-// was 3% faster than two and 6% than four on the 131072-row head (no partial sums to exchange).  Four
+// takes 29.6 us on the 131072-row head, two 31.5 and four 32.9 (no partial sums to exchange).  Four
 // column tiles leave no room for the partial sums, so they need tiles for every warp.
 bool q4_plan(int N, int K, int cols, int group, int kind, Q4Plan &p) {
     const int KC = (K + 255) / 256, tiles = (N + 15) / 16;
