@@ -394,7 +394,8 @@ rl_status moe_prefill_chunk_f32(const rl_moe_shape *shp, int32_t layer, int32_t 
  * enough for the largest, but must not overlap on the GPU); after RL_DEVERR_WAIT_TIMEOUT it must
  * be zero-filled again.  Bytes 64..71 are test knobs as in moe_decode_stack (a poll limit; a CTA
  * n - 1 that leaves before its first arrival), zero in normal use.  Cooperative launch, one CTA per
- * SM; it may be captured in a CUDA graph.
+ * SM, on a GPU of 128 SMs or more (RL_ERR_UNSUPPORTED on a smaller one); it may be captured in a CUDA
+ * graph.  RL_DEVERR_RANGE and RL_DEVERR_NAN are set as by rl_route.
  */
 #define RL_MAX_DECODE_TOKENS 32
 size_t moe_decode_tokens_workspace_bytes(const rl_moe_shape *shp, int32_t T);

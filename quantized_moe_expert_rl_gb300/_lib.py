@@ -259,6 +259,12 @@ def _sized(what: str, t, itemsize: int, numel: int) -> None:
         raise ValueError(f"{what}: {numel} items of {itemsize} bytes expected, got {t.dtype} {tuple(t.shape)}")
 
 
+def _holds(what: str, t, itemsize: int, numel: int) -> None:
+    """Refuses a buffer of another item size or of fewer items than a call reads or writes."""
+    if t is not None and (t.element_size() != itemsize or t.numel() < numel):
+        raise ValueError(f"{what}: {numel} items of {itemsize} bytes needed, got {t.dtype} {tuple(t.shape)}")
+
+
 def _ptrs(*tensors):
     """Raw addresses of device tensors (None: NULL), all dense and on the current device, where the
     call will launch."""
@@ -285,6 +291,20 @@ def moe_decode_tokens_workspace_bytes(shape, T) -> int:
 
 def moe_decode_tokens(shape, layer, T, x, norm_eps, w_router, bias, residency, codebook, ids, weights, slots, miss,
                       ctrl, logits_out, y, accumulate, ws, ws_bytes, stream=None):
+    H, E, TK, layers = shape.hidden, shape.n_experts, T * shape.top_k, shape.n_layers
+    _holds("x", x, 4, T * H)
+    _holds("w_router", w_router, 4, E * H)
+    _holds("bias", bias, 4, E)
+    _holds("residency", residency, 8, layers * E)
+    _holds("codebook", codebook, 1, 2048)
+    _holds("ids", ids, 4, TK)
+    _holds("weights", weights, 4, TK)
+    _holds("slots", slots, 8, TK)
+    _holds("miss", miss, 4, layers)
+    _holds("ctrl", ctrl, 4, 2)
+    _holds("logits_out", logits_out, 4, T * E)
+    _holds("y", y, 4, T * H)
+    _holds("ws", ws, 1, ws_bytes)
     x, w, bias, res, cb, ids, wt, slots, miss, ctrl, lg, y, ws = _ptrs(x, w_router, bias, residency, codebook, ids,
                                                                        weights, slots, miss, ctrl, logits_out, y, ws)
     _check("moe_decode_tokens", load().moe_decode_tokens(
@@ -336,6 +356,7 @@ def rl_logprobs(logits, T, V, targets, logprob, entropy, top_n, top_ids, top_log
     _sized("entropy", entropy, 4, T)
     _sized("top_ids", top_ids, 4, T * top_n)
     _sized("top_logprob", top_logprob, 4, T * top_n)
+    _holds("ws", ws, 1, ws_bytes)
     x, targets, logprob, entropy, ids, top, ws = _ptrs(logits, targets, logprob, entropy, top_ids, top_logprob, ws)
     _check("rl_logprobs", load().rl_logprobs(x, dt, T, V, targets, logprob, entropy, top_n, ids, top, ws, ws_bytes,
                                              _stream(stream)))

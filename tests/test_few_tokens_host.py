@@ -125,6 +125,39 @@ def test_binding_checks_types_and_sizes():
         L.rl_logprobs(x, 2, 256, torch.zeros(2, dtype=torch.int64), y, None, 0, None, None, None, 0)
 
 
+@pytest.mark.parametrize("what, small", [
+    ("x", lambda t: t[:2]), ("y", lambda t: t[:2]), ("x", lambda t: t.half()), ("w_router", lambda t: t[:-1]),
+    ("bias", lambda t: t[:-1]), ("residency", lambda t: t[:0]), ("codebook", lambda t: t[:-1]),
+    ("ids", lambda t: t[:2]), ("weights", lambda t: t[:2]), ("slots", lambda t: t.int()), ("miss", lambda t: t[:0]),
+    ("ctrl", lambda t: t[:1]), ("logits_out", lambda t: t[:2]), ("ws", lambda t: t[:-1])])
+def test_binding_checks_the_buffers_of_a_layer(what, small):
+    """A step of fewer rows than the buffers' tokens, or any buffer too small for the call, is refused before
+    the library sees its address."""
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    sh, T = L.RlShape.of(256, 8, 2, 256, 1), 3
+    i32, i64 = torch.int32, torch.int64
+    b = dict(x=torch.zeros(T, 256), w_router=torch.zeros(8, 256), bias=torch.zeros(8),
+             residency=torch.zeros(1, 8, dtype=i64), codebook=torch.zeros(256, 8, dtype=torch.int8),
+             ids=torch.zeros(T, 2, dtype=i32), weights=torch.zeros(T, 2), slots=torch.zeros(T, 2, dtype=i64),
+             miss=torch.zeros(1, dtype=i32), ctrl=torch.zeros(2, dtype=i32), logits_out=torch.zeros(T, 8),
+             y=torch.zeros(T, 256), ws=torch.zeros(L.moe_decode_tokens_workspace_bytes(sh, T), dtype=torch.uint8))
+    size = b["ws"].numel()
+    b[what] = small(b[what])
+    with pytest.raises(ValueError, match=f"^{what}:"):
+        L.moe_decode_tokens(sh, 0, T, b["x"], -1.0, b["w_router"], b["bias"], b["residency"], b["codebook"], b["ids"],
+                            b["weights"], b["slots"], b["miss"], b["ctrl"], b["logits_out"], b["y"], 0, b["ws"], size)
+
+
+def test_binding_checks_the_workspace_of_logprobs():
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    x, size = torch.zeros(2, 256), L.rl_logprobs_workspace_bytes(2, 256, 0)
+    with pytest.raises(ValueError, match="^ws:"):
+        L.rl_logprobs(x, 2, 256, None, None, torch.zeros(2), 0, None, None,
+                      torch.zeros(size - 1, dtype=torch.uint8), size)
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_pack_q4(group):
     """Values come back within half a step of their group's scale (rounded to half precision, 2^-11
