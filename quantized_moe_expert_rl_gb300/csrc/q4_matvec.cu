@@ -27,7 +27,7 @@
 //
 // Measured back to back in a graph: 131072 x 2048, groups of 128, one e4m3 row 29.4 us (138.9 MB, 4.7 TB/s,
 // 70% of the measured copy rate); 100003 x 2048, groups of 32, 16 bf16 rows 38.4 us (47%); 512 x 2048, one
-// row 4.8 us (latency).  The large ones are bound by instruction issue (60% of the slots used, 37
+// row 4.2 us (latency).  The large ones are bound by instruction issue (60% of the slots used, 37
 // instructions per 512 weights and column tile, 18 of them the conversion); DRAM reads are the weights once.
 #include "qdot.cuh"
 #include "row_types.cuh"
@@ -277,10 +277,20 @@ __device__ __forceinline__ void q4_store(const Q4Args &a, int tok, int row, floa
 
 // NT: column tiles of 8; GL: 32-value chunks per group
 template <int NT, int KIND, int GL>
-__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args a, const Q4Layout lay) {
+__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args call, const Q4Layout lay) {
     constexpr bool SPLIT = KIND == kQ4Split;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int TOK = NT * (SPLIT ? 4 : 8);
+    // CTA row blockIdx.y takes TOK tokens of its own
+    Q4Args a = call;
+    if (blockIdx.y) {
+        const int t0 = blockIdx.y * TOK;
+        a.x = static_cast<const uint8_t *>(call.x) + (size_t)t0 * call.K * dtype_bytes(call.xdt);
+        if (KIND == kQ4F8) a.xs = call.xs + (size_t)t0 * (call.K / call.group);
+        a.y = static_cast<uint8_t *>(call.y) + (size_t)t0 * call.N * dtype_bytes(call.ydt);
+        a.T -= t0;
+    }
+    if (a.T > TOK) a.T = TOK;
     constexpr int GS = 8 / GL;         // groups per stage: 8, 4, 2
     constexpr int YV = SPLIT ? 2 : 4;  // outputs per lane and column tile
     float *sc = reinterpret_cast<float *>(smem + lay.o_sc);
@@ -445,7 +455,8 @@ bool q4_plan(int N, int K, int cols, int group, int kind, Q4Plan &p) {
 template <int NT, int KIND>
 rl_status launch_q4(const Q4Args &a, const Q4Layout &lay, cudaStream_t s) {
     const int tiles = (a.N + 15) / 16, sms = sm_count();
-    const dim3 grid(tiles < sms ? tiles : sms), block(kQ4Threads);
+    const int tok = NT * (KIND == kQ4Split ? 4 : 8);
+    const dim3 grid(tiles < sms ? tiles : sms, (a.T + tok - 1) / tok), block(kQ4Threads);
     if (a.group == 32) return launch_pdl(q4_kernel<NT, KIND, 1>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
     if (a.group == 64) return launch_pdl(q4_kernel<NT, KIND, 2>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
     return launch_pdl(q4_kernel<NT, KIND, 4>, grid, block, lay.total, s, "rl_q4_matvec", a, lay);
@@ -495,7 +506,12 @@ extern "C" rl_status rl_q4_matvec(const uint8_t *w, const void *w_scale, int32_t
         a.y = static_cast<uint8_t *>(y) + (size_t)t0 * N * dtype_bytes(y_dtype);
         a.N = N;
         a.K = K;
-        a.T = T - t0 < most ? T - t0 : most;
+        // All full column groups in one launch (64 f32 rows: 512 x 2048 takes 11.7 us, with a launch per group
+        // 44.4; 20000 x 2048 78.5 and 94.7).  The rest joins it where the tiles leave SMs idle; a larger
+        // matrix takes the rest with fewer columns (100003 x 2048, 40 bf16 rows: 85.8 us, joined 109).
+        const int rest = T - t0, full = rest / most * most;
+        a.T = rest < most || (N + 15) / 16 < sm_count() ? rest : full;
+        if (a.T > most * 65535) a.T = most * 65535;
         a.group = group;
         a.xdt = x_dtype;
         a.ydt = y_dtype;

@@ -9,7 +9,7 @@
 
 namespace rl {
 
-inline size_t dtype_bytes(int dt) { return dt == RL_F32 ? 4 : dt == RL_F8_E4M3 ? 1 : 2; }
+__host__ __device__ inline size_t dtype_bytes(int dt) { return dt == RL_F32 ? 4 : dt == RL_F8_E4M3 ? 1 : 2; }
 
 __device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));

@@ -201,6 +201,18 @@ def test_q4_matvec(L, N, K, T, group, xt):
     assert torch.all((y.double() - 2 * first.double()).abs() <= 2 * first.double().abs() * U)
 
 
+@pytest.mark.parametrize("N,K,T,group", [(3000, 256, 75, 64), (2431, 512, 64, 128), (2433, 512, 65, 128), (40, 128, 129, 32)])
+@pytest.mark.parametrize("xt", ["f8", "f32", "bf16"])
+def test_q4_matvec_many_rows(L, N, K, T, group, xt):
+    """Column groups that share a launch, with and without a rest, on both sides of 152 tiles."""
+    w, ws, x, xs = q4_case(N, K, T, group, xt, seed=N)
+    guard = torch.full((T * N + 64,), 3.0, device="cuda")
+    y = guard[:T * N].view(T, N)
+    L.rl_q4_matvec(w, ws, x, y, T, N, K, group, x_scale=xs)
+    check_q4(y, *q4_ref(w, ws, x, xs, group), K, group, xt)
+    assert torch.all(guard[T * N:] == 3.0)
+
+
 def test_q4_matvec_extremes(L):
     """Smallest and largest nibbles, activations from 1e-38 to 1e30, zero rows and a token with a NaN
     beside healthy ones."""
