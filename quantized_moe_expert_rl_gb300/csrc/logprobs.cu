@@ -373,6 +373,7 @@ __device__ __noinline__ void lp_cut_rows(const LpArgs &a, LpShared &sh, int r0, 
             if (last) a.done[c0] = 0u;
         }
         last = __shfl_sync(kFull, last, 0);
+        __syncwarp();  // lane 0's acquire holds for the loads of every lane (a shuffle orders no memory)
         if (last && total <= 64) {  // few keys: a warp ranks them by itself
             unsigned long long *cand = sh.cand + k * 64;
             unsigned long long key[2];

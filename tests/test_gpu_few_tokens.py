@@ -363,6 +363,28 @@ def test_logprobs_masked_vocabulary(L):
             assert torch.all((o[k] - small[k]).abs() <= 300 * U * (1 + small[k].abs())), k
 
 
+@pytest.mark.parametrize("T,V,n", [(1, 250001, 1), (7, 250001, 1), (40, 12289, 16), (3, 9001, 20), (500, 20011, 5)])
+def test_logprobs_merges_what_the_other_pieces_published(L, T, V, n):
+    """Rows in pieces that one warp merges (at most 64 keys), call after call in one workspace without a wait
+    between them: a merge that reads a piece before its CTA's publication is ordered sees the other input's
+    triple or keys of the call before."""
+    xs = [3 * randn(T, V, seed=V + i) - 5 * i for i in range(2)]
+    t = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+    ws = torch.zeros(L.rl_logprobs_workspace_bytes(T, V, n), dtype=torch.uint8, device="cuda")
+    want = [lp_run(L, x, t, n) for x in xs]
+    for i in range(2):
+        check_lp(want[i], xs[i], t, n)
+    outs = [dict(logprob=torch.empty(T, device="cuda"), entropy=torch.empty(T, device="cuda"),
+                 ids=torch.empty(T, n, dtype=torch.int32, device="cuda"), top=torch.empty(T, n, device="cuda"))
+            for _ in range(100)]
+    for i, o in enumerate(outs):
+        L.rl_logprobs(xs[i % 2], T, V, t, o["logprob"], o["entropy"], n, o["ids"], o["top"], ws, ws.numel())
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        for k in o:
+            assert torch.equal(o[k], want[i % 2][k]), (i, k)
+
+
 # ---- moe_decode_tokens --------------------------------------------------------------------
 TINY = synth.WORKLOADS["tiny"]
 SHAPES = {
