@@ -241,7 +241,7 @@ def enqueue_decode_token_fused(model: Model, b: DecodeBuffers, x_in: torch.Tenso
 
 @dataclass
 class TokensBuffers:
-    """Buffers of a step of up to `T` tokens through every layer (moe_decode_tokens)."""
+    """Buffers of a step of `T` tokens through every layer (moe_decode_tokens)."""
     ids: torch.Tensor        # [L][T][K] int32
     weights: torch.Tensor    # [L][T][K] f32
     slots: torch.Tensor      # [L][T][K] u64 (as int64)
@@ -263,12 +263,24 @@ class TokensBuffers:
             ws=torch.zeros(L.moe_decode_tokens_workspace_bytes(model.shape, T), dtype=torch.uint8, device=d))
 
 
+def _step_tokens(model: Model, b: TokensBuffers, x: torch.Tensor, y: torch.Tensor) -> int:
+    """The number of tokens of a step, x [T][H] to y [T][H].  Refuses rows that the buffers were not made
+    for (the layers would pass them by) and an x that is not y's size (copy_ would spread one row)."""
+    if x.dim() != 2 or x.shape[1] != model.w.hidden or y.shape != x.shape:
+        raise ValueError(f"x of shape {tuple(x.shape)}, y of shape {tuple(y.shape)}: "
+                         f"[tokens][{model.w.hidden}] expected of both")
+    T = x.shape[0]
+    if T != b.ids.shape[1]:
+        raise ValueError(f"a step of {T} tokens: the buffers were made for {b.ids.shape[1]}")
+    return T
+
+
 def enqueue_tokens_layer(model: Model, b: TokensBuffers, layer: int, x: torch.Tensor, y: torch.Tensor,
                          stacked: bool, routed: bool = True, logits: torch.Tensor | None = None) -> None:
-    """One layer for the b.ids.shape[1] tokens x [T][H], router and experts in ONE launch:
+    """One layer for the tokens x [T][H], router and experts in ONE launch:
     stacked: y = x + MoE(RMSNorm(x)) in place (y is x), else y = MoE(x).  routed=False runs the
     experts with the ids and weights b holds (after a fill and rl_resolve_slots)."""
-    T = b.ids.shape[1]
+    T = _step_tokens(model, b, x, y)
     L.moe_decode_tokens(model.shape, layer, T, x, EPS if stacked else -1.0, model.routers[layer] if routed else None,
                         None if model.bias is None else model.bias[layer], model.table, model.codebook, b.ids[layer],
                         b.weights[layer], b.slots[layer], b.miss, b.ctrl, logits, y, int(stacked), b.ws, b.ws.numel())
@@ -278,6 +290,7 @@ def enqueue_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out: to
     """Stacked decode of a few tokens, one launch per layer: y_out = x_in, then for layers
     [layer0, L) y_out += MoE(RMSNorm(y_out)).  A layer in which some token selects an absent
     expert raises the flag and later layers do nothing (run_bounded_tokens fills and resumes)."""
+    _step_tokens(model, b, x_in, y_out)
     if y_out.data_ptr() != x_in.data_ptr():
         y_out.copy_(x_in)
     for l in range(layer0, model.L):
@@ -299,7 +312,7 @@ def pack_q4(weight: torch.Tensor, group: int = 128) -> tuple[torch.Tensor, torch
 @dataclass
 class Head:
     """The end of a verification step: final RMSNorm with gain into 8 bits, an output head in 4
-    bits, log probabilities.  Buffers for up to T tokens."""
+    bits, log probabilities.  Buffers for T tokens."""
     w: torch.Tensor            # uint8 [V][H / 2]
     scale: torch.Tensor        # half [V][H / group]
     gain: torch.Tensor | None  # f32 [H]
@@ -331,8 +344,12 @@ def enqueue_verify(model: Model, b: TokensBuffers, head: Head, x_in: torch.Tenso
     """A few tokens through every layer and the output head: y_out as enqueue_tokens, then
     head.logits = head(RMSNorm(y_out)) and the log probabilities of `targets` (int32 [T]), the
     entropies and the most probable tokens.  Valid when b.ctrl still reads (RL_NO_EARLY_OUT, 0)."""
-    T, H = x_in.shape
+    T, H = _step_tokens(model, b, x_in, y_out), model.w.hidden
     V = head.logits.shape[1]
+    if head.q.shape != (T, H):
+        raise ValueError(f"a step of {T} tokens: the head was made for {tuple(head.q.shape)}")
+    if targets.dtype != torch.int32 or targets.numel() != T:
+        raise ValueError(f"targets: {T} int32 values expected, got {targets.dtype} {tuple(targets.shape)}")
     enqueue_tokens(model, b, x_in, y_out)
     L.rl_add_rmsnorm(y_out, T, H, EPS, gain=head.gain, q=head.q, scale=head.q_scale, group=head.group)
     L.rl_q4_matvec(head.w, head.scale, head.q, head.logits, T, V, H, head.group, x_scale=head.q_scale)
@@ -423,7 +440,7 @@ def run_bounded_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out
     token of layer f selects an absent expert the flag stops the chain with y_out = x_f, the host
     fills the layer's missing experts, re-resolves the slots, runs the layer with the ids and
     weights the GPU selected, and goes on at f + 1.  The caller zeroes b.miss; b.ctrl is reset here."""
-    T = b.ids.shape[1]
+    T = _step_tokens(model, b, x_in, y_out)
     b.ctrl.copy_(torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32))
     y_out.copy_(x_in)
     st = DecodeStats([], [], 0, 0)
