@@ -241,7 +241,8 @@ def enqueue_decode_token_fused(model: Model, b: DecodeBuffers, x_in: torch.Tenso
 
 @dataclass
 class TokensBuffers:
-    """Buffers of a step of `T` tokens through every layer (moe_decode_tokens)."""
+    """Buffers of a step of up to `T` tokens through every layer (moe_decode_tokens); a smaller step
+    uses the first rows of each layer's."""
     ids: torch.Tensor        # [L][T][K] int32
     weights: torch.Tensor    # [L][T][K] f32
     slots: torch.Tensor      # [L][T][K] u64 (as int64)
@@ -264,14 +265,14 @@ class TokensBuffers:
 
 
 def _step_tokens(model: Model, b: TokensBuffers, x: torch.Tensor, y: torch.Tensor) -> int:
-    """The number of tokens of a step, x [T][H] to y [T][H].  Refuses rows that the buffers were not made
-    for (the layers would pass them by) and an x that is not y's size (copy_ would spread one row)."""
+    """The number of tokens of a step, x [T][H] to y [T][H].  Refuses more rows than the buffers hold and
+    an x that is not y's size (copy_ would spread one row)."""
     if x.dim() != 2 or x.shape[1] != model.w.hidden or y.shape != x.shape:
         raise ValueError(f"x of shape {tuple(x.shape)}, y of shape {tuple(y.shape)}: "
                          f"[tokens][{model.w.hidden}] expected of both")
     T = x.shape[0]
-    if T != b.ids.shape[1]:
-        raise ValueError(f"a step of {T} tokens: the buffers were made for {b.ids.shape[1]}")
+    if T > b.ids.shape[1]:
+        raise ValueError(f"a step of {T} tokens: the buffers hold {b.ids.shape[1]}")
     return T
 
 
@@ -282,8 +283,9 @@ def enqueue_tokens_layer(model: Model, b: TokensBuffers, layer: int, x: torch.Te
     experts with the ids and weights b holds (after a fill and rl_resolve_slots)."""
     T = _step_tokens(model, b, x, y)
     L.moe_decode_tokens(model.shape, layer, T, x, EPS if stacked else -1.0, model.routers[layer] if routed else None,
-                        None if model.bias is None else model.bias[layer], model.table, model.codebook, b.ids[layer],
-                        b.weights[layer], b.slots[layer], b.miss, b.ctrl, logits, y, int(stacked), b.ws, b.ws.numel())
+                        None if model.bias is None else model.bias[layer], model.table, model.codebook,
+                        b.ids[layer, :T], b.weights[layer, :T], b.slots[layer, :T], b.miss, b.ctrl, logits, y,
+                        int(stacked), b.ws, b.ws.numel())
 
 
 def enqueue_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out: torch.Tensor, layer0: int = 0) -> None:
@@ -312,7 +314,7 @@ def pack_q4(weight: torch.Tensor, group: int = 128) -> tuple[torch.Tensor, torch
 @dataclass
 class Head:
     """The end of a verification step: final RMSNorm with gain into 8 bits, an output head in 4
-    bits, log probabilities.  Buffers for T tokens."""
+    bits, log probabilities.  Buffers for up to T tokens; a smaller step uses their first rows."""
     w: torch.Tensor            # uint8 [V][H / 2]
     scale: torch.Tensor        # half [V][H / group]
     gain: torch.Tensor | None  # f32 [H]
@@ -343,19 +345,20 @@ def enqueue_verify(model: Model, b: TokensBuffers, head: Head, x_in: torch.Tenso
                    targets: torch.Tensor) -> None:
     """A few tokens through every layer and the output head: y_out as enqueue_tokens, then
     head.logits = head(RMSNorm(y_out)) and the log probabilities of `targets` (int32 [T]), the
-    entropies and the most probable tokens.  Valid when b.ctrl still reads (RL_NO_EARLY_OUT, 0)."""
+    entropies and the most probable tokens, in the head's first T rows, T being x_in's rows.  Valid when
+    b.ctrl still reads (RL_NO_EARLY_OUT, 0)."""
     T, H = _step_tokens(model, b, x_in, y_out), model.w.hidden
     V = head.logits.shape[1]
-    if head.q.shape != (T, H):
-        raise ValueError(f"a step of {T} tokens: the head was made for {tuple(head.q.shape)}")
+    if T > head.q.shape[0] or head.q.shape[1] != H:
+        raise ValueError(f"a step of {T} tokens of {H}: the head holds {tuple(head.q.shape)}")
     if targets.dtype != torch.int32 or targets.numel() != T:
         raise ValueError(f"targets: {T} int32 values expected, got {targets.dtype} {tuple(targets.shape)}")
     enqueue_tokens(model, b, x_in, y_out)
-    L.rl_add_rmsnorm(y_out, T, H, EPS, gain=head.gain, q=head.q, scale=head.q_scale, group=head.group)
-    L.rl_q4_matvec(head.w, head.scale, head.q, head.logits, T, V, H, head.group, x_scale=head.q_scale)
-    L.rl_logprobs(head.logits, T, V, targets, head.logprob, head.entropy,
-                  0 if head.top_ids is None else head.top_ids.shape[1], head.top_ids, head.top_logprob, head.ws,
-                  head.ws.numel())
+    q, q_scale, logits = head.q[:T], head.q_scale[:T], head.logits[:T]
+    L.rl_add_rmsnorm(y_out, T, H, EPS, gain=head.gain, q=q, scale=q_scale, group=head.group)
+    L.rl_q4_matvec(head.w, head.scale, q, logits, T, V, H, head.group, x_scale=q_scale)
+    top = (0, None, None) if head.top_ids is None else (head.top_ids.shape[1], head.top_ids[:T], head.top_logprob[:T])
+    L.rl_logprobs(logits, T, V, targets, head.logprob[:T], head.entropy[:T], *top, head.ws, head.ws.numel())
 
 
 @dataclass
@@ -454,12 +457,12 @@ def run_bounded_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out
         f = ctrl[0]
         if f == RL_NO_EARLY_OUT:
             break
-        ids, slots = b.ids[f].flatten().tolist(), b.slots[f].flatten().tolist()
+        ids, slots = b.ids[f, :T].flatten().tolist(), b.slots[f, :T].flatten().tolist()
         missing = sorted({e for e, s in zip(ids, slots) if s == 0})
         st.fill_bytes += model.fill(f, missing)
         st.filled += [(f, e) for e in missing]
         st.early_outs.append(f)
-        L.rl_resolve_slots(model.shape, f, T, b.ids[f], model.table, b.slots[f])
+        L.rl_resolve_slots(model.shape, f, T, b.ids[f, :T], model.table, b.slots[f, :T])
         b.ctrl[0] = RL_NO_EARLY_OUT
         enqueue_tokens_layer(model, b, f, y_out, y_out, stacked=True, routed=False)
         l0 = f + 1

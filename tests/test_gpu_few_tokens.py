@@ -673,6 +673,37 @@ def test_verify_step(L, T):
                  targets, n)
 
 
+def test_smaller_steps_in_the_same_buffers(L):
+    """Steps of any number of tokens up to the buffers' in one set of buffers: the bits of a step in buffers of
+    its own size, and the rows behind it left as they were."""
+    from quantized_moe_expert_rl_gb300 import engine
+    w = replace(TINY, n_layers=2)
+    m = engine.Model(w)
+    weight, n = 0.05 * randn(1009, w.hidden, seed=33), 4
+    b, head = engine.TokensBuffers.make(m, 7), engine.Head.make(weight, 7, group=64, top_n=n)
+    for T in (7, 1, 4, 0, 7, 3):
+        x = rows(w, T, seed=80 + T) if T else torch.empty(0, w.hidden, device="cuda")
+        t = torch.arange(T, dtype=torch.int32, device="cuda")
+        outs = (head.logits, head.logprob, head.entropy, head.top_ids, head.top_logprob)
+        for o in outs:
+            o.fill_(7)
+        ids = b.ids.clone()
+        y = torch.empty_like(x)
+        engine.enqueue_verify(m, b, head, x, y, t)
+        torch.cuda.synchronize()
+        assert b.ctrl.tolist() == [NO_EARLY_OUT, 0] and torch.equal(b.ids[:, T:], ids[:, T:])
+        assert all(torch.all(o[T:] == 7) for o in outs)
+        if T == 0:
+            continue
+        b1, h1 = engine.TokensBuffers.make(m, T), engine.Head.make(weight, T, group=64, top_n=n)
+        z = torch.empty_like(x)
+        engine.enqueue_verify(m, b1, h1, x, z, t)
+        torch.cuda.synchronize()
+        assert torch.equal(z, y) and torch.equal(b1.ids, b.ids[:, :T])
+        for o, o1 in zip(outs, (h1.logits, h1.logprob, h1.entropy, h1.top_ids, h1.top_logprob)):
+            assert torch.equal(o[:T], o1)
+
+
 def test_bounded_tokens_match_full_residency(L):
     from quantized_moe_expert_rl_gb300 import engine
     w = replace(TINY, n_layers=4, n_resident=24)

@@ -163,3 +163,47 @@ def test_a_step_as_large_as_its_buffers_runs(host):
     z = x.clone()
     engine.enqueue_tokens(m, b, z, z)          # in place
     assert torch.equal(z, y)
+
+
+# ---- steps of fewer tokens than the buffers hold ------------------------------------------
+@pytest.mark.parametrize("T", [0, 1, 3])
+def test_a_smaller_step_runs_in_the_same_buffers(host, T):
+    """Only its rows are run and written; the results are those of buffers of its own size."""
+    engine, m, lib = host(replace(W, n_resident=-1))
+    b, head = engine.TokensBuffers.make(m, 5), a_head(engine, 5)
+    engine.enqueue_verify(m, b, head, tokens(5), torch.empty(5, H), torch.zeros(5, dtype=torch.int32))
+    x, y = tokens(T, at=7), torch.empty(T, H)
+    ids, weights = b.ids.clone(), b.weights.clone()
+    for out in (head.logits, head.logprob, head.entropy, head.top_logprob, head.top_ids):
+        out.fill_(7)
+    lib.rows.clear()
+    engine.enqueue_verify(m, b, head, x, y, torch.zeros(T, dtype=torch.int32))
+    assert {n for _, n in lib.rows} == {T}
+    assert torch.all(head.logits[:T] == 1) and torch.all(head.logits[T:] == 7)
+    assert torch.all(head.logprob[:T] == -1) and torch.all(head.logprob[T:] == 7)
+    assert torch.all(head.top_ids[:T] == 3) and torch.all(head.top_ids[T:] == 7)
+    assert torch.equal(b.ids[:, T:], ids[:, T:]) and torch.equal(b.weights[:, T:], weights[:, T:])
+    if T:
+        own = engine.TokensBuffers.make(m, T)
+        z = torch.empty(T, H)
+        engine.enqueue_tokens(m, own, x, z)
+        assert torch.equal(z, y) and torch.equal(own.ids, b.ids[:, :T]) and torch.equal(own.slots, b.slots[:, :T])
+
+
+def test_a_smaller_bounded_step_fills_for_its_own_rows_only(host):
+    """The rows behind it hold the ids and absent slots of an earlier, larger step."""
+    engine, m, lib = host()
+    b = engine.TokensBuffers.make(m, 5)
+    engine.enqueue_tokens(m, b, tokens(5), torch.empty(5, H))          # stops at a layer; its slots stay absent
+    assert bool((b.slots[:, 2:] == 0).any())
+    x, y = tokens(2, at=11), torch.empty(2, H)
+    st = engine.run_bounded_tokens(m, b, x, y)
+    engine2, m2, _ = host()
+    b2, y2 = engine2.TokensBuffers.make(m2, 2), torch.empty(2, H)
+    st2 = engine2.run_bounded_tokens(m2, b2, x, y2)
+    assert (st.early_outs, st.filled, st.fill_bytes) == (st2.early_outs, st2.filled, st2.fill_bytes) and st.filled
+    assert torch.equal(y, y2) and np.array_equal(m.table_host, m2.table_host)
+    full, mf, libf = host(replace(W, n_resident=-1))
+    yf = torch.empty(2, H)
+    full.enqueue_tokens(mf, full.TokensBuffers.make(mf, 2), x, yf)
+    assert rel_l2(y.numpy(), yf.numpy()) == 0
