@@ -366,7 +366,9 @@ class DecodeStats:
     early_outs: list        # layers at which the chain stopped for a fill
     filled: list            # (layer, expert) filled at a stop
     fill_bytes: int
-    syncs: int              # host reads of the control block or of routing results
+    # host reads of the flag (one per launch of the chain) or of routing results; the check of the error
+    # bits after a stop at the last layer is not one
+    syncs: int
     prefetched: list = field(default_factory=list)  # (layer, expert) filled ahead (lookahead)
 
 
@@ -442,7 +444,8 @@ def run_bounded_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out
     """A few tokens through every layer with bounded residency: enqueue the layers; where some
     token of layer f selects an absent expert the flag stops the chain with y_out = x_f, the host
     fills the layer's missing experts, re-resolves the slots, runs the layer with the ids and
-    weights the GPU selected, and goes on at f + 1.  The caller zeroes b.miss; b.ctrl is reset here."""
+    weights the GPU selected, and goes on at f + 1.  Device error bits of any of these launches are
+    raised.  The caller zeroes b.miss; b.ctrl is reset here."""
     T = _step_tokens(model, b, x_in, y_out)
     b.ctrl.copy_(torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32))
     y_out.copy_(x_in)
@@ -466,6 +469,10 @@ def run_bounded_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out
         b.ctrl[0] = RL_NO_EARLY_OUT
         enqueue_tokens_layer(model, b, f, y_out, y_out, stacked=True, routed=False)
         l0 = f + 1
+    else:  # the last layer ran with the given routing: no later launch reads its error bits
+        bits = int(b.ctrl[1])
+        if bits != 0:
+            raise RuntimeError(f"moe_decode_tokens: device error bits {bits:#x}")
     return st
 
 

@@ -207,3 +207,24 @@ def test_a_smaller_bounded_step_fills_for_its_own_rows_only(host):
     yf = torch.empty(2, H)
     full.enqueue_tokens(mf, full.TokensBuffers.make(mf, 2), x, yf)
     assert rel_l2(y.numpy(), yf.numpy()) == 0
+
+
+# ---- error bits of the last launch --------------------------------------------------------
+@pytest.mark.parametrize("bits", [RL_DEVERR_MISSING, RL_DEVERR_WAIT_TIMEOUT])
+@pytest.mark.parametrize("last", [True, False])
+def test_error_bits_after_a_fill_are_raised(host, bits, last):
+    """A layer that runs with the routing it was given after a fill and raises an error bit leaves y
+    without that layer's experts: an error at the last layer too, after which no launch follows."""
+    engine, m, lib = host()
+    x, y = tokens(3), torch.empty(3, H)
+    stops = engine.run_bounded_tokens(m, engine.TokensBuffers.make(m, 3), x, y).early_outs
+    assert stops[-1] == m.L - 1 and len(stops) > 1
+    engine, m, lib = host()
+    lib.device_error = {stops[-1] if last else stops[0]: bits}
+    b = engine.TokensBuffers.make(m, 3)
+    with pytest.raises(RuntimeError, match=f"error bits {bits:#x}"):
+        engine.run_bounded_tokens(m, b, x, y)
+    # the next step on the same buffers starts afresh
+    lib.device_error = {}
+    engine.run_bounded_tokens(m, b, x, y)
+    assert b.ctrl.tolist() == [RL_NO_EARLY_OUT, 0]
