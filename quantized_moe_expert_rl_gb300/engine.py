@@ -437,6 +437,10 @@ def run_bounded_decode_token(model: Model, b: DecodeBuffers, x_in: torch.Tensor,
                 st.fill_bytes += model.fill(la, absent)
                 st.prefetched += [(la, e) for e in absent]
         l0 = f + 1
+    else:  # the last layer ran through moe_decode: no later launch reads its error bits
+        bits = int(b.ctrl[1])
+        if bits != 0:
+            raise RuntimeError(f"moe_decode: device error bits {bits:#x}")
     return st
 
 

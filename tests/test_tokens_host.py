@@ -228,3 +228,26 @@ def test_error_bits_after_a_fill_are_raised(host, bits, last):
     lib.device_error = {}
     engine.run_bounded_tokens(m, b, x, y)
     assert b.ctrl.tolist() == [RL_NO_EARLY_OUT, 0]
+
+
+@pytest.mark.parametrize("last", [True, False])
+@pytest.mark.parametrize("lookahead", [True, False])
+def test_error_bits_after_a_fill_are_raised_for_one_token(host, monkeypatch, last, lookahead):
+    """The same in run_bounded_decode_token, whose stopped layer runs through moe_decode."""
+    engine, m, lib = host()
+    x, y = tokens(1, at=2)[0], torch.empty(H)
+    stops = engine.run_bounded_decode_token(m, engine.DecodeBuffers.make(m), x, y, lookahead=lookahead).early_outs
+    at = stops[-1] if last else stops[0]
+    assert not last or at == m.L - 1
+    engine, m, lib = host()
+    b = engine.DecodeBuffers.make(m)
+    real = lib.moe_decode
+
+    def failing(shape, layer, x, norm_eps, slots, weights, codebook, y, accumulate, ctrl, ws, ws_bytes, stream=None):
+        if layer == at:
+            ctrl[1] = int(ctrl[1]) | RL_DEVERR_MISSING
+        else:
+            real(shape, layer, x, norm_eps, slots, weights, codebook, y, accumulate, ctrl, ws, ws_bytes)
+    monkeypatch.setattr(engine.L, "moe_decode", failing)
+    with pytest.raises(RuntimeError, match="device error bits 0x8"):
+        engine.run_bounded_decode_token(m, b, x, y, lookahead=lookahead)
