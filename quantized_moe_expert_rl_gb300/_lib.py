@@ -254,15 +254,30 @@ def _typed(what: str, t, allowed, numel: int | None = None) -> int:
     return code
 
 
-def _sized(what: str, t, itemsize: int, numel: int) -> None:
-    if t is not None and (t.element_size() != itemsize or t.numel() != numel):
-        raise ValueError(f"{what}: {numel} items of {itemsize} bytes expected, got {t.dtype} {tuple(t.shape)}")
+_kinds = None
 
 
-def _holds(what: str, t, itemsize: int, numel: int) -> None:
-    """Refuses a buffer of another item size or of fewer items than a call reads or writes."""
-    if t is not None and (t.element_size() != itemsize or t.numel() < numel):
-        raise ValueError(f"{what}: {numel} items of {itemsize} bytes needed, got {t.dtype} {tuple(t.shape)}")
+def _load_kinds():
+    """What the tensor types of a buffer may be.  Integers may come signed or unsigned (torch has few
+    operations on unsigned ones), 8-bit floats also as their bytes."""
+    global _kinds
+    import torch
+    u = lambda n: tuple(getattr(torch, k) for k in (f"int{n}", f"uint{n}") if hasattr(torch, k))  # noqa: E731
+    _kinds = {"f32": (torch.float32,), "i32": u(32), "i64": u(64), "bytes": u(8),
+              "e4m3": (torch.float8_e4m3fn, *u(8))}
+    return _kinds
+
+
+def _sized(what: str, t, kind: str, numel: int) -> None:
+    """Refuses a buffer of another type or of another size than the call's."""
+    if t is not None and (t.dtype not in (_kinds or _load_kinds())[kind] or t.numel() != numel):
+        raise ValueError(f"{what}: {numel} items of type {kind} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _holds(what: str, t, kind: str, numel: int) -> None:
+    """Refuses a buffer of another type or of fewer items than a call reads or writes."""
+    if t is not None and (t.dtype not in (_kinds or _load_kinds())[kind] or t.numel() < numel):
+        raise ValueError(f"{what}: {numel} items of type {kind} needed, got {t.dtype} {tuple(t.shape)}")
 
 
 def _ptrs(*tensors):
@@ -292,19 +307,19 @@ def moe_decode_tokens_workspace_bytes(shape, T) -> int:
 def moe_decode_tokens(shape, layer, T, x, norm_eps, w_router, bias, residency, codebook, ids, weights, slots, miss,
                       ctrl, logits_out, y, accumulate, ws, ws_bytes, stream=None):
     H, E, TK, layers = shape.hidden, shape.n_experts, T * shape.top_k, shape.n_layers
-    _holds("x", x, 4, T * H)
-    _holds("w_router", w_router, 4, E * H)
-    _holds("bias", bias, 4, E)
-    _holds("residency", residency, 8, layers * E)
-    _holds("codebook", codebook, 1, 2048)
-    _holds("ids", ids, 4, TK)
-    _holds("weights", weights, 4, TK)
-    _holds("slots", slots, 8, TK)
-    _holds("miss", miss, 4, layers)
-    _holds("ctrl", ctrl, 4, 2)
-    _holds("logits_out", logits_out, 4, T * E)
-    _holds("y", y, 4, T * H)
-    _holds("ws", ws, 1, ws_bytes)
+    _holds("x", x, "f32", T * H)
+    _holds("w_router", w_router, "f32", E * H)
+    _holds("bias", bias, "f32", E)
+    _holds("residency", residency, "i64", layers * E)
+    _holds("codebook", codebook, "bytes", 2048)
+    _holds("ids", ids, "i32", TK)
+    _holds("weights", weights, "f32", TK)
+    _holds("slots", slots, "i64", TK)
+    _holds("miss", miss, "i32", layers)
+    _holds("ctrl", ctrl, "i32", 2)
+    _holds("logits_out", logits_out, "f32", T * E)
+    _holds("y", y, "f32", T * H)
+    _holds("ws", ws, "bytes", ws_bytes)
     x, w, bias, res, cb, ids, wt, slots, miss, ctrl, lg, y, ws = _ptrs(x, w_router, bias, residency, codebook, ids,
                                                                        weights, slots, miss, ctrl, logits_out, y, ws)
     _check("moe_decode_tokens", load().moe_decode_tokens(
@@ -323,7 +338,7 @@ def rl_add_rmsnorm(x, T, H, eps, res=None, gain=None, x_out=None, xn=None, q=Non
     if gain is not None:
         _typed("gain", gain, (RL_F32,), H)
     if q is not None:
-        _sized("q", q, 1, n)
+        _sized("q", q, "e4m3", n)
     if scale is not None and group > 0:
         _typed("scale", scale, (RL_F32,), T * (H // group))
     x, res, gain, x_out, xn, q, scale = _ptrs(x, res, gain, x_out, xn, q, scale)
@@ -335,7 +350,7 @@ def rl_q4_matvec(w, w_scale, x, y, T, N, K, group, x_scale=None, accumulate=0, s
     """y [T][N] (+)= x [T][K] times the 4-bit matrix (w, w_scale) transposed; types from the tensors, x in
     e4m3 with x_scale [T][K / group]."""
     xdt, ydt = _typed("x", x, (*_ROW, RL_F8_E4M3), T * K), _typed("y", y, _ROW, T * N)
-    _sized("w", w, 1, N * K // 2)
+    _sized("w", w, "bytes", N * K // 2)
     if group > 0:
         _typed("w_scale", w_scale, (RL_F16,), N * (K // group))
         if x_scale is not None:
@@ -351,12 +366,12 @@ def rl_logprobs_workspace_bytes(T, V, top_n) -> int:
 
 def rl_logprobs(logits, T, V, targets, logprob, entropy, top_n, top_ids, top_logprob, ws, ws_bytes, stream=None):
     dt = _typed("logits", logits, _ROW, T * V)
-    _sized("targets", targets, 4, T)
-    _sized("logprob", logprob, 4, T)
-    _sized("entropy", entropy, 4, T)
-    _sized("top_ids", top_ids, 4, T * top_n)
-    _sized("top_logprob", top_logprob, 4, T * top_n)
-    _holds("ws", ws, 1, ws_bytes)
+    _sized("targets", targets, "i32", T)
+    _sized("logprob", logprob, "f32", T)
+    _sized("entropy", entropy, "f32", T)
+    _sized("top_ids", top_ids, "i32", T * top_n)
+    _sized("top_logprob", top_logprob, "f32", T * top_n)
+    _holds("ws", ws, "bytes", ws_bytes)
     x, targets, logprob, entropy, ids, top, ws = _ptrs(logits, targets, logprob, entropy, top_ids, top_logprob, ws)
     _check("rl_logprobs", load().rl_logprobs(x, dt, T, V, targets, logprob, entropy, top_n, ids, top, ws, ws_bytes,
                                              _stream(stream)))

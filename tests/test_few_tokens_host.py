@@ -174,3 +174,53 @@ def test_pack_q4(group):
     step = s.float().repeat_interleave(group, 1)
     assert torch.all((back - v).abs() <= step * (0.5 + 8 * 2.0 ** -11))
     assert torch.all(back[4] == 0)
+
+
+@pytest.mark.parametrize("what, dtype", [
+    ("x", "int32"), ("w_router", "int32"), ("bias", "int32"), ("residency", "float64"), ("codebook", "bool"),
+    ("ids", "float32"), ("weights", "int32"), ("slots", "float64"), ("miss", "float32"), ("ctrl", "float32"),
+    ("logits_out", "int32"), ("y", "int32")])
+def test_binding_checks_the_types_of_a_layer(what, dtype):
+    """A tensor of another type of the same width (ids and weights changed over, say) is refused: the
+    library would read its bits as what they are not."""
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    sh, T = L.RlShape.of(256, 8, 2, 256, 1), 3
+    i32, i64 = torch.int32, torch.int64
+    b = dict(x=torch.zeros(T, 256), w_router=torch.zeros(8, 256), bias=torch.zeros(8),
+             residency=torch.zeros(1, 8, dtype=i64), codebook=torch.zeros(256, 8, dtype=torch.int8),
+             ids=torch.zeros(T, 2, dtype=i32), weights=torch.zeros(T, 2), slots=torch.zeros(T, 2, dtype=i64),
+             miss=torch.zeros(1, dtype=i32), ctrl=torch.zeros(2, dtype=i32), logits_out=torch.zeros(T, 8),
+             y=torch.zeros(T, 256), ws=torch.zeros(L.moe_decode_tokens_workspace_bytes(sh, T), dtype=torch.uint8))
+    b[what] = b[what].to(getattr(torch, dtype))
+    with pytest.raises(ValueError, match=f"^{what}:"):
+        L.moe_decode_tokens(sh, 0, T, b["x"], -1.0, b["w_router"], b["bias"], b["residency"], b["codebook"], b["ids"],
+                            b["weights"], b["slots"], b["miss"], b["ctrl"], b["logits_out"], b["y"], 0, b["ws"],
+                            b["ws"].numel())
+
+
+@pytest.mark.parametrize("what, dtype", [("targets", "float32"), ("logprob", "int32"), ("entropy", "int32"),
+                                         ("top_ids", "float32"), ("top_logprob", "int32")])
+def test_binding_checks_the_types_of_logprobs(what, dtype):
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    b = dict(targets=torch.zeros(2, dtype=torch.int32), logprob=torch.zeros(2), entropy=torch.zeros(2),
+             top_ids=torch.zeros(2, 3, dtype=torch.int32), top_logprob=torch.zeros(2, 3))
+    b[what] = b[what].to(getattr(torch, dtype))
+    ws = torch.zeros(L.rl_logprobs_workspace_bytes(2, 256, 3), dtype=torch.uint8)
+    with pytest.raises(ValueError, match=f"^{what}:"):
+        L.rl_logprobs(torch.zeros(2, 256), 2, 256, b["targets"], b["logprob"], b["entropy"], 3, b["top_ids"],
+                      b["top_logprob"], ws, ws.numel())
+
+
+def test_binding_checks_the_types_of_eight_bits():
+    """The 8-bit copy of a norm is e4m3 (or its bytes), not another 8-bit float; 4-bit weights are bytes."""
+    torch = pytest.importorskip("torch")
+    from quantized_moe_expert_rl_gb300 import _lib as L
+    x, scale = torch.zeros(2, 256), torch.zeros(2, 2)
+    for dt in (torch.float8_e5m2, torch.bool):
+        with pytest.raises(ValueError, match="^q:"):
+            L.rl_add_rmsnorm(x, 2, 256, 1e-6, q=torch.zeros(2, 256).to(dt), scale=scale)
+    with pytest.raises(ValueError, match="^w:"):
+        L.rl_q4_matvec(torch.zeros(5, 128).to(torch.float8_e4m3fn), torch.zeros(5, 2).half(), x, torch.zeros(2, 5), 2, 5,
+                       256, 128)
