@@ -105,8 +105,17 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
                 s2 = fmaf(v, v, s2);
             }
         s2 = row_reduce<false>(s2, part, w0, nw);
-        if (odd && fin && s2 == s2)
-            r = (float)(1.0 / sqrt(ldexp((double)s2 / a.H, 2 * ex) + (double)a.eps));
+        if (odd && fin && s2 == s2) {
+            double rd = 1.0 / sqrt(ldexp((double)s2 / a.H, 2 * ex) + (double)a.eps);
+            if (rd > 1e38) {  // beyond f32: 2^64 of it go to the values, which are below 2e-36 (rd is at most 2^156)
+                rd *= 1.0 / 18446744073709551616.0;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[c][j] *= 18446744073709551616.0f;
+            }
+            r = (float)rd;
+        }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {

@@ -103,6 +103,29 @@ def test_add_rmsnorm_magnitudes(L):
     check_norm(L, x[4:].contiguous() * 1e-37, None, None, 1e-6, 64)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [128, 2048, 16384])
+def test_add_rmsnorm_below_the_normal_range(L, dt, H):
+    """Rows whose factor 1 / RMS leaves the f32 range (RMS below 2.9e-39) are of order 1 all the same, their
+    zeros stay zeros, and the rows beside them keep their bits."""
+    g = torch.Generator().manual_seed(H)
+    size = torch.tensor([1e-40, 2e-39, 4e-39, 1.0, 1e-38, 1e-30, 3e-39], dtype=torch.float64)[:, None]
+    x = torch.randn(7, H, generator=g, dtype=torch.float64) * size
+    x[0, ::3] = 0
+    x = x.to(TYPES[dt]).cuda()
+    assert torch.all(x[1:].double().abs().amax(1) > 0)
+    gain = 1 + 0.3 * randn(H, seed=5)
+    check_norm(L, x, None, None, 0.0, 32)
+    check_norm(L, x, None, gain, 0.0, 128)
+    one = torch.zeros_like(x)           # a single smallest value in a row
+    one[:, 5] = float(torch.finfo(TYPES[dt]).smallest_normal) * torch.finfo(TYPES[dt]).eps
+    check_norm(L, one, None, None, 0.0, 64)
+    plain, beside = torch.empty_like(x[3:4]), torch.empty_like(x)
+    L.rl_add_rmsnorm(x[3:4], 1, H, 0.0, xn=plain)
+    L.rl_add_rmsnorm(x, 7, H, 0.0, xn=beside)
+    assert torch.equal(plain[0], beside[3])
+
+
 def test_add_rmsnorm_without_eight_bits_takes_any_multiple_of_8(L):
     for H in (8, 24, 1000, 2056):
         x = randn(3, H, seed=H)
