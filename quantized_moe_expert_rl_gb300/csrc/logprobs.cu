@@ -557,26 +557,31 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const __grid_co
                 m = tm;
             }
             if (m > kNinf) {
-                const unsigned long long nm = dup2(-m), l2 = dup2(kLog2e), u0 = U2;
+                // The tile's terms are added among themselves first: one by one, those below half a step of a
+                // running sum that holds a large term would all be lost.
+                const unsigned long long nm = dup2(-m), l2 = dup2(kLog2e);
+                unsigned long long s = 0ull, w = 0ull;
 #pragma unroll
                 for (int i = 0; i < kLpEpt; i += 2) {
                     const unsigned long long d = fadd2(pack2(__float_as_uint(v[i]), __float_as_uint(v[i + 1])), nm);
                     const unsigned long long t = fmul2(d, l2);
                     const unsigned long long e = pack2(__float_as_uint(ex2(__uint_as_float((uint32_t)t))),
                                                        __float_as_uint(ex2(__uint_as_float((uint32_t)(t >> 32)))));
-                    S2 = fadd2(S2, e);
-                    U2 = ffma2(d, e, U2);
+                    s = i == 0 ? e : fadd2(s, e);
+                    w = i == 0 ? fmul2(d, e) : ffma2(d, e, w);
                 }
-                const float u = hsum2(U2);
+                const float u = hsum2(w);
                 if (u != u) {  // a value of -inf (its 0 * -inf contributes 0), or a NaN
-                    U2 = u0;
+                    w = 0ull;
 #pragma unroll
                     for (int i = 0; i < kLpEpt; i += 2) {
                         const float d0 = v[i] - m, d1 = v[i + 1] - m;
                         const float c0 = fmaxf(d0, -1e4f) * ex2(d0 * kLog2e), c1 = fmaxf(d1, -1e4f) * ex2(d1 * kLog2e);
-                        U2 = fadd2(U2, pack2(__float_as_uint(c0), __float_as_uint(c1)));
+                        w = fadd2(w, pack2(__float_as_uint(c0), __float_as_uint(c1)));
                     }
                 }
+                S2 = fadd2(S2, s);
+                U2 = fadd2(U2, w);
             }
             bool again = false;  // the first tile, with a NaN in it
             if (n > 0 && t0 == begin) again = lp_first(sh, order_key(tm), n, nan);

@@ -408,6 +408,33 @@ def test_logprobs_merges_what_the_other_pieces_published(L, T, V, n):
             assert torch.equal(o[k], want[i % 2][k]), (i, k)
 
 
+@pytest.mark.parametrize("V", [131072, 1 << 20])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_logprobs_small_terms_beside_large_ones(L, V, dt):
+    """4096 zeros (16 per thread of the row's CTA), then V - 4096 values whose terms lie below half a step of the
+    sum of eight ones: added one by one to it they would all be lost, 1.4e-5 and 1.1e-4 of the sum.
+    Bounds: of a sum of positive terms, the terms of a tile among themselves (7), the tiles, 2 values per
+    lane, 5 + 5 shuffles and the merge of 2 pieces (7) make V / 4096 + 27 additions; the small terms'
+    own error (|d| log2 e in the argument, 1.2 u each, and 4 u of ex2) counts with their share of S, below
+    2^-13, and in full in U.  log S, U / S and the differences: 4 u of their magnitude, as in check_lp."""
+    T, d = 456, -14.625
+    x = torch.full((T, V), d, dtype=TYPES[dt], device="cuda")
+    x[:, :4096] = 0
+    t = torch.zeros(T, dtype=torch.int32, device="cuda")
+    t[1::2] = V - 1
+    o = lp_run(L, x, t, 0)
+    e = math.exp(d)
+    S, Um = 4096 + (V - 4096) * e, (V - 4096) * -d * e     # Um = -sum (x - m) e^(x - m)
+    n = V / 4096 + 27
+    rel_S = n * U + 2.0 ** -13 * (1.2 * -d + 4) * U
+    want = torch.full((T,), -math.log(S), dtype=torch.float64, device="cuda")
+    want[1::2] += d
+    assert torch.all((o["logprob"].double() - want).abs() <= rel_S + 4 * U * (want.abs() + 1) + 4 * U * -d)
+    entropy = math.log(S) + Um / S
+    bound = rel_S + Um / S * (2 * n + 1.2 * -d + 4) * U + 4 * U * (entropy + 1)
+    assert torch.all((o["entropy"].double() - entropy).abs() <= bound)
+
+
 # ---- moe_decode_tokens --------------------------------------------------------------------
 TINY = synth.WORKLOADS["tiny"]
 SHAPES = {
