@@ -298,6 +298,20 @@ def test_logprobs(L, T, V, n, dt):
     check_lp(lp_run(L, x, targets, n), x, targets, n)
 
 
+@pytest.mark.parametrize("V,T", [(4095, 456), (4096, 457), (4097, 228), (4097, 229), (16384, 114), (16384, 115),
+                                 (62 * 4096 + 1, 7), (62 * 4096 + 1, 8), (63 * 4096, 7), (17, 456), (1, 1000)])
+def test_logprobs_on_both_sides_of_a_split(L, V, T):
+    """Rows in pieces of a tile (up to 456 pieces of at most 1/62 of a row) and in equal runs over all CTAs, V on
+    both sides of a tile: every value belongs to exactly one piece.  A row's largest value marks a piece that
+    is left out, the sums one that is counted twice."""
+    n = min(V, 3)
+    x = randn(T, V, seed=T)
+    at = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(V)).cuda()
+    x[torch.arange(T, device="cuda"), at] = 9.0
+    x[: T // 2] = 0.5                                  # every value counts the same: log V
+    check_lp(lp_run(L, x, at.to(torch.int32), n), x, at.to(torch.int32), n)
+
+
 def test_logprobs_orders_that_defeat_a_threshold(L):
     """Rising, falling and equal rows, a row whose largest values share one thread's positions, ties
     across segments, signed zeros."""
