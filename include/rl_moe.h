@@ -377,7 +377,8 @@ rl_status moe_prefill_chunk_f32(const rl_moe_shape *shp, int32_t layer, int32_t 
  * GPU-routed decode", "What changed": router and experts of a decode step with no host round
  * trip; "Red Lite dev20", "What changed", item 3: pairs sorted by expert, sums in selection
  * order).  Arithmetic at f32 accuracy: the router's dots in f32, the experts on the tensor cores
- * with every activation as an exact sum of three bf16 values and f32 accumulation.
+ * with every activation as a sum of three bf16 values (exact from a magnitude of 2^-110 on; below, to
+ * 2^-133) and f32 accumulation.
  * Misses: if any token selects an absent expert, ids, weights and slots of all tokens are
  * written, miss[layer] += the number of such selections, ctrl[0] = min(ctrl[0], layer), and y is
  * left as it was; after a fill and rl_resolve_slots the experts run through the same call with
@@ -430,7 +431,8 @@ rl_status rl_add_rmsnorm(const void *x, const void *res, const float *gain, int3
  * x [T][K] of x_dtype: RL_F32, RL_F16, RL_BF16, or RL_F8_E4M3 with x_scale f32 [T][K / group] (else
  * NULL), as rl_add_rmsnorm writes them with the same group.  y [T][N] of y_dtype (not
  * RL_F8_E4M3), rounded once.  f32 accumulation; f32 activations are held to 22 bits each, and f32,
- * f16 and bf16 ones to no finer than 2^-38 of their row's largest magnitude.  An infinity or a NaN in
+ * f16 and bf16 ones to no finer than 2^-38 of their row's largest magnitude; the product of two scales
+ * is an f32 value.  An infinity or a NaN in
  * x reaches its own token's outputs only.
  * Any T >= 0; weights are read once per 32 (or, with f32 x or a small matrix, 16 or 8) columns.
  * w, w_scale, x 16-byte aligned; y must not overlap an input.

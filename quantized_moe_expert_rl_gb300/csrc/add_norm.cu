@@ -11,8 +11,8 @@
 // fewer than 256 threads share a CTA of about 256 threads.
 //
 // Bound: memory for many rows, the launch and two memory round trips for few.  Measured back to back in a
-// graph: 8192 rows of 2048 bf16 values with residual, gain and the 8-bit copy (151 MB) 29.5 us, 5.1 TB/s; 2048
-// rows 10.5 to 10.9 us, 3.5 TB/s; one row 2.9 us.  Two and four runs per thread, which leave fewer warps to meet
+// graph: 8192 rows of 2048 bf16 values with residual, gain and the 8-bit copy (151 MB) 29.7 us, 5.1 TB/s; 2048
+// rows 10.5 to 10.9 us, 3.5 TB/s; one row 2.8 us; 8192 and 2048 f32 rows 44.3 us, 6.4 TB/s, and 14.3 us.  Two and four runs per thread, which leave fewer warps to meet
 // per row, were the same to 15% slower from 2048 rows on.
 #include "qdot.cuh"
 #include "row_types.cuh"

@@ -8,8 +8,8 @@
 // that any number of rows keeps the GPU evenly busy.  A CTA streams its run in tiles of 4096 values;
 // every thread copies the 16-byte pieces that it will read itself, three tiles
 // ahead and on across the rows, so that no barrier stands between the copies and their use.  Rows
-// that lie whole in a run are finished at once.  Every thread keeps a running (m, S, U): when a tile raises m by d, S and U are rescaled by
-// e^-d (U loses d S first).  The pieces of a row cut by a run's end meet in the last of their CTAs to
+// that lie whole in a run are finished at once.  Every thread keeps a running (m, S, U), to which a tile's 16
+// terms are added as one sum; when a tile raises m by d, S and U are rescaled by e^-d (U loses d S first).  The pieces of a row cut by a run's end meet in the last of their CTAs to
 // finish (a completion counter in the workspace), which merges them in row order, so results do not
 // depend on arrival order.
 //
@@ -23,10 +23,10 @@
 // goes through those tiles again with the groups' largest keys, which are distinct, so that a tile
 // leaves at most n groups x 64 of them.
 //
-// Measured back to back in a graph: 512 x 131072 f32 (268.5 MB, 39.6 us at the measured copy rate) 72 us
-// with the 20 best tokens, 54 to 56 us without any; 912 rows without any 73 us, 6.5 TB/s.  What is left are the
-// rows cut by the runs' ends (with 512 rows every CTA has two: two publications and a merge, about 10
-// us) and the insertions.  One row of 131072 takes 9.6 us, 16 rows of 100003 bf16 11.7 us: a chain of latencies
+// Measured back to back in a graph: 512 x 131072 f32 (268.5 MB, 39.6 us at the measured copy rate) 72.3 us
+// with the 20 best tokens, 53.8 without any; 912 rows without any 71.8 us, 6.7 TB/s.  What is left are the
+// rows cut by the runs' ends (with 512 rows every CTA has two: two publications and a merge; 456 rows, which
+// have none, take 51.1 us with the 20 best and 38.6 without) and the insertions.  One row of 131072 takes 9.7 us, 16 rows of 100003 bf16 11.7 us: a chain of latencies
 // (launch, tile, first threshold, publication, merge).
 #include <math.h>
 

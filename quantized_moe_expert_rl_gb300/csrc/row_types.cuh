@@ -54,7 +54,8 @@ __device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 // v = a + b rounded to the element type.  A 16-bit add rounds the exact sum once, which is what adding in
-// f32 and rounding gives: the f32 sum is exact unless the smaller term is below 2^-8 of half a step.
+// f32 and rounding gives: rounding first to p >= 2 q + 2 bits changes no sum's rounding to q bits (24
+// against 11 for half, 8 for bf16).
 template <typename E>
 __device__ __forceinline__ void add8(const E *a, const E *b, float (&v)[8]) {
     const uint4 p = *reinterpret_cast<const uint4 *>(a), q = *reinterpret_cast<const uint4 *>(b);
