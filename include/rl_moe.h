@@ -71,7 +71,7 @@ typedef enum rl_status {
     RL_ERR_TIMEOUT = 4      /* reserved for host-visible bounded-wait expiry */
 } rl_status;
 
-/* element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_logprobs) */
+/* element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_f8_matmul, rl_f8_gated, rl_logprobs) */
 typedef enum rl_dtype {
     RL_F32 = 0,
     RL_F16 = 1,
@@ -463,6 +463,42 @@ size_t rl_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t top_n);
 rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, int32_t V, const int32_t *targets, float *logprob,
                       float *entropy, int32_t top_n, int32_t *top_ids, float *top_logprob, void *ws, size_t ws_bytes,
                       void *stream);
+
+/*
+ * rl_f8_matmul - product of T rows in 8 bits and an N x K matrix in 8 bits, with a scale for each block
+ * of 128 (dense projections, an output head, a shared expert's down projection):
+ *   y[t][n] = (res ? res[t][n] : 0) + sum_b x_scale[t][b] w_scale[n / 128][b] sum_{k / 128 = b} x[t][k] w[n][k].
+ * w e4m3 bytes [N][K]; w_scale f32 [ceil(N / 128)][ceil(K / 128)]; x e4m3 bytes [T][K] and x_scale f32
+ * [T][ceil(K / 128)], as rl_add_rmsnorm (group 128) and rl_f8_gated write them; y, res [T][N] of y_dtype
+ * (RL_F32, RL_F16, RL_BF16), rounded once; res may be NULL or y itself.  Sums in f32: the 128 products of a
+ * block on the tensor cores, the blocks' sums times the f32 product of their scales in order of the blocks
+ * (or of up to eight equal shares of them, added in order).  Any N; K a multiple of 16 (the last block may be
+ * shorter); any T >= 0; T <= 2^22, N <= 2^26, K <= 2^20.  An infinite or NaN scale and an e4m3 NaN in x reach
+ * their own token's outputs only.
+ * ctrl (NULL: always runs): does nothing when ctrl[0] <= layer, as the other calls for a layer.  A bounded wait
+ * that ran out sets RL_DEVERR_WAIT_TIMEOUT there.
+ * w, x 16-byte aligned; scales 4-byte; y, res to their element (16-byte where N times their size is a
+ * multiple of 16 is faster); y must not overlap w, x or the scales.  It may be captured in a CUDA graph.
+ */
+rl_status rl_f8_matmul(const uint8_t *w, const float *w_scale, int32_t N, int32_t K, const uint8_t *x,
+                       const float *x_scale, int32_t T, const void *res, void *y, int32_t y_dtype, int32_t layer,
+                       int32_t *ctrl, void *stream);
+
+/*
+ * rl_f8_gated - the gated half of a feed-forward block (a shared expert's gate and up projections) in one
+ * kernel: with g, u [T][I] the products of rl_f8_matmul with the two matrices, in f32,
+ *   v = silu(g) * u,  silu(z) = z / (1 + e^-z);  h = v rounded to h_dtype
+ *   per 128 consecutive values (the last run of a row may be shorter): scale = max|v| / 448,
+ *   q = e4m3(v * (448 / max|v|)), round to nearest even (zeros: q = scale = 0; an infinity or a NaN among
+ *   them: scale NaN, q = 0).
+ * w_gate, w_up e4m3 bytes [I][K]; their scales f32 [ceil(I / 128)][ceil(K / 128)]; x, x_scale, ctrl and the limits
+ * as for rl_f8_matmul (I for N).  h [T][I] of h_dtype (RL_F32, RL_F16, RL_BF16) or NULL; q e4m3 bytes [T][I]
+ * with scale f32 [T][ceil(I / 128)], or both NULL; one of the two is given.  The down projection reads (q, scale)
+ * through rl_f8_matmul where I is a multiple of 16.  q and scale 4-byte aligned, h to its element.
+ */
+rl_status rl_f8_gated(const uint8_t *w_gate, const float *gate_scale, const uint8_t *w_up, const float *up_scale,
+                      int32_t I, int32_t K, const uint8_t *x, const float *x_scale, int32_t T, void *h,
+                      int32_t h_dtype, uint8_t *q, float *scale, int32_t layer, int32_t *ctrl, void *stream);
 
 #ifdef __cplusplus
 }

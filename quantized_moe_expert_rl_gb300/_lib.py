@@ -25,7 +25,7 @@ EXPORTS = ("rl_abi_version", "rl_last_error", "rl_record_bytes", "rl_rmsnorm", "
            "moe_prefill_chunk", "moe_prefill_chunk_f32", "moe_decode_static", "moe_decode_stack_workspace_bytes",
            "moe_decode_stack", "rl_fill_workspace_bytes", "rl_fill_missing", "rl_host_device_pointer",
            "moe_decode_stack_fill", "moe_decode_layer", "moe_decode_tokens_workspace_bytes", "moe_decode_tokens",
-           "rl_add_rmsnorm", "rl_q4_matvec", "rl_logprobs_workspace_bytes", "rl_logprobs")
+           "rl_add_rmsnorm", "rl_q4_matvec", "rl_logprobs_workspace_bytes", "rl_logprobs", "rl_f8_matmul", "rl_f8_gated")
 
 RL_F32, RL_F16, RL_BF16, RL_F8_E4M3 = 0, 1, 2, 3
 RL_MAX_DECODE_TOKENS = 32
@@ -87,6 +87,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                     vp]),
         "rl_add_rmsnorm": (i32, [vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, i32, vp]),
         "rl_q4_matvec": (i32, [vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, i32, i32, vp]),
+        "rl_f8_matmul": (i32, [vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp]),
+        "rl_f8_gated": (i32, [vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, vp, vp]),
         "rl_logprobs_workspace_bytes": (sz, [i32, i32, i32]),
         "rl_logprobs": (i32, [vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
         "rl_fill_workspace_bytes": (sz, [shp]),
@@ -358,6 +360,42 @@ def rl_q4_matvec(w, w_scale, x, y, T, N, K, group, x_scale=None, accumulate=0, s
     w, w_scale, x, x_scale, y = _ptrs(w, w_scale, x, x_scale, y)
     _check("rl_q4_matvec", load().rl_q4_matvec(w, w_scale, N, K, group, x, xdt, x_scale, T, y, ydt, accumulate,
                                                _stream(stream)))
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def rl_f8_matmul(w, w_scale, x, x_scale, y, T, N, K, res=None, layer=0, ctrl=None, stream=None):
+    """y [T][N] = (res +) x [T][K] times w [N][K] transposed, both e4m3 with a scale per block of 128; y's type
+    is the tensor's.  With ctrl, nothing where layer `layer` or an earlier one raised the flag."""
+    dt = _typed("y", y, _ROW, T * N)
+    if res is not None and (res.dtype != y.dtype or res.numel() != T * N):
+        raise ValueError(f"res: {T * N} values of {y.dtype} expected, got {res.dtype} {tuple(res.shape)}")
+    _sized("w", w, "e4m3", N * K)
+    _sized("w_scale", w_scale, "f32", _blocks(N) * _blocks(K))
+    _sized("x", x, "e4m3", T * K)
+    _sized("x_scale", x_scale, "f32", T * _blocks(K))
+    _holds("ctrl", ctrl, "i32", 2)
+    w, w_scale, x, x_scale, res, y, ctrl = _ptrs(w, w_scale, x, x_scale, res, y, ctrl)
+    _check("rl_f8_matmul", load().rl_f8_matmul(w, w_scale, N, K, x, x_scale, T, res, y, dt, layer, ctrl, _stream(stream)))
+
+
+def rl_f8_gated(w_gate, gate_scale, w_up, up_scale, x, x_scale, T, I, K, h=None, q=None, scale=None, layer=0, ctrl=None,
+                stream=None):
+    """silu(x w_gate^T) * (x w_up^T) for rows x [T][K], all e4m3 with a scale per block of 128, into h [T][I] of
+    its tensor's type or in 8 bits (q, scale), or both."""
+    dt = RL_F32 if h is None else _typed("h", h, _ROW, T * I)
+    for what, t, kind, n in (("w_gate", w_gate, "e4m3", I * K), ("gate_scale", gate_scale, "f32", _blocks(I) * _blocks(K)),
+                             ("w_up", w_up, "e4m3", I * K), ("up_scale", up_scale, "f32", _blocks(I) * _blocks(K)),
+                             ("x", x, "e4m3", T * K), ("x_scale", x_scale, "f32", T * _blocks(K)),
+                             ("q", q, "e4m3", T * I), ("scale", scale, "f32", T * _blocks(I))):
+        _sized(what, t, kind, n)
+    _holds("ctrl", ctrl, "i32", 2)
+    w_gate, gate_scale, w_up, up_scale, x, x_scale, h, q, scale, ctrl = _ptrs(w_gate, gate_scale, w_up, up_scale, x, x_scale,
+                                                                             h, q, scale, ctrl)
+    _check("rl_f8_gated", load().rl_f8_gated(w_gate, gate_scale, w_up, up_scale, I, K, x, x_scale, T, h, dt, q, scale, layer,
+                                             ctrl, _stream(stream)))
 
 
 def rl_logprobs_workspace_bytes(T, V, top_n) -> int:

@@ -1,0 +1,876 @@
+// f8_matmul.cu - rl_f8_matmul and rl_f8_gated: products of 8-bit activations (e4m3, an f32 scale per 128
+// values of a row) and 8-bit weights (e4m3, an f32 scale per block of 128 x 128).
+//
+//   acc[t][n] = sum_b xs[t][b] ws[n / 128][b] sum_{k in block b} x[t][k] w[n][k]
+//   rl_f8_matmul: y = acc (+ res);  rl_f8_gated: h = silu(acc of gate) * (acc of up), as it is or in 8 bits
+//
+// The sum over a block of 128 runs on the tensor cores (tcgen05, kind::f8f6f4, f32 accumulators in tensor
+// memory); the two scales multiply it when it is read back, in f32 registers ("promotion"), while the tensor
+// cores work on the next block in another accumulator.  Two kernels:
+//
+//   rows  up to 128 rows per pass.  A operand: 128 weight rows, B operand: the activation rows (16, 32, 64
+//         or 128 of them), so that few rows waste no tensor work.  Lane = weight row, column = token.
+//   wide  many rows.  A operand: 128 activation rows, B operand: 256 weight rows.  Lane = token, so that a
+//         lane's scale is one number per block.
+//
+// Both: warps 0-7 promote (warp w reads the lanes of quadrant w % 4, a half of the columns each), warp 8
+// loads (tensor copies with the 128-byte swizzle, 4-byte asynchronous copies for the scales), one thread of
+// warp 9 issues the MMAs.
+#include "qdot.cuh"
+#include "row_types.cuh"
+#include "tc_desc.cuh"
+
+using namespace rl;
+
+namespace {
+
+constexpr int kG = 128;                       // values per scale
+constexpr int kTileBytes = 128 * kG;          // 128 rows of one block
+constexpr int kThreads = 320, kLoadW = 8, kMmaW = 9;
+constexpr int kMaxCluster = 8;
+
+struct F8Args {
+    CUtensorMap wmap[2];   // weights (gate, up), boxes of 128 rows x 128 values
+    CUtensorMap xmap;      // activations, boxes of the kernel's row tile x 128 values
+    const float *ws[2];    // [ceil(N / 128)][KB]
+    const float *xs;       // [T][KB]
+    void *y;               // [T][N] of dtype (gated: h, may be NULL)
+    const void *res;       // [T][N] of dtype or NULL
+    uint8_t *q;            // gated: e4m3 [T][N]
+    float *scale;          // gated: [T][ceil(N / 128)]
+    int32_t *ctrl;
+    int layer;
+    int T, N, K, KB, dtype;
+    int tiles_n, tiles;    // weight tiles, all tiles
+};
+
+__device__ __forceinline__ float load1(const void *p, size_t i, int dt) {
+    if (dt == RL_F32) return static_cast<const float *>(p)[i];
+    if (dt == RL_F16) return __half2float(static_cast<const __half *>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store1(void *p, size_t i, float v, int dt) {
+    if (dt == RL_F32) static_cast<float *>(p)[i] = v;
+    else if (dt == RL_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ unsigned long long dup2(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ unsigned long long fmul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// arrives on `bar` (which counts every lane) when this thread's cp.async copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+// Barrier of the 256 promoting threads; true for all where any of them brought `pred`, so that they leave
+// together after a wait that ran out.
+__device__ __forceinline__ bool epi_sync(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred)
+        : "memory");
+    __syncwarp();
+    return r != 0u;
+}
+
+// The outputs of the gated form for 128 values of one row, lane L holding values 4 L .. 4 L + 3 of group g:
+// stored in the row type, or as e4m3 with the group's scale max|h| / 448 (a group that holds an infinity or
+// a NaN: scale NaN, zeros).  Whole warp.
+__device__ __forceinline__ void gated_store(const F8Args &a, int t, int g, float (&h)[4]) {
+    const int lane = threadIdx.x & 31, i = g * kG + 4 * lane;
+    const size_t at = (size_t)t * a.N + i;
+    if (a.y) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < a.N) store1(a.y, at + j, h[j], a.dtype);
+    }
+    if (!a.q) return;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max_abs_nan(m, i + j < a.N ? h[j] : 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
+    const bool bad = !(m < INFINITY);
+    const float f = m > 0.f && !bad ? 448.f / m : 0.f;
+    if (lane == 0) a.scale[(size_t)t * a.tiles_n + g] = bad ? __int_as_float(0x7fffffff) : m / 448.f;
+    uint32_t w = 0u;
+    if (f > 0.f) {
+        // a quotient beyond f32 (m below 448 / the largest f32) goes in two steps
+        if (f < INFINITY) w = pack4_e4m3(h[0] * f, h[1] * f, h[2] * f, h[3] * f);
+        else {
+            const float s = 18446744073709551616.f, f2 = 448.f / (m * s);
+            w = pack4_e4m3(h[0] * s * f2, h[1] * s * f2, h[2] * s * f2, h[3] * s * f2);
+        }
+    }
+    if (i + 4 <= a.N && (a.N & 3) == 0) {
+        *reinterpret_cast<uint32_t *>(a.q + at) = w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < a.N) a.q[at + j] = (uint8_t)(w >> (8 * j));
+    }
+}
+
+// ---- rows: 128 weight rows x TT tokens per tile -----------------------------------------------
+template <int TT, bool GATED>
+struct Rows {
+    static constexpr int NA = GATED ? 2 : 1;
+    static constexpr int kStage = NA * kTileBytes + TT * kG;
+    static constexpr int kStages = TT >= 128 || (GATED && TT >= 64) ? 4 : GATED ? 3 : 5;
+    static constexpr int kBufs = NA * TT >= 128 ? 2 : 4;              // accumulators in tensor memory
+    static constexpr int kCols = kBufs * NA * TT < 32 ? 32 : kBufs * NA * TT;
+    static constexpr int kScales = (TT + 4) * 4;                       // bytes per stage: xs of the tokens, ws
+    static constexpr int o_sc = 1024;
+    static constexpr int o_ring = (o_sc + kStages * kScales + 1023) / 1024 * 1024;
+    static constexpr int o_part = o_ring + kStages * kStage;           // f32 [NA][TT][128] (see below)
+    static constexpr size_t bytes(bool split) {
+        return o_part + (split ? NA * TT * 512 : GATED ? TT * 512 : 0);
+    }
+};
+
+// Tiles of 128 weight rows (of each matrix) x TT tokens.  With a cluster of S > 1 CTAs every CTA takes a
+// share of the blocks of one tile, the partial sums are left in shared memory and added in rank order by
+// the cluster, each CTA a share of the outputs; with S = 1 the CTAs walk over the tiles.
+template <int TT, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_constant__ F8Args a, int S) {
+    using R = Rows<TT, GATED>;
+    constexpr int NA = R::NA, CW = TT / 2;  // columns per promoting warp
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *sc_full = full + 16, *sc_empty = full + 24;
+    uint64_t *d_full = full + 32, *d_empty = full + 36, *fin = full + 40;
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
+    int *abort_s = reinterpret_cast<int *>(smem + 516);
+    float *sc = reinterpret_cast<float *>(smem + R::o_sc);
+    float *part = reinterpret_cast<float *>(smem + R::o_part);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < R::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&sc_full[i], 32);
+            mbar_init(&sc_empty[i], 8);
+        }
+        for (int i = 0; i < R::kBufs; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 8);
+        }
+        mbar_init(fin, 1);
+        *abort_s = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(tmem_s, R::kCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_s;
+    pdl_wait();
+    pdl_trigger();  // after the allocation: a dependent that allocates first could never be passed
+    const bool skip = a.ctrl && ld_ctrl(a.ctrl) <= a.layer;
+    const int rank = S > 1 ? (int)cluster_rank() : 0;
+    const int first = S > 1 ? blockIdx.x / S : blockIdx.x, step = gridDim.x / S;
+    const int kb0 = (int)((long long)a.KB * rank / S), kb1 = (int)((long long)a.KB * (rank + 1) / S);
+    bool failed = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_spin_warp(bar, parity)) {
+            if (lane == 0) atomicExch(abort_s, 1);
+            failed = true;
+        }
+        return !failed;
+    };
+
+    if (skip) {
+        // nothing to do, in any CTA
+    } else if (warp == kLoadW) {
+        uint32_t n = 0;
+        for (int tile = first; tile < a.tiles && !failed; tile += step) {
+            const int tn = tile % a.tiles_n, t0 = tile / a.tiles_n * TT;
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                const int s = n % R::kStages;
+                if (n >= (uint32_t)R::kStages) {
+                    const uint32_t par = (n / R::kStages - 1) & 1;
+                    if (!wait(&empty[s], par) || !wait(&sc_empty[s], par)) break;
+                }
+                if (lane == 0) {
+                    uint8_t *st = smem + R::o_ring + s * R::kStage;
+                    mbar_arrive_expect_tx(&full[s], R::kStage);
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) tma_load_2d(st + m * kTileBytes, &a.wmap[m], kb * kG, tn * 128, &full[s]);
+                    tma_load_2d(st + NA * kTileBytes, &a.xmap, kb * kG, t0, &full[s]);
+                }
+                const uint32_t dst = smem_addr(sc + s * (TT + 4));
+#pragma unroll
+                for (int i = 0; i < (TT + 31) / 32; ++i) {
+                    const int t = 32 * i + lane;
+                    if (t < TT)
+                        cp_async_ca<4>(dst + 4 * t, a.xs + (t0 + t < a.T ? (size_t)(t0 + t) * a.KB + kb : 0),
+                                       t0 + t < a.T ? 4 : 0);
+                }
+                if (lane < NA) cp_async_ca<4>(dst + 4 * (TT + lane), a.ws[lane] + (size_t)tn * a.KB + kb, 4);
+                cp_async_arrive(&sc_full[s]);
+                __syncwarp();
+            }
+        }
+        cp_async_commit();
+        cp_async_wait_all_but<0>();
+        // copies that nobody waited for (only after a failure) land before the CTA exits
+        if (failed)
+            for (uint32_t j = n >= (uint32_t)R::kStages ? n - R::kStages : 0; j < n; ++j)
+                mbar_wait_warp(&full[j % R::kStages], (j / R::kStages) & 1);
+    } else if (warp == kMmaW) {
+        const uint32_t idesc = tc::instr_desc(0u, 128, TT);
+        uint32_t n = 0;
+        for (int tile = first; tile < a.tiles && !failed; tile += step) {
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                const int s = n % R::kStages, b = n % R::kBufs;
+                if (n >= (uint32_t)R::kBufs && !wait(&d_empty[b], (n / R::kBufs - 1) & 1)) break;
+                if (!wait(&full[s], (n / R::kStages) & 1)) break;
+                tc::fence_after();
+                if (lane == 0) {
+                    const uint32_t st = smem_addr(smem + R::o_ring + s * R::kStage);
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) {
+                        const uint64_t ad = tc::smem_desc_sw128(st + m * kTileBytes, 1024);
+                        const uint64_t bd = tc::smem_desc_sw128(st + NA * kTileBytes, 1024);
+#pragma unroll
+                        for (int k = 0; k < kG / 32; ++k)
+                            tc::mma_f8(tmem + (b * NA + m) * TT, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                    }
+                    tc::commit(&empty[s]);
+                    tc::commit(&d_full[b]);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < 8) {
+        const int qd = warp & 3, c0 = (warp >> 2) * CW;  // lane quadrant, first column
+        const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16) + c0;
+        const int row = 32 * qd + lane;
+        uint32_t n = 0;
+        for (int tile = first; tile < a.tiles && !failed; tile += step) {
+            const int tn = tile % a.tiles_n, t0 = tile / a.tiles_n * TT;
+            const int nt = a.T - t0 < TT ? a.T - t0 : TT;
+            unsigned long long acc[NA][CW / 2];
+#pragma unroll
+            for (int m = 0; m < NA; ++m)
+#pragma unroll
+                for (int j = 0; j < CW / 2; ++j) acc[m][j] = 0ull;
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                const int s = n % R::kStages, b = n % R::kBufs;
+                if (!wait(&sc_full[s], (n / R::kStages) & 1) || !wait(&d_full[b], (n / R::kBufs) & 1)) break;
+                tc::fence_after();
+                const uint32_t xa = smem_addr(sc + s * (TT + 4) + c0);
+                constexpr int C = CW < 16 ? CW : 16;
+#pragma unroll
+                for (int c = 0; c < CW; c += C) {
+                    uint32_t d[NA][C];
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) {
+                        if constexpr (C == 8) tc::ld8(trow + (b * NA + m) * TT + c, d[m]);
+                        else tc::ld16(trow + (b * NA + m) * TT + c, d[m]);
+                    }
+                    unsigned long long x2[C / 2];
+#pragma unroll
+                    for (int j = 0; j < C; j += 4) {
+                        const float4 v = lds_f4(xa + 4 * (c + j));
+                        x2[j / 2] = pack2(__float_as_uint(v.x), __float_as_uint(v.y));
+                        x2[j / 2 + 1] = pack2(__float_as_uint(v.z), __float_as_uint(v.w));
+                    }
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) {
+                        const unsigned long long w2 = dup2(sc[s * (TT + 4) + TT + m]);
+                        tc::ld_wait(d[m]);
+#pragma unroll
+                        for (int j = 0; j < C; j += 2)
+                            acc[m][(c + j) / 2] = ffma2(pack2(d[m][j], d[m][j + 1]), fmul2(x2[j / 2], w2), acc[m][(c + j) / 2]);
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&d_empty[b]);
+                    mbar_arrive(&sc_empty[s]);
+                }
+            }
+            if (GATED && S == 1) failed = epi_sync(failed);
+            if (failed) break;
+            if (S > 1) {
+#pragma unroll
+                for (int m = 0; m < NA; ++m)
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        if (c0 + j < nt)
+                            part[(m * TT + c0 + j) * 128 + row] = j & 1 ? hi2(acc[m][j / 2]) : lo2(acc[m][j / 2]);
+            } else if constexpr (!GATED) {
+                const int col = tn * 128 + row;
+                if (col < a.N) {
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) {
+                        if (c0 + j < nt) {
+                            const size_t at = (size_t)(t0 + c0 + j) * a.N + col;
+                            float v = j & 1 ? hi2(acc[0][j / 2]) : lo2(acc[0][j / 2]);
+                            if (a.res) v += load1(a.res, at, a.dtype);
+                            store1(a.y, at, v, a.dtype);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < CW; ++j) {
+                    const float g = j & 1 ? hi2(acc[0][j / 2]) : lo2(acc[0][j / 2]);
+                    const float u = j & 1 ? hi2(acc[NA - 1][j / 2]) : lo2(acc[NA - 1][j / 2]);
+                    if (c0 + j < nt) part[(c0 + j) * 128 + row] = silu(g) * u;
+                }
+                epi_sync(false);
+                for (int t = warp; t < nt; t += 8) {
+                    const float4 v = lds_f4(smem_addr(part + t * 128 + 4 * lane));
+                    float h[4] = {v.x, v.y, v.z, v.w};
+                    gated_store(a, t0 + t, tn, h);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    const bool bad = *reinterpret_cast<volatile int *>(abort_s) != 0;
+    if (S > 1) {
+        cluster_sync();
+        if (!skip && !bad) {
+            const int tn = first % a.tiles_n, t0 = first / a.tiles_n * TT;
+            const int nt = a.T - t0 < TT ? a.T - t0 : TT;
+            const uint32_t base = smem_addr(part);
+            if constexpr (!GATED) {
+                for (int e = rank * kThreads + tid; e < nt * 128; e += S * kThreads) {
+                    const int t = e >> 7, col = tn * 128 + (e & 127);
+                    float v = 0.f;
+                    for (int p = 0; p < S; ++p) v += ld_peer(peer_addr(base + 4 * e, p));
+                    if (col < a.N) {
+                        const size_t at = (size_t)(t0 + t) * a.N + col;
+                        if (a.res) v += load1(a.res, at, a.dtype);
+                        store1(a.y, at, v, a.dtype);
+                    }
+                }
+            } else {
+                for (int t = rank + S * warp; t < nt; t += S * (kThreads / 32)) {
+                    float h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float g = 0.f, u = 0.f;
+                        const uint32_t at = base + 4 * (t * 128 + 4 * lane + j);
+                        for (int p = 0; p < S; ++p) {
+                            const uint32_t pa = peer_addr(at, p);
+                            g += ld_peer(pa);
+                            u += ld_peer(pa + 4 * TT * 128);
+                        }
+                        h[j] = silu(g) * u;
+                    }
+                    __syncwarp();
+                    gated_store(a, t0 + t, tn, h);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    if (bad) {  // MMAs in flight end before tensor memory is given back
+        if (tid == 0 && a.ctrl) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
+        if (tid == kMmaW * 32) {
+            tc::commit(fin);
+            mbar_wait(fin, 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_dealloc(tmem, R::kCols);
+}
+
+// ---- wide: 128 tokens x 256 weight rows per tile -----------------------------------------------
+constexpr int kWStages = 4, kWStage = 3 * kTileBytes, kWScales = 132;   // xs of 128 tokens, ws of two blocks
+constexpr int kWoSc = 1024, kWoRing = 4096;
+constexpr int kWoOut = kWoRing + kWStages * kWStage;                    // per warp 32 x 17 floats
+constexpr int kWOutFloats = 32 * 17;
+constexpr size_t kWBytes = kWoOut + 8 * kWOutFloats * 4 + 1024;         // + the gated form's row maxima
+static_assert(kWoSc + kWStages * kWScales * 4 <= kWoRing, "the scales fit");
+static_assert(kWBytes <= 232448, "shared memory of one CTA");
+
+// 16 values of a row from column n on
+__device__ __forceinline__ void put16(const F8Args &a, float *stage, int t, int n, const float (&v0)[16], bool vec) {
+    const int lane = threadIdx.x & 31;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = v0[j];
+    if (vec && n + 16 <= a.N) {  // rows and pieces start at 16-byte boundaries
+        if (t < a.T) {
+            const size_t at = (size_t)t * a.N + n;
+            if (a.dtype == RL_F32) {
+                float *y = static_cast<float *>(a.y) + at;
+                const float *r = static_cast<const float *>(a.res) + at;
+#pragma unroll
+                for (int j = 0; j < 16; j += 8) {
+                    float w[8], e[8];
+                    if (a.res) load8(r + j, e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = a.res ? v[j + i] + e[i] : v[j + i];
+                    store8(y + j, w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j += 8) {
+                    float w[8], e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = v[j + i];
+                    if (a.dtype == RL_F16) {
+                        if (a.res) load8(static_cast<const __half *>(a.res) + at + j, e);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = a.res ? w[i] + e[i] : w[i];
+                        store8(static_cast<__half *>(a.y) + at + j, w);
+                    } else {
+                        if (a.res) load8(static_cast<const __nv_bfloat16 *>(a.res) + at + j, e);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = a.res ? w[i] + e[i] : w[i];
+                        store8(static_cast<__nv_bfloat16 *>(a.y) + at + j, w);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        return;
+    }
+    // through shared memory, so that neighbouring lanes store neighbouring values
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[j];
+    __syncwarp();
+    const int tb = t - lane;
+#pragma unroll 4
+    for (int r = lane >> 4; r < 32; r += 2) {
+        const int c = n + (lane & 15);
+        if (tb + r < a.T && c < a.N) {
+            const size_t at = (size_t)(tb + r) * a.N + c;
+            float w = stage[r * 17 + (lane & 15)];
+            if (a.res) w += load1(a.res, at, a.dtype);
+            store1(a.y, at, w, a.dtype);
+        }
+    }
+    __syncwarp();
+}
+
+// GATED: the tile's 256 weight rows are 128 rows of the gate's matrix and the same 128 of the up matrix.
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *sc_full = full + 16, *sc_empty = full + 24;
+    uint64_t *d_full = full + 32, *d_empty = full + 36, *fin = full + 40;
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
+    int *abort_s = reinterpret_cast<int *>(smem + 516);
+    float *sc = reinterpret_cast<float *>(smem + kWoSc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kWStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&sc_full[i], 32);
+            mbar_init(&sc_empty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 8);
+        }
+        mbar_init(fin, 1);
+        *abort_s = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(tmem_s, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_s;
+    pdl_wait();
+    pdl_trigger();
+    const bool skip = a.ctrl && ld_ctrl(a.ctrl) <= a.layer;
+    bool failed = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_spin_warp(bar, parity)) {
+            if (lane == 0) atomicExch(abort_s, 1);
+            failed = true;
+        }
+        return !failed;
+    };
+    const int tiles_t = (a.T + 127) / 128;  // token tiles run fastest: CTAs side by side share their weights
+
+    if (skip) {
+    } else if (warp == kLoadW) {
+        uint32_t n = 0;
+        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
+            const int t0 = tile % tiles_t * 128, j = tile / tiles_t;
+            // first weight rows of the two boxes, and their rows of scales (past the end: any, the rows are zero)
+            const int r0 = GATED ? j * 128 : j * 256, r1 = GATED ? j * 128 : j * 256 + 128;
+            const int last = (a.N - 1) / 128, s0 = r0 / 128, s1 = r1 / 128 < last ? r1 / 128 : last;
+            for (int kb = 0; kb < a.KB; ++kb, ++n) {
+                const int s = n % kWStages;
+                if (n >= (uint32_t)kWStages) {
+                    const uint32_t par = (n / kWStages - 1) & 1;
+                    if (!wait(&empty[s], par) || !wait(&sc_empty[s], par)) break;
+                }
+                if (lane == 0) {
+                    uint8_t *st = smem + kWoRing + s * kWStage;
+                    mbar_arrive_expect_tx(&full[s], kWStage);
+                    tma_load_2d(st, &a.xmap, kb * kG, t0, &full[s]);
+                    tma_load_2d(st + kTileBytes, &a.wmap[0], kb * kG, r0, &full[s]);
+                    tma_load_2d(st + 2 * kTileBytes, &a.wmap[GATED ? 1 : 0], kb * kG, r1, &full[s]);
+                }
+                const uint32_t dst = smem_addr(sc + s * kWScales);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = t0 + 32 * i + lane;
+                    cp_async_ca<4>(dst + 4 * (32 * i + lane), a.xs + (t < a.T ? (size_t)t * a.KB + kb : 0), t < a.T ? 4 : 0);
+                }
+                if (lane < 2)
+                    cp_async_ca<4>(dst + 4 * (128 + lane), a.ws[GATED ? lane : 0] + (size_t)(lane ? s1 : s0) * a.KB + kb, 4);
+                cp_async_arrive(&sc_full[s]);
+                __syncwarp();
+            }
+        }
+        cp_async_commit();
+        cp_async_wait_all_but<0>();
+        if (failed)
+            for (uint32_t j = n >= (uint32_t)kWStages ? n - kWStages : 0; j < n; ++j)
+                mbar_wait_warp(&full[j % kWStages], (j / kWStages) & 1);
+    } else if (warp == kMmaW) {
+        const uint32_t idesc = tc::instr_desc(0u, 128, 256);
+        uint32_t n = 0;
+        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
+            for (int kb = 0; kb < a.KB; ++kb, ++n) {
+                const int s = n % kWStages, b = n & 1;
+                if (n >= 2 && !wait(&d_empty[b], (n / 2 - 1) & 1)) break;
+                if (!wait(&full[s], (n / kWStages) & 1)) break;
+                tc::fence_after();
+                if (lane == 0) {
+                    const uint32_t st = smem_addr(smem + kWoRing + s * kWStage);
+                    const uint64_t ad = tc::smem_desc_sw128(st, 1024), bd = tc::smem_desc_sw128(st + kTileBytes, 1024);
+#pragma unroll
+                    for (int k = 0; k < kG / 32; ++k) tc::mma_f8(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                    tc::commit(&empty[s]);
+                    tc::commit(&d_full[b]);
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        const int qd = warp & 3, half = warp >> 2, row = 32 * qd + lane;
+        // two runs of 64 columns: neighbours, or the same rows of gate and up
+        const int col0 = GATED ? 64 * half : 128 * half, col1 = GATED ? 128 + 64 * half : 128 * half + 64;
+        const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
+        float *stage = reinterpret_cast<float *>(smem + kWoOut) + warp * kWOutFloats;
+        float *top = reinterpret_cast<float *>(smem + kWoOut + 8 * kWOutFloats * 4);  // [2][128]
+        const int es = a.dtype == RL_F32 ? 4 : 2;
+        const bool vec = ((size_t)a.N * es) % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.res)) & 15) == 0;
+        uint32_t n = 0;
+        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
+            const int t = tile % tiles_t * 128 + row, j = tile / tiles_t;
+            unsigned long long acc[2][32];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[r][i] = 0ull;
+            for (int kb = 0; kb < a.KB; ++kb, ++n) {
+                const int s = n % kWStages, b = n & 1;
+                if (!wait(&sc_full[s], (n / kWStages) & 1) || !wait(&d_full[b], (n / 2) & 1)) break;
+                tc::fence_after();
+                const float *ss = sc + s * kWScales;
+                const float x = ss[row];
+                const unsigned long long f0 = dup2(x * ss[GATED ? 128 : 128 + half]), f1 = dup2(x * ss[GATED ? 129 : 128 + half]);
+                uint32_t d[2][16];
+                tc::ld16(trow + b * 256 + col0, d[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tc::ld_wait(d[c & 1]);
+                    if (c < 7) tc::ld16(trow + b * 256 + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c + 1 - 4)), d[(c + 1) & 1]);
+                    const int r = c >> 2;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[r][8 * (c & 3) + i] = ffma2(pack2(d[c & 1][2 * i], d[c & 1][2 * i + 1]), r ? f1 : f0, acc[r][8 * (c & 3) + i]);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&d_empty[b]);
+                    mbar_arrive(&sc_empty[s]);
+                }
+            }
+            if (GATED) failed = epi_sync(failed);  // also: both halves have read the last tile's maxima
+            if (failed) break;
+            if constexpr (!GATED) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[2 * i] = lo2(acc[c >> 2][8 * (c & 3) + i]), v[2 * i + 1] = hi2(acc[c >> 2][8 * (c & 3) + i]);
+                    put16(a, stage, t, j * 256 + 128 * half + 16 * c, v, vec);
+                }
+            } else {
+                const int i0 = j * 128 + 64 * half;
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float h0 = silu(lo2(acc[0][i])) * lo2(acc[1][i]), h1 = silu(hi2(acc[0][i])) * hi2(acc[1][i]);
+                    if (i0 + 2 * i < a.N) m = max_abs_nan(m, h0);
+                    if (i0 + 2 * i + 1 < a.N) m = max_abs_nan(m, h1);
+                    acc[0][i] = pack2(__float_as_uint(h0), __float_as_uint(h1));
+                }
+                if (a.y) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[2 * i] = lo2(acc[0][8 * c + i]), v[2 * i + 1] = hi2(acc[0][8 * c + i]);
+                        put16(a, stage, t, i0 + 16 * c, v, vec);
+                    }
+                }
+                if (a.q) {
+                    top[128 * half + row] = m;
+                    epi_sync(false);
+                    m = max_nan(m, top[128 * (half ^ 1) + row]);
+                    const bool bad = !(m < INFINITY);
+                    float f = m > 0.f && !bad ? 448.f / m : 0.f, f1 = 1.f;
+                    if (f == INFINITY) f1 = 18446744073709551616.f, f = 448.f / (m * f1);  // in two steps
+                    if (half == 0 && t < a.T)
+                        a.scale[(size_t)t * a.tiles_n + j] = bad ? __int_as_float(0x7fffffff) : m / 448.f;
+                    if (t < a.T) {
+                        uint8_t *q = a.q + (size_t)t * a.N + i0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const unsigned long long p0 = acc[0][8 * c + 2 * i], p1 = acc[0][8 * c + 2 * i + 1];
+                                w[i] = f > 0.f ? pack4_e4m3(lo2(p0) * f1 * f, hi2(p0) * f1 * f, lo2(p1) * f1 * f, hi2(p1) * f1 * f) : 0u;
+                            }
+                            if ((a.N & 15) == 0 && i0 + 16 * c + 16 <= a.N && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0) {
+                                *reinterpret_cast<uint4 *>(q + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (i0 + 16 * c + i < a.N) q[16 * c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*reinterpret_cast<volatile int *>(abort_s) != 0) {
+        if (tid == 0 && a.ctrl) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
+        if (tid == kMmaW * 32) {
+            tc::commit(fin);
+            mbar_wait(fin, 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+rl_status byte_map(CUtensorMap *map, const void *base, int rows, int cols, int box_rows, const char *what) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+    if (!enc) return fail(RL_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
+    const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t gstride[1] = {(cuuint64_t)cols};
+    const cuuint32_t box[2] = {(cuuint32_t)kG, (cuuint32_t)box_rows};
+    const cuuint32_t estride[2] = {1, 1};
+    const CUresult cr = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), gdim, gstride, box, estride,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (cr != CUDA_SUCCESS) return fail(RL_ERR_CUDA, "%s: tensor map rejected (error %d)", what, (int)cr);
+    return RL_OK;
+}
+
+template <typename Kern, typename... Args>
+rl_status launch_cluster(Kern kernel, int ctas, int cluster, size_t smem, cudaStream_t s, const char *what, Args... args) {
+    rl_status st = allow_smem((const void *)kernel, smem);
+    if (st != RL_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) return fail(RL_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+    return RL_OK;
+}
+
+template <int TT, bool GATED>
+rl_status run_rows(F8Args &a, const void *x, cudaStream_t s, const char *what) {
+    rl_status st = byte_map(&a.xmap, x, a.T, a.K, TT, what);
+    if (st != RL_OK) return st;
+    const int sms = sm_count(), tt = (a.T + TT - 1) / TT;
+    a.tiles = a.tiles_n * tt;
+    int S = 1;
+    while (S < kMaxCluster && 2 * S <= a.KB && a.tiles * 2 * S <= sms) S *= 2;
+    const int ctas = S > 1 ? a.tiles * S : a.tiles < 2 * sms ? a.tiles : 2 * sms;
+    return launch_cluster(f8_rows_kernel<TT, GATED>, ctas, S, Rows<TT, GATED>::bytes(S > 1), s, what, a, S);
+}
+
+template <bool GATED>
+rl_status run_wide(F8Args &a, const void *x, cudaStream_t s, const char *what) {
+    rl_status st = byte_map(&a.xmap, x, a.T, a.K, 128, what);
+    if (st != RL_OK) return st;
+    const int per = GATED ? 128 : 256;
+    a.tiles = (a.T + 127) / 128 * ((a.N + per - 1) / per);
+    const int ctas = a.tiles < sm_count() ? a.tiles : sm_count();
+    return launch_cluster(f8_wide_kernel<GATED>, ctas, 1, kWBytes, s, what, a);
+}
+
+// shared checks; 0 rows: nothing to do
+rl_status check(const char *what, const void *const *w, const float *const *ws, int nw, int N, int K, const void *x,
+                const float *xs, int T, int32_t layer, const int32_t *ctrl) {
+    if (T < 0 || N <= 0 || K <= 0) return fail(RL_ERR_INVALID, "%s: T=%d rows=%d K=%d", what, T, N, K);
+    if (K % 16) return fail(RL_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 16", what, K);
+    if (N > (1 << 26) || K > (1 << 20) || T > (1 << 22))
+        return fail(RL_ERR_UNSUPPORTED, "%s: T=%d rows=%d K=%d (at most 2^22, 2^26, 2^20)", what, T, N, K);
+    if (ctrl && layer < 0) return fail(RL_ERR_INVALID, "%s: layer=%d", what, layer);
+    if (T == 0) return RL_OK;
+    if (!x || !xs) return fail(RL_ERR_INVALID, "%s: NULL x or x_scale", what);
+    uintptr_t p16 = reinterpret_cast<uintptr_t>(x), p4 = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ctrl);
+    for (int i = 0; i < nw; ++i) {
+        if (!w[i] || !ws[i]) return fail(RL_ERR_INVALID, "%s: NULL weights or their scales", what);
+        p16 |= reinterpret_cast<uintptr_t>(w[i]);
+        p4 |= reinterpret_cast<uintptr_t>(ws[i]);
+    }
+    if (p16 & 15) return fail(RL_ERR_INVALID, "%s: x and the weights must be 16-byte aligned", what);
+    if (p4 & 3) return fail(RL_ERR_INVALID, "%s: scales and ctrl must be 4-byte aligned", what);
+    return RL_OK;
+}
+
+rl_status fill_args(F8Args &a, const void *const *w, const float *const *ws, int nw, int N, int K, const float *xs, int T,
+                    int32_t layer, int32_t *ctrl, const char *what) {
+    for (int i = 0; i < nw; ++i) {
+        rl_status st = byte_map(&a.wmap[i], w[i], N, K, 128, what);
+        if (st != RL_OK) return st;
+        a.ws[i] = ws[i];
+    }
+    a.xs = xs;
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.KB = (K + kG - 1) / kG;
+    a.tiles_n = (N + 127) / 128;
+    a.layer = layer;
+    a.ctrl = ctrl;
+    return RL_OK;
+}
+
+bool row_type(int dt) { return dt == RL_F32 || dt == RL_F16 || dt == RL_BF16; }
+
+}  // namespace
+
+extern "C" rl_status rl_f8_matmul(const uint8_t *w, const float *w_scale, int32_t N, int32_t K, const uint8_t *x,
+                                  const float *x_scale, int32_t T, const void *res, void *y, int32_t y_dtype,
+                                  int32_t layer, int32_t *ctrl, void *stream) {
+    const char *what = "rl_f8_matmul";
+    const void *const ww[1] = {w};
+    const float *const ss[1] = {w_scale};
+    if (!row_type(y_dtype)) return fail(RL_ERR_INVALID, "%s: y_dtype %d is none of RL_F32, RL_F16, RL_BF16", what, y_dtype);
+    rl_status st = check(what, ww, ss, 1, N, K, x, x_scale, T, layer, ctrl);
+    if (st != RL_OK || T == 0) return st;
+    if (!y) return fail(RL_ERR_INVALID, "%s: NULL y", what);
+    if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(res)) % dtype_bytes(y_dtype))
+        return fail(RL_ERR_INVALID, "%s: y or res misaligned", what);
+    F8Args a = {};
+    st = fill_args(a, ww, ss, 1, N, K, x_scale, T, layer, ctrl, what);
+    if (st != RL_OK) return st;
+    a.y = y;
+    a.res = res;
+    a.dtype = y_dtype;
+    cudaStream_t s = as_stream(stream);
+    if (T <= 16) return run_rows<16, false>(a, x, s, what);
+    if (T <= 32) return run_rows<32, false>(a, x, s, what);
+    if (T <= 64) return run_rows<64, false>(a, x, s, what);
+    if (T <= 128) return run_rows<128, false>(a, x, s, what);
+    return run_wide<false>(a, x, s, what);
+}
+
+extern "C" rl_status rl_f8_gated(const uint8_t *w_gate, const float *gate_scale, const uint8_t *w_up,
+                                 const float *up_scale, int32_t I, int32_t K, const uint8_t *x, const float *x_scale,
+                                 int32_t T, void *h, int32_t h_dtype, uint8_t *q, float *scale, int32_t layer,
+                                 int32_t *ctrl, void *stream) {
+    const char *what = "rl_f8_gated";
+    const void *const ww[2] = {w_gate, w_up};
+    const float *const ss[2] = {gate_scale, up_scale};
+    if (h && !row_type(h_dtype)) return fail(RL_ERR_INVALID, "%s: h_dtype %d is none of RL_F32, RL_F16, RL_BF16", what, h_dtype);
+    rl_status st = check(what, ww, ss, 2, I, K, x, x_scale, T, layer, ctrl);
+    if (st != RL_OK || T == 0) return st;
+    if ((q == nullptr) != (scale == nullptr)) return fail(RL_ERR_INVALID, "%s: q and scale come together", what);
+    if (!h && !q) return fail(RL_ERR_INVALID, "%s: no output", what);
+    if (h && reinterpret_cast<uintptr_t>(h) % dtype_bytes(h_dtype)) return fail(RL_ERR_INVALID, "%s: h misaligned", what);
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(scale)) & 3)
+        return fail(RL_ERR_INVALID, "%s: q and scale must be 4-byte aligned", what);
+    F8Args a = {};
+    st = fill_args(a, ww, ss, 2, I, K, x_scale, T, layer, ctrl, what);
+    if (st != RL_OK) return st;
+    a.y = h;
+    a.dtype = h_dtype;
+    a.q = q;
+    a.scale = scale;
+    cudaStream_t s = as_stream(stream);
+    if (T <= 16) return run_rows<16, true>(a, x, s, what);
+    if (T <= 32) return run_rows<32, true>(a, x, s, what);
+    if (T <= 64) return run_rows<64, true>(a, x, s, what);
+    return run_wide<true>(a, x, s, what);
+}
