@@ -71,7 +71,8 @@ typedef enum rl_status {
     RL_ERR_TIMEOUT = 4      /* reserved for host-visible bounded-wait expiry */
 } rl_status;
 
-/* element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_f8_matmul, rl_f8_gated, rl_logprobs) */
+/* element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_f8_matmul, rl_f8_gated, rl_logprobs,
+ * rl_sample) */
 typedef enum rl_dtype {
     RL_F32 = 0,
     RL_F16 = 1,
@@ -499,6 +500,32 @@ rl_status rl_f8_matmul(const uint8_t *w, const float *w_scale, int32_t N, int32_
 rl_status rl_f8_gated(const uint8_t *w_gate, const float *gate_scale, const uint8_t *w_up, const float *up_scale,
                       int32_t I, int32_t K, const uint8_t *x, const float *x_scale, int32_t T, void *h,
                       int32_t h_dtype, uint8_t *q, float *scale, int32_t layer, int32_t *ctrl, void *stream);
+
+/*
+ * rl_sample - the next token of T rows of V logits, from given random numbers.  For a row with logits l,
+ * maximum m and temperature h > 0:
+ *   order: logits descending, equal values (-0.0 == +0.0) by index
+ *   A: the first top_k tokens of the order (all where top_k <= 0 or top_k >= V);  e_v = e^((l_v - m) / h)
+ *   B: the shortest prefix of A whose sum of e reaches top_p times that of A, the first token at least (A where
+ *      top_p >= 1 or NaN)
+ *   C: the tokens of B with e_v >= min_p, min_p above 1 counting as 1 (B where min_p <= 0 or NaN)
+ *   ids[t]: the first token v of C in the order of the indices with  sum of e over C up to v  >  uniform[t] *
+ *   sum of e over C (uniform is clamped to [0, 1], NaN to 0; at 1 the last token of C that has a weight)
+ *   logprob[t]: log(e_v / sum of e over C) of that token, its log probability among the kept ones
+ * A temperature of 0 (or below, or NaN), and top_k = 1, take the first token of the order (logprob 0).  A row that holds
+ * a NaN or +infinity, or nothing but -infinities, has no distribution: ids -1, logprob NaN.  Tokens at -infinity are
+ * never drawn.
+ * The sums are integer, in multiples of 2^-45 of the largest e (2^-(62 - ceil(log2 V)) beyond 2^17 tokens), so they depend
+ * on no order; each e is good to 2^-30 of itself, then rounded to such a multiple (below one it is none).
+ * Temperatures below 8.5e-39 count as that, an infinite one as the largest f32.
+ * logits [T][V] of `dtype` (RL_F32, RL_F16, RL_BF16), aligned to their element; uniform f32 [T]; temperature f32
+ * [T] or NULL (1); top_k int32 [T], top_p f32 [T], min_p f32 [T], each or NULL (off); ids int32 [T]; logprob
+ * f32 [T] or NULL.  V <= 2^26, 0 <= T <= 2^24.  No workspace: the launch may overlap with any other, and may be captured in a
+ * CUDA graph (with new numbers in `uniform` a replay draws anew).
+ */
+rl_status rl_sample(const void *logits, int32_t dtype, int32_t T, int32_t V, const float *uniform,
+                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                    int32_t *ids, float *logprob, void *stream);
 
 #ifdef __cplusplus
 }

@@ -11,4 +11,5 @@ from ._lib import (  # noqa: F401
     moe_prefill_workspace_bytes, rl_abi_version, rl_add_rmsnorm, rl_build_pairs, rl_build_pairs_workspace_bytes,
     rl_f8_gated, rl_f8_matmul, rl_fill_missing, rl_fill_workspace_bytes, rl_host_device_pointer, rl_logprobs, rl_logprobs_workspace_bytes,
     rl_q4_matvec, rl_record_bytes, rl_resolve_slots, rl_rmsnorm, rl_route, rl_route_workspace_bytes,
+    rl_sample,
 )

@@ -25,7 +25,8 @@ EXPORTS = ("rl_abi_version", "rl_last_error", "rl_record_bytes", "rl_rmsnorm", "
            "moe_prefill_chunk", "moe_prefill_chunk_f32", "moe_decode_static", "moe_decode_stack_workspace_bytes",
            "moe_decode_stack", "rl_fill_workspace_bytes", "rl_fill_missing", "rl_host_device_pointer",
            "moe_decode_stack_fill", "moe_decode_layer", "moe_decode_tokens_workspace_bytes", "moe_decode_tokens",
-           "rl_add_rmsnorm", "rl_q4_matvec", "rl_logprobs_workspace_bytes", "rl_logprobs", "rl_f8_matmul", "rl_f8_gated")
+           "rl_add_rmsnorm", "rl_q4_matvec", "rl_logprobs_workspace_bytes", "rl_logprobs", "rl_f8_matmul", "rl_f8_gated",
+           "rl_sample")
 
 RL_F32, RL_F16, RL_BF16, RL_F8_E4M3 = 0, 1, 2, 3
 RL_MAX_DECODE_TOKENS = 32
@@ -89,6 +90,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "rl_q4_matvec": (i32, [vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, i32, i32, vp]),
         "rl_f8_matmul": (i32, [vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp]),
         "rl_f8_gated": (i32, [vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, vp, vp]),
+        "rl_sample": (i32, [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
         "rl_logprobs_workspace_bytes": (sz, [i32, i32, i32]),
         "rl_logprobs": (i32, [vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
         "rl_fill_workspace_bytes": (sz, [shp]),
@@ -413,6 +415,18 @@ def rl_logprobs(logits, T, V, targets, logprob, entropy, top_n, top_ids, top_log
     x, targets, logprob, entropy, ids, top, ws = _ptrs(logits, targets, logprob, entropy, top_ids, top_logprob, ws)
     _check("rl_logprobs", load().rl_logprobs(x, dt, T, V, targets, logprob, entropy, top_n, ids, top, ws, ws_bytes,
                                              _stream(stream)))
+
+
+def rl_sample(logits, T, V, uniform, ids, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, stream=None):
+    """The next token of each row of logits [T][V] into ids (int32 [T]), drawn by uniform (f32 [T]); one temperature,
+    top_k (int32), top_p and min_p per row, each may be None."""
+    dt = _typed("logits", logits, _ROW, T * V)
+    for what, t, kind in (("uniform", uniform, "f32"), ("ids", ids, "i32"), ("temperature", temperature, "f32"),
+                          ("top_k", top_k, "i32"), ("top_p", top_p, "f32"), ("min_p", min_p, "f32"),
+                          ("logprob", logprob, "f32")):
+        _sized(what, t, kind, T)
+    x, u, temp, k, p, m, ids, lp = _ptrs(logits, uniform, temperature, top_k, top_p, min_p, ids, logprob)
+    _check("rl_sample", load().rl_sample(x, dt, T, V, u, temp, k, p, m, ids, lp, _stream(stream)))
 
 
 def rl_build_pairs_workspace_bytes(shape, T) -> int:
