@@ -10,12 +10,12 @@
 //
 //   rows  up to 128 rows per pass.  A operand: 128 weight rows, B operand: the activation rows (16, 32, 64
 //         or 128 of them), so that few rows waste no tensor work.  Lane = weight row, column = token.
-//   wide  many rows.  A operand: 128 activation rows, B operand: 256 weight rows.  Lane = token, so that a
-//         lane's scale is one number per block.
+//   wide  many rows.  A operand: 256 activation rows over a pair of CTAs, B operand: 256 weight rows.  Lane =
+//         token, so that a lane's scale is one number per block.
 //
-// Both: warps 0-7 promote (warp w reads the lanes of quadrant w % 4, a half of the columns each), warp 8
-// loads (tensor copies with the 128-byte swizzle, 4-byte asynchronous copies for the scales), one thread of
-// warp 9 issues the MMAs.
+// Both: the first 8 or 16 warps promote (warp w reads the lanes of quadrant w % 4, a share of the columns
+// each), one warp loads (tensor copies with the 128-byte swizzle, 4-byte asynchronous copies for the
+// scales), one thread of another issues the MMAs.
 #include "qdot.cuh"
 #include "row_types.cuh"
 #include "tc_desc.cuh"
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                     for (int m = 0; m < NA; ++m) tma_load_2d(st + m * kTileBytes, &a.wmap[m], kb * kG, tn * 128, &full[s]);
                     tma_load_2d(st + NA * kTileBytes, &a.xmap, kb * kG, t0, &full[s]);
                 }
+                __syncwarp();
                 const uint32_t dst = smem_addr(sc + s * (TT + 4));
 #pragma unroll
                 for (int i = 0; i < (TT + 31) / 32; ++i) {
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                     mbar_arrive(&d_empty[b]);
                     mbar_arrive(&sc_empty[s]);
                 }
+                __syncwarp();  // rejoin the warp (see cta_sync)
             }
             if (GATED && S == 1) failed = epi_sync(failed);
             if (failed) break;
@@ -422,69 +424,72 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     if (warp == 0) tc::tmem_dealloc(tmem, R::kCols);
 }
 
-// ---- wide: 128 tokens x 256 weight rows per tile -----------------------------------------------
-constexpr int kWStages = 4, kWStage = 3 * kTileBytes, kWScales = 132;   // xs of 128 tokens, ws of two blocks
-constexpr int kWoSc = 1024, kWoRing = 4096;
-constexpr int kWoOut = kWoRing + kWStages * kWStage;                    // per warp 32 x 17 floats
-constexpr int kWOutFloats = 32 * 17;
-constexpr size_t kWBytes = kWoOut + 8 * kWOutFloats * 4 + 1024;         // + the gated form's row maxima
-static_assert(kWoSc + kWStages * kWScales * 4 <= kWoRing, "the scales fit");
+// ---- wide: 256 tokens x 256 weight rows per pair of CTAs ----------------------------------------
+// A pair shares its weights: each CTA has 128 tokens (its lanes) and loads half of the 256 weight rows, so that a
+// block costs an SM 32 KB of shared memory traffic in instead of 48 KB.  Sixteen warps promote, 64 columns
+// each.  Two threads issue the MMAs of every other block: one needs about 1200 cycles for a block's two waits, four MMAs
+// and two commits beside the promoting warps, the tensor cores 512.
+constexpr int kWThreads = 640, kWEpi = 16, kWLoadW = 16, kWMmaW = 17 /* and 18 */, kWPollW = 19;
+constexpr int kWStages = 6, kWStage = 2 * kTileBytes;
+constexpr int kWScales = 132, kWSlots = 16;                              // a block's scales: 128 tokens, the two halves' weights
+constexpr int kWoRing = 1024;
+constexpr int kWoOut = kWoRing + kWStages * kWStage;                    // per warp 32 x 9 floats
+constexpr int kWOutFloats = 32 * 9;
+constexpr int kWoTop = kWoOut + kWEpi * kWOutFloats * 4;                // gated: maxima of [4][128] row quarters
+constexpr int kWoSc = kWoTop + 4 * 128 * 4;
+constexpr size_t kWBytes = kWoSc + kWSlots * kWScales * 4;
 static_assert(kWBytes <= 232448, "shared memory of one CTA");
 
-// 16 values of a row from column n on
-__device__ __forceinline__ void put16(const F8Args &a, float *stage, int t, int n, const float (&v0)[16], bool vec) {
-    const int lane = threadIdx.x & 31;
-    float v[16];
+__device__ __forceinline__ void wide_sync() {  // the sixteen promoting warps
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    __syncwarp();
+}
+// Arrive on an mbarrier of the cluster, by its address there.  Relaxed: what it tells of are reads of tensor memory that
+// have returned their values; it publishes no memory (a release would also wait for the loads of the next scales).
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// tma_load_2d into this CTA's shared memory, completing on the mbarrier `bar` of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <typename E>
+__device__ __forceinline__ void put8_as(const F8Args &a, size_t at, float (&v)[8]) {
+    if (a.res) {
+        float e[8];
+        load8(static_cast<const E *>(a.res) + at, e);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = v0[j];
-    if (vec && n + 16 <= a.N) {  // rows and pieces start at 16-byte boundaries
+        for (int i = 0; i < 8; ++i) v[i] += e[i];
+    }
+    store8(static_cast<E *>(a.y) + at, v);
+}
+// 8 values of this lane's row t from column n on
+__device__ __forceinline__ void put8(const F8Args &a, float *stage, int t, int n, float (&v)[8], bool vec) {
+    if (vec && n + 8 <= a.N) {  // rows and pieces start at 16-byte boundaries
         if (t < a.T) {
             const size_t at = (size_t)t * a.N + n;
-            if (a.dtype == RL_F32) {
-                float *y = static_cast<float *>(a.y) + at;
-                const float *r = static_cast<const float *>(a.res) + at;
-#pragma unroll
-                for (int j = 0; j < 16; j += 8) {
-                    float w[8], e[8];
-                    if (a.res) load8(r + j, e);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = a.res ? v[j + i] + e[i] : v[j + i];
-                    store8(y + j, w);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; j += 8) {
-                    float w[8], e[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = v[j + i];
-                    if (a.dtype == RL_F16) {
-                        if (a.res) load8(static_cast<const __half *>(a.res) + at + j, e);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] = a.res ? w[i] + e[i] : w[i];
-                        store8(static_cast<__half *>(a.y) + at + j, w);
-                    } else {
-                        if (a.res) load8(static_cast<const __nv_bfloat16 *>(a.res) + at + j, e);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] = a.res ? w[i] + e[i] : w[i];
-                        store8(static_cast<__nv_bfloat16 *>(a.y) + at + j, w);
-                    }
-                }
-            }
+            if (a.dtype == RL_F32) put8_as<float>(a, at, v);
+            else if (a.dtype == RL_F16) put8_as<__half>(a, at, v);
+            else put8_as<__nv_bfloat16>(a, at, v);
         }
         __syncwarp();
         return;
     }
     // through shared memory, so that neighbouring lanes store neighbouring values
+    const int lane = threadIdx.x & 31, tb = t - lane, c = n + (lane & 7);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[j];
+    for (int j = 0; j < 8; ++j) stage[lane * 9 + j] = v[j];
     __syncwarp();
-    const int tb = t - lane;
-#pragma unroll 4
-    for (int r = lane >> 4; r < 32; r += 2) {
-        const int c = n + (lane & 15);
+#pragma unroll 2
+    for (int r = lane >> 3; r < 32; r += 4) {
         if (tb + r < a.T && c < a.N) {
             const size_t at = (size_t)(tb + r) * a.N + c;
-            float w = stage[r * 17 + (lane & 15)];
+            float w = stage[r * 9 + (lane & 7)];
             if (a.res) w += load1(a.res, at, a.dtype);
             store1(a.y, at, w, a.dtype);
         }
@@ -492,168 +497,213 @@ __device__ __forceinline__ void put16(const F8Args &a, float *stage, int t, int 
     __syncwarp();
 }
 
-// GATED: the tile's 256 weight rows are 128 rows of the gate's matrix and the same 128 of the up matrix.
+// GATED: the 256 weight rows are 128 rows of the gate's matrix and the same 128 of the up matrix.
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
+__global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *sc_full = full + 16, *sc_empty = full + 24;
-    uint64_t *d_full = full + 32, *d_empty = full + 36, *fin = full + 40;
+    // full and d_empty: of the even CTA, for both; the others: of each CTA
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *d_full = full + 16, *d_empty = full + 18;
+    uint64_t *fin = full + 20, *sc_full = full + 21;
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
-    int *abort_s = reinterpret_cast<int *>(smem + 516);
+    int *abort_s = reinterpret_cast<int *>(smem + 516), *leave_s = reinterpret_cast<int *>(smem + 520);
     float *sc = reinterpret_cast<float *>(smem + kWoSc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank();
 
     if (tid == 0) {
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-            mbar_init(&sc_full[i], 32);
-            mbar_init(&sc_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 8);
+            mbar_init(&d_empty[i], 2 * kWEpi);
         }
-        mbar_init(fin, 1);
-        *abort_s = 0;
+        for (int i = 0; i < 2; ++i) mbar_init(&sc_full[i], 32);
+        mbar_init(fin, 2);
+        *abort_s = *leave_s = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
-        tc::tmem_alloc(tmem_s, 512);
-        tc::tmem_relinquish();
+        tc::tmem_alloc_pair(tmem_s, 512);
+        tc::tmem_relinquish_pair();
     }
     tc::fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers and tensor memory are there
     tc::fence_after();
     const uint32_t tmem = *tmem_s;
     pdl_wait();
     pdl_trigger();
     const bool skip = a.ctrl && ld_ctrl(a.ctrl) <= a.layer;
     bool failed = false;
+    // Waits of one thread.  A poll occupies the pipe that every shared-memory operation takes: with sixteen warps
+    // polling for themselves each load, arrival and read of tensor memory took about 300 cycles.  So one warp waits
+    // for the promoting ones, which park at CTA barriers.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_spin_warp(bar, parity)) {
-            if (lane == 0) atomicExch(abort_s, 1);
-            failed = true;
-        }
-        return !failed;
+        for (uint32_t i = 0; i < kSpinPolls; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        atomicExch(abort_s, 1);
+        failed = true;
+        return false;
     };
-    const int tiles_t = (a.T + 127) / 128;  // token tiles run fastest: CTAs side by side share their weights
+    const int tiles_t = (a.T + 255) / 256;  // token tiles run fastest: pairs side by side share their weights
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    if (skip) {
-    } else if (warp == kLoadW) {
-        uint32_t n = 0;
-        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
-            const int t0 = tile % tiles_t * 128, j = tile / tiles_t;
-            // first weight rows of the two boxes, and their rows of scales (past the end: any, the rows are zero)
-            const int r0 = GATED ? j * 128 : j * 256, r1 = GATED ? j * 128 : j * 256 + 128;
-            const int last = (a.N - 1) / 128, s0 = r0 / 128, s1 = r1 / 128 < last ? r1 / 128 : last;
-            for (int kb = 0; kb < a.KB; ++kb, ++n) {
-                const int s = n % kWStages;
-                if (n >= (uint32_t)kWStages) {
-                    const uint32_t par = (n / kWStages - 1) & 1;
-                    if (!wait(&empty[s], par) || !wait(&sc_empty[s], par)) break;
+    // registers: 640 threads at 96 = 512 promoting ones at 104 + 128 at 64
+    if (warp >= kWEpi) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (!skip && warp == kWLoadW) {
+            uint32_t s = 0, par = 1, n = 0;  // stage; parity of its last release (the first round passes); block
+            const uint32_t full0 = peer_addr(smem_addr(full), 0);
+            // Scales: copied for eight blocks at a time into a ring of sixteen slots (loads by the promoting warps,
+            // a block ahead, cost a quarter of the time: every eighth block they wait for L2).  This lane copies for block
+            // m = 8 batch + (lane & 7), tokens 4 i + (lane >> 3).
+            const uint32_t blocks = (uint32_t)(first < a.tiles ? (a.tiles - 1 - first) / step + 1 : 0) * a.KB;
+            uint32_t m = lane & 7;
+            int mtile = first, mkb = lane & 7;
+            for (int tile = first; tile < a.tiles && !failed; tile += step) {
+                const int t0 = tile % tiles_t * 256 + 128 * rank, j = tile / tiles_t;
+                const int r0 = GATED ? j * 128 : j * 256 + 128 * rank;  // this CTA's weight rows
+                const CUtensorMap *wmap = &a.wmap[GATED ? rank : 0];
+                for (int kb = 0; kb < a.KB; ++kb, ++n) {
+                    if (lane == 0 && wait(&empty[s], par)) {
+                        uint8_t *st = smem + kWoRing + s * kWStage;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kWStage);
+                        tma_load_2d_pair(st, &a.xmap, kb * kG, t0, full0 + 8 * s);
+                        tma_load_2d_pair(st + kTileBytes, wmap, kb * kG, r0, full0 + 8 * s);
+                    }
+                    __syncwarp();
+                    if (__any_sync(kFull, failed)) {
+                        failed = true;
+                        break;
+                    }
+                    if (++s == kWStages) s = 0, par ^= 1;
+                    if ((n & 7) == 0) {
+                        // the MMAs of block n - 6 are done, so block n - 8 and the ones before it were released
+                        while (mkb >= a.KB) mkb -= a.KB, mtile += step;
+                        if (m < blocks) {
+                            const int mt = mtile % tiles_t * 256 + 128 * rank, mj = mtile / tiles_t;
+                            const uint32_t dst = smem_addr(sc + (m % kWSlots) * kWScales);
+#pragma unroll 4
+                            for (int i = lane >> 3; i < 128; i += 4)
+                                cp_async_ca<4>(dst + 4 * i, a.xs + (mt + i < a.T ? (size_t)(mt + i) * a.KB + mkb : 0), mt + i < a.T ? 4 : 0);
+                            if (lane < 16) {  // of both halves of the weight rows (past the end: any, their products are zero)
+                                const int half = lane >> 3, last = (a.N - 1) / 128, nb = GATED ? mj : 2 * mj + half;
+                                cp_async_ca<4>(dst + 4 * (128 + half), a.ws[GATED ? half : 0] + (size_t)(nb < last ? nb : last) * a.KB + mkb, 4);
+                            }
+                        }
+                        cp_async_arrive(&sc_full[(n >> 3) & 1]);
+                        m += 8;
+                        mkb += 8;
+                        __syncwarp();
+                    }
                 }
-                if (lane == 0) {
-                    uint8_t *st = smem + kWoRing + s * kWStage;
-                    mbar_arrive_expect_tx(&full[s], kWStage);
-                    tma_load_2d(st, &a.xmap, kb * kG, t0, &full[s]);
-                    tma_load_2d(st + kTileBytes, &a.wmap[0], kb * kG, r0, &full[s]);
-                    tma_load_2d(st + 2 * kTileBytes, &a.wmap[GATED ? 1 : 0], kb * kG, r1, &full[s]);
-                }
-                const uint32_t dst = smem_addr(sc + s * kWScales);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = t0 + 32 * i + lane;
-                    cp_async_ca<4>(dst + 4 * (32 * i + lane), a.xs + (t < a.T ? (size_t)t * a.KB + kb : 0), t < a.T ? 4 : 0);
-                }
-                if (lane < 2)
-                    cp_async_ca<4>(dst + 4 * (128 + lane), a.ws[GATED ? lane : 0] + (size_t)(lane ? s1 : s0) * a.KB + kb, 4);
-                cp_async_arrive(&sc_full[s]);
-                __syncwarp();
             }
+            cp_async_commit();
+            cp_async_wait_all_but<0>();
+            if (failed)  // copies in flight land within microseconds; nobody waits for them any more
+                for (int i = 0; i < 4096; ++i) __nanosleep(1000);
+            __syncwarp();
         }
-        cp_async_commit();
-        cp_async_wait_all_but<0>();
-        if (failed)
-            for (uint32_t j = n >= (uint32_t)kWStages ? n - kWStages : 0; j < n; ++j)
-                mbar_wait_warp(&full[j % kWStages], (j / kWStages) & 1);
-    } else if (warp == kMmaW) {
-        const uint32_t idesc = tc::instr_desc(0u, 128, 256);
-        uint32_t n = 0;
-        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
-            for (int kb = 0; kb < a.KB; ++kb, ++n) {
-                const int s = n % kWStages, b = n & 1;
-                if (n >= 2 && !wait(&d_empty[b], (n / 2 - 1) & 1)) break;
-                if (!wait(&full[s], (n / kWStages) & 1)) break;
+        if (!skip && (warp == kWMmaW || warp == kWMmaW + 1) && rank == 0 && lane == 0) {
+            // blocks b, b + 2, .. of all that this CTA goes through, into accumulator b
+            const uint32_t b = warp - kWMmaW, idesc = tc::instr_desc(0u, 256, 256), ring = smem_addr(smem + kWoRing);
+            const uint32_t blocks = (uint32_t)(first < a.tiles ? (a.tiles - 1 - first) / step + 1 : 0) * a.KB;
+            uint32_t s = b, par = 0, dpar = 1;
+            for (uint32_t n = b; n < blocks; n += 2) {
+                if (!wait(&full[s], par) || !wait(&d_empty[b], dpar)) break;
                 tc::fence_after();
-                if (lane == 0) {
-                    const uint32_t st = smem_addr(smem + kWoRing + s * kWStage);
-                    const uint64_t ad = tc::smem_desc_sw128(st, 1024), bd = tc::smem_desc_sw128(st + kTileBytes, 1024);
+                const uint32_t st = ring + s * kWStage;
+                const uint64_t ad = tc::smem_desc_sw128(st, 1024), bd = tc::smem_desc_sw128(st + kTileBytes, 1024);
 #pragma unroll
-                    for (int k = 0; k < kG / 32; ++k) tc::mma_f8(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-                    tc::commit(&empty[s]);
-                    tc::commit(&d_full[b]);
-                }
-                __syncwarp();
+                for (int k = 0; k < kG / 32; ++k) tc::mma_f8_pair(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                tc::commit_pair(&d_full[b]);
+                tc::commit_pair(&empty[s]);
+                dpar ^= 1;
+                s += 2;
+                if (s >= kWStages) s -= kWStages, par ^= 1;
             }
         }
+        if (!skip && warp == kWPollW) {
+            // Waits for each block's product and lets the two groups of eight promoting warps pass their barrier of its
+            // buffer (ids 2 + buffer and 4 + buffer); the next arrival there comes after both have released the buffer.
+            const uint32_t blocks = (uint32_t)(first < a.tiles ? (a.tiles - 1 - first) / step + 1 : 0) * a.KB;
+            for (uint32_t n = 0; n < blocks; ++n) {
+                bool ok = true;
+                if (lane == 0 && (((n & 7) == 0 && !wait(&sc_full[(n >> 3) & 1], (n >> 4) & 1)) || !wait(&d_full[n & 1], (n >> 1) & 1))) {
+                    ok = false;
+                    *reinterpret_cast<volatile int *>(leave_s) = 1;
+                    __threadfence_block();
+                }
+                __syncwarp();
+                ok = __all_sync(kFull, ok);
+                asm volatile("bar.arrive %0, 288;\n\tbar.arrive %1, 288;" ::"r"(2 + (n & 1)), "r"(4 + (n & 1)) : "memory");
+                if (!ok) break;
+            }
+        }
+        __syncwarp();
     } else {
-        const int qd = warp & 3, half = warp >> 2, row = 32 * qd + lane;
-        // two runs of 64 columns: neighbours, or the same rows of gate and up
-        const int col0 = GATED ? 64 * half : 128 * half, col1 = GATED ? 128 + 64 * half : 128 * half + 64;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int qd = warp & 3, part = warp >> 2, group = warp >> 3, row = 32 * qd + lane;
+        // two runs of 32 columns: neighbours, or the same rows of gate and up
+        const int col0 = GATED ? 32 * part : 64 * part, col1 = col0 + (GATED ? 128 : 32);
         const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
+        const uint32_t release = peer_addr(smem_addr(d_empty), 0);
         float *stage = reinterpret_cast<float *>(smem + kWoOut) + warp * kWOutFloats;
-        float *top = reinterpret_cast<float *>(smem + kWoOut + 8 * kWOutFloats * 4);  // [2][128]
+        float *top = reinterpret_cast<float *>(smem + kWoTop);
         const int es = a.dtype == RL_F32 ? 4 : 2;
         const bool vec = ((size_t)a.N * es) % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.res)) & 15) == 0;
         uint32_t n = 0;
-        for (int tile = blockIdx.x; tile < a.tiles && !failed; tile += gridDim.x) {
-            const int t = tile % tiles_t * 128 + row, j = tile / tiles_t;
-            unsigned long long acc[2][32];
+        for (int tile = skip ? a.tiles : first; tile < a.tiles && !failed; tile += step) {
+            const int t = tile % tiles_t * 256 + 128 * rank + row, j = tile / tiles_t;
+            unsigned long long acc[2][16];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[r][i] = 0ull;
+                for (int i = 0; i < 16; ++i) acc[r][i] = 0ull;
             for (int kb = 0; kb < a.KB; ++kb, ++n) {
-                const int s = n % kWStages, b = n & 1;
-                if (!wait(&sc_full[s], (n / kWStages) & 1) || !wait(&d_full[b], (n / 2) & 1)) break;
-                tc::fence_after();
-                const float *ss = sc + s * kWScales;
-                const float x = ss[row];
-                const unsigned long long f0 = dup2(x * ss[GATED ? 128 : 128 + half]), f1 = dup2(x * ss[GATED ? 129 : 128 + half]);
-                uint32_t d[2][16];
-                tc::ld16(trow + b * 256 + col0, d[0]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tc::ld_wait(d[c & 1]);
-                    if (c < 7) tc::ld16(trow + b * 256 + (c + 1 < 4 ? col0 + 16 * (c + 1) : col1 + 16 * (c + 1 - 4)), d[(c + 1) & 1]);
-                    const int r = c >> 2;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[r][8 * (c & 3) + i] = ffma2(pack2(d[c & 1][2 * i], d[c & 1][2 * i + 1]), r ? f1 : f0, acc[r][8 * (c & 3) + i]);
-                }
-                tc::fence_before();
+                const int b = n & 1;
+                asm volatile("bar.sync %0, 288;" ::"r"(2 + 2 * group + b) : "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&d_empty[b]);
-                    mbar_arrive(&sc_empty[s]);
+                if (*reinterpret_cast<volatile int *>(leave_s)) {  // the same for all sixteen warps: set before the arrival
+                    failed = true;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t db = trow + b * 256;
+                const float *ss = sc + (n % kWSlots) * kWScales;
+                const float x = ss[row], f0 = x * ss[128 + (GATED ? 0 : group)], f1 = GATED ? x * ss[129] : f0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t d[16];
+                    tc::ld16(db + (c < 2 ? col0 : col1) + 16 * (c & 1), d);
+                    tc::ld_wait(d);
+                    if (c == 3) {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(release + 8 * b);
+                        __syncwarp();  // rejoin the warp (see cta_sync)
+                    }
+                    const unsigned long long f = dup2(c < 2 ? f0 : f1);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[c >> 1][8 * (c & 1) + i] = ffma2(pack2(d[2 * i], d[2 * i + 1]), f, acc[c >> 1][8 * (c & 1) + i]);
                 }
             }
-            if (GATED) failed = epi_sync(failed);  // also: both halves have read the last tile's maxima
             if (failed) break;
             if constexpr (!GATED) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    float v[16];
+                    float v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[2 * i] = lo2(acc[c >> 2][8 * (c & 3) + i]), v[2 * i + 1] = hi2(acc[c >> 2][8 * (c & 3) + i]);
-                    put16(a, stage, t, j * 256 + 128 * half + 16 * c, v, vec);
+                    for (int i = 0; i < 4; ++i) v[2 * i] = lo2(acc[c >> 2][4 * (c & 3) + i]), v[2 * i + 1] = hi2(acc[c >> 2][4 * (c & 3) + i]);
+                    put8(a, stage, t, j * 256 + 64 * part + 8 * c, v, vec);
                 }
             } else {
-                const int i0 = j * 128 + 64 * half;
+                const int i0 = j * 128 + 32 * part;
                 float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const float h0 = silu(lo2(acc[0][i])) * lo2(acc[1][i]), h1 = silu(hi2(acc[0][i])) * hi2(acc[1][i]);
                     if (i0 + 2 * i < a.N) m = max_abs_nan(m, h0);
                     if (i0 + 2 * i + 1 < a.N) m = max_abs_nan(m, h1);
@@ -662,32 +712,34 @@ __global__ void __launch_bounds__(kThreads, 1) f8_wide_kernel(const __grid_const
                 if (a.y) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float v[16];
+                        float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[2 * i] = lo2(acc[0][8 * c + i]), v[2 * i + 1] = hi2(acc[0][8 * c + i]);
-                        put16(a, stage, t, i0 + 16 * c, v, vec);
+                        for (int i = 0; i < 4; ++i) v[2 * i] = lo2(acc[0][4 * c + i]), v[2 * i + 1] = hi2(acc[0][4 * c + i]);
+                        put8(a, stage, t, i0 + 8 * c, v, vec);
                     }
                 }
                 if (a.q) {
-                    top[128 * half + row] = m;
-                    epi_sync(false);
-                    m = max_nan(m, top[128 * (half ^ 1) + row]);
+                    wide_sync();  // every warp has read the last tile's maxima
+                    top[128 * part + row] = m;
+                    wide_sync();
+                    m = max_nan(max_nan(top[row], top[128 + row]), max_nan(top[256 + row], top[384 + row]));
                     const bool bad = !(m < INFINITY);
                     float f = m > 0.f && !bad ? 448.f / m : 0.f, f1 = 1.f;
                     if (f == INFINITY) f1 = 18446744073709551616.f, f = 448.f / (m * f1);  // in two steps
-                    if (half == 0 && t < a.T)
+                    if (part == 0 && t < a.T)
                         a.scale[(size_t)t * a.tiles_n + j] = bad ? __int_as_float(0x7fffffff) : m / 448.f;
                     if (t < a.T) {
                         uint8_t *q = a.q + (size_t)t * a.N + i0;
+                        const bool vec_q = (a.N & 15) == 0 && i0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 2; ++c) {
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const unsigned long long p0 = acc[0][8 * c + 2 * i], p1 = acc[0][8 * c + 2 * i + 1];
                                 w[i] = f > 0.f ? pack4_e4m3(lo2(p0) * f1 * f, hi2(p0) * f1 * f, lo2(p1) * f1 * f, hi2(p1) * f1 * f) : 0u;
                             }
-                            if ((a.N & 15) == 0 && i0 + 16 * c + 16 <= a.N && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0) {
+                            if (vec_q) {
                                 *reinterpret_cast<uint4 *>(q + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
                             } else {
 #pragma unroll
@@ -705,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) f8_wide_kernel(const __grid_const
     __syncthreads();
     if (*reinterpret_cast<volatile int *>(abort_s) != 0) {
         if (tid == 0 && a.ctrl) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
-        if (tid == kMmaW * 32) {
-            tc::commit(fin);
+        if (rank == 0 && lane == 0 && (warp == kWMmaW || warp == kWMmaW + 1)) {
+            tc::commit_pair(fin);  // MMAs in flight end before tensor memory is given back
             mbar_wait(fin, 0);
         }
         __syncwarp();
@@ -714,8 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1) f8_wide_kernel(const __grid_const
     }
     tc::fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's operands and barriers are no longer used
     tc::fence_after();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    if (warp == 0) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 // ---- host side ----------------------------------------------------------------------------------
@@ -734,12 +787,12 @@ rl_status byte_map(CUtensorMap *map, const void *base, int rows, int cols, int b
 }
 
 template <typename Kern, typename... Args>
-rl_status launch_cluster(Kern kernel, int ctas, int cluster, size_t smem, cudaStream_t s, const char *what, Args... args) {
+rl_status launch_cluster(Kern kernel, int ctas, int threads, int cluster, size_t smem, cudaStream_t s, const char *what, Args... args) {
     rl_status st = allow_smem((const void *)kernel, smem);
     if (st != RL_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -764,7 +817,7 @@ rl_status run_rows(F8Args &a, const void *x, cudaStream_t s, const char *what) {
     int S = 1;
     while (S < kMaxCluster && 2 * S <= a.KB && a.tiles * 2 * S <= sms) S *= 2;
     const int ctas = S > 1 ? a.tiles * S : a.tiles < 2 * sms ? a.tiles : 2 * sms;
-    return launch_cluster(f8_rows_kernel<TT, GATED>, ctas, S, Rows<TT, GATED>::bytes(S > 1), s, what, a, S);
+    return launch_cluster(f8_rows_kernel<TT, GATED>, ctas, kThreads, S, Rows<TT, GATED>::bytes(S > 1), s, what, a, S);
 }
 
 template <bool GATED>
@@ -772,9 +825,9 @@ rl_status run_wide(F8Args &a, const void *x, cudaStream_t s, const char *what) {
     rl_status st = byte_map(&a.xmap, x, a.T, a.K, 128, what);
     if (st != RL_OK) return st;
     const int per = GATED ? 128 : 256;
-    a.tiles = (a.T + 127) / 128 * ((a.N + per - 1) / per);
-    const int ctas = a.tiles < sm_count() ? a.tiles : sm_count();
-    return launch_cluster(f8_wide_kernel<GATED>, ctas, 1, kWBytes, s, what, a);
+    a.tiles = (a.T + 255) / 256 * ((a.N + per - 1) / per);
+    const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
+    return launch_cluster(f8_wide_kernel<GATED>, 2 * pairs, kWThreads, 2, kWBytes, s, what, a);
 }
 
 // shared checks; 0 rows: nothing to do
