@@ -90,10 +90,9 @@ struct Shared {
     int mine, found;
     Factor fac;
     float bound;
-    double gap;              // -temperature ln(min_p), or negative: off
     int32_t table[32];
     int k;
-    float p, u;
+    float p, u, min_p;
 };
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -143,22 +142,77 @@ __device__ __forceinline__ void exponent(float l, float m, Factor c, float &t, f
     t = d * c.hi;
     t_lo = fmaf(e, c.hi, fmaf(d * c.pre, c.lo, fmaf(d, c.hi, -t)));
 }
-// w(l) in multiples of 2^-shift, rounded to the nearest; 0 from 2^-shift down and for -infinity
-__device__ __forceinline__ u64 weight(float l, float m, Factor c, int shift, const int32_t *table) {
-    float t, t_lo;
-    exponent(l, m, c, t, t_lo);
-    const bool none = !(t > -(float)shift);
-    t = none ? 0.f : t;
-    const float kf = t + 393216.f;  // 1.5 * 2^18: the nearest multiple of 1 / 32
-    const int k = __float_as_int(kf) - __float_as_int(393216.f);
-    const float r = (t - (kf - 393216.f)) + (none ? 0.f : t_lo);
-    // e^(r ln 2) - 1, |r| <= 1 / 64: the fifth term is below 2^-39
-    const float p = r * fmaf(r, fmaf(r, fmaf(r, 9.618129e-3f, 5.550411e-2f), 0.24022651f), 0.69314718f);
-    const int P = __float2int_rn(p * 4294967296.f);
-    const int32_t T = table[k & 31];
-    const u64 e = (u64)((long long)T * P + ((long long)T << 32));  // 2^62 ... 2^63
-    return none ? 0ull : ((e >> (61 - shift - (k >> 5))) + 1ull) >> 1;
+
+// ceil(p * total) and floor(p * total) for 0 <= p < 1, exactly: p is an integer over a power of two
+__device__ __forceinline__ u64 share(float p, u64 total, bool up) {
+    const uint32_t bits = __float_as_uint(p), ex = bits >> 23;
+    const u64 mant = ex ? (bits & 0x7fffffu) | 0x800000u : bits;
+    const int sh = ex ? 150 - (int)ex : 149;  // p = mant / 2^sh, sh >= 24
+    const u64 lo = mant * total, hi = __umul64hi(mant, total);
+    u64 q, rest;
+    if (sh < 64) {
+        q = (hi << (64 - sh)) | (lo >> sh);
+        rest = lo & ((1ull << sh) - 1ull);
+    } else {
+        const int s2 = sh - 64;
+        q = s2 < 64 ? hi >> s2 : 0ull;
+        rest = lo | (s2 < 64 ? hi & ((1ull << s2) - 1ull) : hi);
+    }
+    return q + (up && rest ? 1ull : 0ull);
 }
+
+// The steps of w(l) for two logits (packed f32 pairs); one logit is the same with both halves alike.  Valid for
+// t = (l - m) log2(e) / temperature in [-shift, 0], anything below (the callers leave that out).
+//   d + e = l - m exactly (two-sum);  k / 32 = t rounded (the magic sum leaves k in the low bits);  r = t - k / 32
+//   P = 2^32 (e^(r ln 2) - 1), |r| <= 1 / 64: the fifth term of the series is below 2^-39
+//   w = 2^(k / 32 + shift) (1 + P / 2^32), truncated and made odd, which is off by at most a unit to either side and not
+//   on the average (131072 truncations would sum up to 2^-30 of the largest w)
+struct Weigh {
+    u64 m, nm, hi, lo, pre;
+    int sh;
+    uint32_t table;
+    static constexpr float kMagic = 393216.f;  // 1.5 * 2^18: sums with it are rounded to multiples of 1 / 32
+    static __device__ __forceinline__ u64 both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+    static __device__ __forceinline__ u64 add2(u64 a, u64 b) {
+        u64 d;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+        return d;
+    }
+    static __device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+        u64 d;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+        return d;
+    }
+    __device__ __forceinline__ void set(float max, Factor c, int shift, const int32_t *tab) {
+        m = both(max), nm = both(-max), hi = both(c.hi), lo = both(c.lo), pre = both(c.pre);
+        sh = 62 - shift + (__float_as_int(kMagic) >> 5);
+        table = smem_addr(tab);
+    }
+    __device__ __forceinline__ u64 finish(uint32_t kf, uint32_t p) const {
+        const int P = __float2int_rn(__uint_as_float(p));
+        int32_t T;
+        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(T) : "r"(table + ((kf & 31u) << 2)));
+        const u64 e = (u64)((long long)T * P + ((long long)T << 32));  // 2^62 ... 2^63
+        return (e >> ((sh - (int)(kf >> 5)) & 63)) | 1ull;
+    }
+    __device__ __forceinline__ void pair(float l0, float l1, u64 &w0, u64 &w1) const {
+        const u64 l = pack2(__float_as_uint(l0), __float_as_uint(l1)), neg = both(-1.f), magic = both(kMagic);
+        const u64 d = add2(l, nm), b = add2(d, m), e = add2(ffma2(b, neg, l), add2(ffma2(d, neg, b), nm));
+        const u64 kf = ffma2(d, hi, magic);
+        u64 r = ffma2(d, hi, ffma2(kf, neg, magic));
+        r = ffma2(mul2(d, pre), lo, ffma2(e, hi, r));
+        u64 q = ffma2(r, both(9.618129e-3f * 4294967296.f), both(5.550411e-2f * 4294967296.f));
+        q = ffma2(q, r, both(0.24022651f * 4294967296.f));
+        q = mul2(ffma2(q, r, both(0.69314718f * 4294967296.f)), r);
+        w0 = finish((uint32_t)kf, (uint32_t)q);
+        w1 = finish((uint32_t)(kf >> 32), (uint32_t)(q >> 32));
+    }
+    __device__ __forceinline__ u64 one(float l) const {
+        u64 a, b;
+        pair(l, l, a, b);
+        return a;
+    }
+};
 
 // The row's pieces of 16 bytes.  Piece i of the row starts at value i EV - skew, so that it lies on a 16-byte
 // boundary; values outside the row are -infinity.  Warp w of CTA c takes the pieces from (16 c + w) 32 iters on.
@@ -267,52 +321,105 @@ struct Sampler {
     u64 *list, *sorted;                  // kCap keys each; together the histograms
     R row;
     int rank, lane, warp;
-    float m;
+    float m, least;                      // least: the smallest logit that has a weight
     Factor fac;
+    Weigh weigh;
+    float bin_scale;                     // bins per unit of the logit
 
+    // bins of equal width in the logit, 0 at the maximum; monotone
+    __device__ __forceinline__ int bin(float l) const { return min((int)((m - l) * bin_scale), kBins - 1); }
     // the sum that the tokens kept by top-p reach: a share p < 1 of `total`, at least the first token's
     __device__ __forceinline__ u64 share_of(u64 total) const {
-        const u64 t = (u64)ceil((double)sh.p * (double)total);
+        const u64 t = share(sh.p, total, true);
         return t > 0ull ? t : 1ull;
     }
-    __device__ __forceinline__ u64 w_of(float l) const { return weight(l, m, fac, a.shift, sh.table); }
+    __device__ __forceinline__ u64 w_of(float l) const { return weigh.one(l); }
+    // the sum of w over the values of a piece for which bit j of `in` is set
+    static __device__ __forceinline__ u64 sum_in(const Weigh &weigh, const float (&v)[EV], uint32_t in) {
+        u64 sum = 0ull;
+#pragma unroll
+        for (int j = 0; j < EV; j += 2) {
+            u64 w0, w1;
+            weigh.pair(v[j], v[j + 1], w0, w1);
+            if (in >> j & 1u) sum += w0;
+            if (in >> (j + 1) & 1u) sum += w1;
+        }
+        return sum;
+    }
+    static __device__ __forceinline__ uint32_t at_least(const float (&v)[EV], float lo) {
+        uint32_t in = 0u;
+#pragma unroll
+        for (int j = 0; j < EV; ++j) in |= v[j] >= lo ? 1u << j : 0u;
+        return in;
+    }
+    // bit j: value j of the piece at `i0` is kept (its logit lies above `lo`, the border's, or its key not below)
+    static __device__ __forceinline__ uint32_t kept(const float (&v)[EV], int i0, float lo, u64 border) {
+        uint32_t in = 0u, even = 0u;
+#pragma unroll
+        for (int j = 0; j < EV; ++j) {
+            in |= v[j] > lo ? 1u << j : 0u;
+            even |= v[j] == lo ? 1u << j : 0u;
+        }
+        const uint32_t bk = (uint32_t)(border >> 32);
+        while (even) {  // equal logits: up to the border's index (all where the border lies below)
+            const int j = __ffs(even) - 1;
+            even &= even - 1u;
+            if (make_key(order_key(lo), i0 + j) >= border || bk == 0u) in |= 1u << j;
+        }
+        return in;
+    }
 
     // Tokens whose logit's key lies in [klo, khi] and that are not below `floor` into this CTA's list; sh.count
     // has their numbers after the next cluster barrier, also beyond kCap.  With ALL also the sums of all w
     // (sh.mass).
-    template <bool ALL>
+    // With HIST also the numbers of these tokens by bin() of their logit.
+    template <bool ALL, bool HIST>
     __device__ __noinline__ void collect(uint32_t klo, uint32_t khi, u64 floor) {
+        // (the members in registers: they lie in local memory, where every use in a loop would load them again)
+        const Weigh weigh = this->weigh;
+        const R row = this->row;
+        const int iters = a.iters;
+        const float m = this->m, least = this->least, bin_scale = this->bin_scale;
+        auto bin = [&](float l) { return min((int)((m - l) * bin_scale), kBins - 1); };
+        u64 *const list = this->list;
+        uint32_t *hist = reinterpret_cast<uint32_t *>(sorted);
+        if (HIST)
+            for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0u;
         if (threadIdx.x == 0) sh.mine = 0;
         cta_sync();
         const float lo = key_value(klo);
         u64 sum = 0ull;
 #pragma unroll 1
-        for (int it = 0; it < a.iters; ++it) {
+        for (int it = 0; it < iters; ++it) {
             float v[EV];
             row.get(it, v);
-            bool any = false;
-#pragma unroll
-            for (int j = 0; j < EV; ++j) any = any || v[j] >= lo;
             if (ALL) {
-#pragma unroll
-                for (int j = 0; j < EV; ++j) sum += w_of(v[j]);
+                const uint32_t in = at_least(v, least);
+                if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
             }
-            if (!__any_sync(kFull, any)) continue;
+            uint32_t in = at_least(v, lo);
+            if (HIST) {
+#pragma unroll
+                for (int j = 0; j < EV; ++j)
+                    if (in >> j & 1u) atomicAdd(&hist[bin(v[j])], 1u);
+            }
+            // beyond kCap the number does not matter: the list is not used
+            if (in && *reinterpret_cast<volatile int *>(&sh.mine) <= kCap) {
 #pragma unroll 1
-            for (int j = 0; j < EV; ++j) {
-                float l = v[0];
+                while (in) {
+                    const int j = __ffs(in) - 1;
+                    in &= in - 1u;
+                    float l = v[0];
 #pragma unroll
-                for (int i = 1; i < EV; ++i) l = i == j ? v[i] : l;
-                const uint32_t k = order_key(l);
-                const bool in = k >= klo && k <= khi && l > -INFINITY && make_key(k, row.at(it) + j) >= floor;
-                const unsigned mask = __ballot_sync(kFull, in);
-                if (mask == 0u) continue;
-                int base = 0;
-                if (lane == 0) base = atomicAdd(&sh.mine, __popc(mask));
-                base = __shfl_sync(kFull, base, 0) + __popc(mask & ((1u << lane) - 1u));
-                if (in && base < kCap) list[base] = make_key(k, row.at(it) + j);
-                __syncwarp();
+                    for (int i = 1; i < EV; ++i) l = i == j ? v[i] : l;
+                    const uint32_t k = order_key(l);
+                    const u64 key = make_key(k, row.at(it) + j);
+                    if (k > khi || key < floor) continue;
+                    const int at = atomicAdd(&sh.mine, 1);
+                    if (at < kCap) list[at] = key;
+                }
             }
+            __syncwarp();
         }
         if (ALL) {
             sum = warp_sum64(sum);
@@ -333,14 +440,14 @@ struct Sampler {
     // Sorts the candidates of all lists (n <= kCap) and finds the border: the k-th token of the order (k > 0)
     // and the first at which the sum reaches p times `total` (of the k tokens' sum with k > 0), counted from
     // `above` tokens and a sum of `above_mass` that lie before the candidates.  Leader CTA; the border goes to
-    // all CTAs.
-    __device__ __noinline__ void border_of_list(int n, uint32_t above, u64 above_mass, int k, bool by_p, u64 total, bool total_of_k) {
+    // all CTAs.  whole: nothing that has a weight lies behind the candidates; else a sum that does not get there leaves
+    // sh.found 0.
+    __device__ __noinline__ void border_of_list(int n, uint32_t above, u64 above_mass, int k, bool by_p, u64 total, bool total_of_k, bool whole) {
         const int tid = threadIdx.x;
-        int at = 0;
-        for (int c = 0; c < a.C; ++c) {
-            const int cnt = (int)sh.count[c];
-            for (int i = tid; i < cnt; i += kThreads) sorted[at + i] = get64(&list[i], c);
-            at += cnt;
+        for (int i = tid; i < n; i += kThreads) {
+            int c = 0, at = i;
+            while (at >= (int)sh.count[c]) at -= (int)sh.count[c++];
+            sorted[i] = get64(&list[at], c);
         }
         const int ept = n <= kThreads ? 1 : n <= 2 * kThreads ? 2 : 4;
         for (int i = n + tid; i < ept * kThreads; i += kThreads) sorted[i] = 0ull;
@@ -376,25 +483,182 @@ struct Sampler {
         if (tid == 0) {
             sh.target = by_p ? share_of(total) : ~0ull;
             sh.border = 0ull;
+            sh.found = 0;
         }
         cta_sync();
         const u64 target = sh.target;
         for (int e = 0; e < ept; ++e) {
             const int i = ept * tid + e;
             // the last place of the run: the sum before it is below the target, with it not, or top-k ends
-            if (i <= last && (i == 0 || before < target) && (i == last || before + w[e] >= target)) sh.border = key[e];
+            if (i <= last && before < target && ((i == last && (whole || !by_p)) || before + w[e] >= target)) {
+                sh.border = key[e];
+                sh.found = 1;
+            }
             before += w[e];
         }
         cta_sync();
-        if (tid < a.C) put64(&sh.border, tid, sh.border);
+        if (tid < a.C) {
+            put64(&sh.border, tid, sh.border);
+            put32(&sh.found, tid, (uint32_t)sh.found);
+        }
         __syncwarp();
+    }
+
+    // The border from the counts that collect() left in the cluster (bins of [low, m]): k > 0: the bin of the k-th token;
+    // else a run of bins around the place where the sum, estimated from the counts and the bins' middles, reaches
+    // p times `total`.  The tokens above it are summed up exactly, those in it sorted.  False (nothing decided): the
+    // run is too large or, by the exact sums, does not hold the border.  Whole cluster.
+    __device__ __noinline__ bool border_by_counts(int k, u64 total) {
+        const int tid = threadIdx.x;
+        uint32_t *cnt = reinterpret_cast<uint32_t *>(sorted);
+        const bool by_k = k > 0;
+        constexpr int Q = kBins / kThreads;
+        const int part = kBins / a.C;
+        uint32_t c4[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            c4[i] = 0u;
+            if (tid + i * kThreads < part)
+                for (int c = 0; c < a.C; ++c) c4[i] += get32(&cnt[rank * part + tid + i * kThreads], c);
+        }
+        __syncwarp();
+        cluster_sync_all();
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            if (tid + i * kThreads < part) put32(&cnt[rank * part + tid + i * kThreads], 0, c4[i]);
+        __syncwarp();
+        cluster_sync_all();
+        if (rank == 0) {
+            // thread t has the bins Q t .. Q t + Q - 1
+            const float octaves = fac.hi / bin_scale, one = (float)(1ull << a.shift);
+            uint32_t n[Q], csum = 0u;
+            float e[Q], esum = 0.f;
+            for (int i = 0; i < Q; ++i) {
+                n[i] = cnt[Q * tid + i];
+                e[i] = (float)n[i] * exp2f(-octaves * ((float)(Q * tid + i) + 0.5f));
+                csum += n[i];
+                esum += e[i];
+            }
+            uint32_t cincl = csum;
+            float eincl = esum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t c = __shfl_up_sync(kFull, cincl, o);
+                const float f = __shfl_up_sync(kFull, eincl, o);
+                if (lane >= o) cincl += c, eincl += f;
+            }
+            if (lane == 31) sh.wcount[warp] = cincl, sh.wtop[warp] = eincl;
+            if (tid == 0) sh.found = 0;
+            cta_sync();
+            uint32_t c0 = cincl - csum;
+            float e0 = eincl - esum;
+            for (int i = 0; i < warp; ++i) c0 += sh.wcount[i], e0 += sh.wtop[i];
+            const float want = sh.p * ((float)total / one);
+            for (int i = 0; i < Q; ++i) {
+                const bool here = by_k ? c0 < (uint32_t)k && c0 + n[i] >= (uint32_t)k : e0 < want && e0 + e[i] >= want && n[i] > 0u;
+                if (here) {
+                    sh.found = 1;
+                    sh.klo = sh.khi = Q * tid + i;  // bins, for now
+                    sh.above = c0;
+                    sh.inside = n[i];
+                }
+                c0 += n[i];
+                e0 += e[i];
+            }
+            cta_sync();
+            if (sh.found) {
+                if (!by_k && tid == 0) {  // as many bins to both sides as half of the list takes
+                    int b0 = (int)sh.klo, b1 = b0;
+                    uint32_t in = sh.inside;
+                    for (int i = 0; i < 64 && in <= kCap / 2; ++i) {
+                        if (b0 > 0) --b0, in += cnt[b0], sh.above -= cnt[b0];
+                        if (b1 < kBins - 1) ++b1, in += cnt[b1];
+                    }
+                    sh.klo = b1, sh.khi = b0, sh.inside = in;  // higher bins hold smaller logits
+                }
+                cta_sync();
+                const uint32_t b = tid == 0 ? sh.klo : sh.khi, bottom = order_key(sh.bound), top = order_key(m);
+                cta_sync();
+                if (tid == 0 || tid == 32) {
+                    // the smallest key whose bin is not beyond klo's, the largest whose bin is not before khi's
+                    uint32_t x0 = bottom, x1 = top;
+                    while (x0 < x1) {
+                        const uint32_t d = x1 - x0, mid = tid == 0 ? x0 + d / 2 : x1 - d / 2;
+                        const uint32_t bm = (uint32_t)bin(key_value(mid));
+                        if (tid == 0) {
+                            if (bm <= b) x1 = mid;
+                            else x0 = mid + 1;
+                        } else {
+                            if (bm >= b) x0 = mid;
+                            else x1 = mid - 1;
+                        }
+                    }
+                    if (tid == 0) sh.klo = x0;
+                    else sh.khi = x0;
+                }
+                __syncwarp();
+                cta_sync();
+            }
+            if (tid < a.C && tid > 0) {
+                put32(&sh.found, tid, (uint32_t)sh.found);
+                put32(&sh.klo, tid, sh.klo);
+                put32(&sh.khi, tid, sh.khi);
+                put32(&sh.inside, tid, sh.inside);
+            }
+            __syncwarp();
+        }
+        cluster_sync_all();
+        if (!sh.found) {
+            if (!by_k) return false;
+            if (tid == 0) sh.border = 0ull;  // fewer tokens than k have a weight
+            cta_sync();
+            return true;
+        }
+        const uint32_t klo = sh.klo, khi = sh.khi, inside = sh.inside;
+        if (inside > (uint32_t)kCap) return false;
+        // sums above the run, and its tokens
+        const Weigh weigh = this->weigh;
+        const R row = this->row;
+        const int iters = a.iters;
+        u64 sum = 0ull;
+        if (!by_k) {
+            const float above = key_value(khi);
+#pragma unroll 1
+            for (int it = 0; it < iters; ++it) {
+                float v[EV];
+                row.get(it, v);
+                uint32_t in = 0u;
+#pragma unroll
+                for (int j = 0; j < EV; ++j) in |= v[j] > above ? 1u << j : 0u;
+                if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
+            }
+            sum = warp_sum64(sum);
+        }
+        if (lane == 0) sh.wmass[warp] = sum;
+        collect<false, false>(klo, khi, 0ull);
+        if (warp == 0) {
+            const u64 t = warp_sum64(lane < kWarps ? sh.wmass[lane] : 0ull);
+            if (lane < a.C) put64(&sh.mass[rank], lane, t);
+            __syncwarp();
+        }
+        cluster_sync_all();
+        if (rank == 0) {
+            u64 above_mass = 0ull;
+            for (int c = 0; c < a.C; ++c) above_mass += sh.mass[c];
+            border_of_list((int)inside, sh.above, above_mass, k, !by_k, total, false, false);
+        }
+        cluster_sync_all();
+        return sh.found != 0;
     }
 
     // The border among more keys than can be sorted: k > 0: the k-th token; else the first token at which the sum of w
     // reaches p times `total`, over the tokens not below `floor`.  Whole cluster; sh.border in every CTA at the end.
     // Keys outside [key of low, key of m] are left out: they hold no border.
     __device__ __noinline__ void border_by_ranges(int k, u64 total, float low, u64 floor) {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, iters = a.iters;
+        const R row = this->row;
+        const Weigh weigh = this->weigh;
+        const float m = this->m;
         uint32_t *cnt = reinterpret_cast<uint32_t *>(sorted);  // [kBins]
         u64 *mass = list;                                      // [kBins]
         uint32_t klo = order_key(low), khi = order_key(m);
@@ -404,19 +668,19 @@ struct Sampler {
         if (tid == 0) sh.target = by_k ? 0ull : share_of(total);
         cta_sync();
         const u64 target = sh.target;
-        const float scale = kBins / fmaxf(m - low, 1e-37f);
-        bool linear = scale < INFINITY;
+        bin_scale = fminf(kBins / fmaxf(m - low, 1e-37f), 1e37f);
+        bool linear = true;
 #pragma unroll 1
         for (;;) {
             const int sh_bits = max(0, 32 - __clz((khi - klo) | 1u) - 11);
             // bin 0 holds the largest logits; both maps are monotone
             auto bin_of = [&](float l, uint32_t key) {
-                return linear ? min((int)((m - l) * scale), kBins - 1) : (int)((khi - key) >> sh_bits);
+                return linear ? bin(l) : (int)((khi - key) >> sh_bits);
             };
             for (int i = tid; i < kBins; i += kThreads) cnt[i] = 0u, mass[i] = 0ull;
             cta_sync();
 #pragma unroll 1
-            for (int it = 0; it < a.iters; ++it) {
+            for (int it = 0; it < iters; ++it) {
                 float v[EV];
                 row.get(it, v);
 #pragma unroll 1
@@ -428,7 +692,7 @@ struct Sampler {
                     if (key >= klo && key <= khi && l > -INFINITY && make_key(key, row.at(it) + j) >= floor) {
                         const int b = bin_of(l, key);
                         atomicAdd(&cnt[b], 1u);
-                        if (!by_k) atomicAdd(&mass[b], w_of(l));
+                        if (!by_k) atomicAdd(&mass[b], weigh.one(l));
                     }
                     __syncwarp();
                 }
@@ -537,9 +801,9 @@ struct Sampler {
             const uint32_t inside = sh.inside;
             linear = false;
             if (inside <= (uint32_t)kCap) {
-                collect<false>(klo, khi, floor);
+                collect<false, false>(klo, khi, floor);
                 cluster_sync_all();
-                if (rank == 0) border_of_list((int)inside, above, above_mass, k, !by_k, total, false);
+                if (rank == 0) border_of_list((int)inside, above, above_mass, k, !by_k, total, false, true);
                 cluster_sync_all();
                 return;
             }
@@ -557,12 +821,14 @@ struct Sampler {
     // Border at the need-th (from 1) token, by index, of those with logit key k (and not below `floor`).
     // Whole cluster.
     __device__ __noinline__ void nth_equal(uint32_t k, uint32_t need, u64 floor) {
+        const R row = this->row;
+        const int iters = a.iters;
         auto tokens = [&](int it, int j, float l) {
             return order_key(l) == k && row.at(it) + j >= 0 && row.at(it) + j < a.V && make_key(k, row.at(it) + j) >= floor;
         };
         uint32_t n = 0u;
 #pragma unroll 1
-        for (int it = 0; it < a.iters; ++it) {
+        for (int it = 0; it < iters; ++it) {
             float v[EV];
             row.get(it, v);
 #pragma unroll
@@ -582,7 +848,7 @@ struct Sampler {
         for (int i = 0; i < warp; ++i) before += sh.wcount[i];
         if (before < need && need <= before + sh.wcount[warp]) {  // warp-uniform
 #pragma unroll 1
-            for (int it = 0; it < a.iters && before < need; ++it) {
+            for (int it = 0; it < iters && before < need; ++it) {
                 float v[EV];
                 row.get(it, v);
                 uint32_t c = 0u;
@@ -610,25 +876,24 @@ struct Sampler {
         cluster_sync_all();
     }
 
+    __device__ __forceinline__ float border_logit(u64 border) const {
+        const uint32_t bk = (uint32_t)(border >> 32);
+        return bk ? fmaxf(key_value(bk), least) : least;
+    }
     // Sums of the w of the kept tokens (key >= border) per warp (sh.wmass) and, after the cluster barrier that
     // ends it, per CTA (sh.mass).
     __device__ __forceinline__ void sum_kept(u64 border) {
-        const uint32_t bk = (uint32_t)(border >> 32);
-        const float lo = bk ? key_value(bk) : -INFINITY;
+        const Weigh weigh = this->weigh;
+        const R row = this->row;
+        const int iters = a.iters;
+        const float lo = border_logit(border);
         u64 sum = 0ull;
 #pragma unroll 1
-        for (int it = 0; it < a.iters; ++it) {
+        for (int it = 0; it < iters; ++it) {
             float v[EV];
             row.get(it, v);
-            bool any = false;
-#pragma unroll
-            for (int j = 0; j < EV; ++j) any = any || v[j] >= lo;
-            if (!__any_sync(kFull, any)) continue;
-#pragma unroll
-            for (int j = 0; j < EV; ++j) {
-                const u64 w = w_of(v[j]);
-                if (v[j] > lo || make_key(order_key(v[j]), row.at(it) + j) >= border) sum += w;
-            }
+            const uint32_t in = kept(v, row.at(it), lo, border);
+            if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
         }
         sum = warp_sum64(sum);
         if (lane == 0) sh.wmass[warp] = sum;
@@ -643,6 +908,8 @@ struct Sampler {
 
     __device__ __forceinline__ void run(int t) {
         const int tid = threadIdx.x;
+        const R row = this->row;
+        const int iters = a.iters;
         // this thread's maximum, the warps' and their j-th lane maxima
         float mine = -INFINITY;
         if (HELD) {
@@ -650,7 +917,7 @@ struct Sampler {
             __syncwarp();
         }
 #pragma unroll 1
-        for (int it = 0; it < a.iters; ++it) {
+        for (int it = 0; it < iters; ++it) {
             float v[EV];
             row.get(it, v);
 #pragma unroll
@@ -694,6 +961,8 @@ struct Sampler {
         }
         const float p = sh.p;
         const bool greedy = !(fac.hi > 0.f) || k0 == 1, by_k = jth > 0, by_p = p < 1.f;
+        least = greedy ? m : fmaxf(m - (float)a.shift / fac.hi, -3.4028234e38f);
+        weigh.set(m, fac, a.shift, sh.table);
         u64 border = 0ull, total = 0ull;
         if (greedy) {
             border = (u64)order_key(m) << 32;
@@ -724,23 +993,28 @@ struct Sampler {
             __syncwarp();
             cta_sync();
             const float bound = sh.bound;
-            const float weightless = m - ((float)a.shift + 1.f) / fac.hi;  // tokens below have w = 0
-            const float low = fmaxf(fmaxf(bound, weightless), -3.4028234e38f);
+            const float low = fmaxf(bound, least);
+            bin_scale = fminf(kBins / fmaxf(m - low, 1e-37f), 1e37f);
+            cta_sync();
+            if (tid == 0) sh.bound = low;
             // the candidates; by top-p alone also the sum of all
-            const bool listed = !by_k || bound > -INFINITY || a.V <= kCap;
-            if (!by_k) collect<true>(order_key(low), order_key(m), 0ull);
-            else if (listed) collect<false>(order_key(low), order_key(m), 0ull);
+            if (by_k) collect<false, true>(order_key(low), order_key(m), 0ull);
+            else collect<true, true>(order_key(low), order_key(m), 0ull);
             cluster_sync_all();
             uint32_t n = 0u;
             for (int c = 0; c < a.C; ++c) {
-                n += listed ? sh.count[c] : 0u;
+                n += sh.count[c];
                 total += by_k ? 0ull : sh.mass[c];
             }
-            if (listed && n <= (uint32_t)kCap) {
-                if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k);
+            // a bound of top-k has k tokens not below it (and without one everything that has a weight is a candidate)
+            if (n <= (uint32_t)kCap) {
+                if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k, true);
                 cluster_sync_all();
                 border = sh.border;
+            } else if (by_k != by_p && border_by_counts(by_k ? k0 : 0, total)) {
+                border = sh.border;
             } else {
+                cluster_sync_all();
                 u64 floor = 0ull;
                 if (by_k) {
                     border_by_ranges(k0, 0ull, low, 0ull);
@@ -753,14 +1027,29 @@ struct Sampler {
                         for (int c = 0; c < a.C; ++c) total += sh.mass[c];
                         cluster_sync_all();  // everybody has read the sums
                     }
-                    const float low_p = fmaxf(m + (log2f((1.f - p) / (float)a.V) - 0.05f) / fac.hi, fmaxf(weightless, -3.4028234e38f));
+                    const float low_p = fmaxf(m + (log2f((1.f - p) / (float)a.V) - 0.05f) / fac.hi, least);
                     border_by_ranges(0, total, low_p, floor);
                     border = sh.border > floor ? sh.border : floor;
                 }
             }
         }
-        if (!greedy && sh.gap >= 0.) {
-            const u64 b = (u64)order_key(__double2float_ru((double)m - sh.gap)) << 32;
+        if (!greedy && sh.min_p > 0.f) {
+            // the smallest logit whose w is at least min_p times the largest: 32 places of the range at a time
+            const u64 want = sh.min_p < 1.f ? share(sh.min_p, 1ull << a.shift, true) : 1ull << a.shift;
+            uint32_t x0 = order_key(least), x1 = order_key(m);
+            if (warp == 0) {
+                while (x0 < x1) {
+                    const uint32_t x = x0 + (uint32_t)((u64)(x1 - x0) * (uint32_t)lane >> 5);
+                    const unsigned in = __ballot_sync(kFull, w_of(key_value(x)) >= want);
+                    const int at = in ? __ffs(in) - 1 : 32;
+                    const uint32_t below = __shfl_sync(kFull, x, at > 0 ? at - 1 : 0), above = __shfl_sync(kFull, x, at & 31);
+                    if (at < 32) x1 = above;
+                    if (at > 0) x0 = below + 1u;
+                }
+                if (lane == 0) sh.klo = x0;
+            }
+            cta_sync();
+            const u64 b = (u64)sh.klo << 32;
             border = b > border ? b : border;
         }
         cta_sync();
@@ -772,25 +1061,28 @@ struct Sampler {
             before += c < rank ? v : 0ull;
         }
         if (tid == 0) {
-            const double u = greedy ? 0. : fmin(fmax((double)sh.u, 0.), 1.);
-            const u64 g = (u64)(u * (double)S);
-            sh.target = g < S ? g : S - 1ull;
+            const float u = greedy ? 0.f : fmaxf(sh.u, 0.f);
+            sh.target = u < 1.f ? share(u, S, false) : S - 1ull;
         }
         cta_sync();
         const u64 target = sh.target;  // the first token at which the sum exceeds it
         for (int i = 0; i < warp; ++i) before += sh.wmass[i];
         if (before <= target && target < before + sh.wmass[warp]) {  // one warp of the cluster
-            const uint32_t bk = (uint32_t)(border >> 32);
-            const float lo = bk ? key_value(bk) : -INFINITY;
+            const Weigh weigh = this->weigh;
+            const float lo = border_logit(border);
 #pragma unroll 1
-            for (int it = 0; it < a.iters; ++it) {
+            for (int it = 0; it < iters; ++it) {
                 float v[EV];
                 row.get(it, v);
+                const uint32_t in = kept(v, row.at(it), lo, border);
+                if (!__any_sync(kFull, in != 0u)) continue;
                 u64 w[EV], sum = 0ull;
 #pragma unroll
-                for (int j = 0; j < EV; ++j) {
-                    w[j] = v[j] > lo || make_key(order_key(v[j]), row.at(it) + j) >= border ? w_of(v[j]) : 0ull;
-                    sum += w[j];
+                for (int j = 0; j < EV; j += 2) {
+                    weigh.pair(v[j], v[j + 1], w[j], w[j + 1]);
+                    w[j] = in >> j & 1u ? w[j] : 0ull;
+                    w[j + 1] = in >> (j + 1) & 1u ? w[j + 1] : 0ull;
+                    sum += w[j] + w[j + 1];
                 }
                 const u64 incl = warp_scan64(sum);
                 u64 at = before + incl - sum;
@@ -809,7 +1101,7 @@ struct Sampler {
                                 const u64 one = 1ull << a.shift, whole = S >> a.shift;
                                 const float s_hi = (float)whole, s_lo = (float)(S & (one - 1ull)) * (1.f / (float)one);
                                 const float s = s_hi + s_lo, rest = s_lo - (s - s_hi);
-                                a.logprob[t] = greedy ? 0.f : (e + e_lo) * 0.69314718f - (logf(s) + rest / s);
+                                a.logprob[t] = greedy || w[j] == S ? 0.f : (e + e_lo) * 0.69314718f - (logf(s) + rest / s);
                             }
                         }
                         at += w[j];
@@ -853,18 +1145,22 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 1) sample_kernel(const __
         sh.u = a.u[t];
         sh.p = sh.p < 1.f ? fmaxf(sh.p, 0.f) : 1.f;  // NaN: off
         if (heat > 0.f) {
-            const double c = fmin(1.4426950408889634 / (double)fminf(heat, 3.4028234e38f), 1.7e38);
-            const bool tiny = c < 1e-18;
-            sh.fac.hi = (float)c;
-            sh.fac.lo = (float)((c - (double)sh.fac.hi) * (tiny ? 16777216. : 1.));
+            // log2(e) / heat in two parts: the quotient of the significands and its remainder's
+            const float h = fminf(fmaxf(heat, 8.5e-39f), 3.4028234e38f);
+            int ex;
+            const float f = 2.f * frexpf(h, &ex), q = 1.44269504f / f;
+            const float rest = (fmaf(-q, f, 1.44269504f) + 1.9259630e-8f) / f;
+            const bool tiny = ex > 60;
+            sh.fac.hi = ldexpf(q, 1 - ex);
+            sh.fac.lo = ldexpf(rest, 1 - ex + (tiny ? 24 : 0)) + (tiny ? ldexpf(ldexpf(q, 25 - ex) - ldexpf(sh.fac.hi, 24), 0) : 0.f);
             sh.fac.pre = tiny ? 5.9604644775390625e-8f : 1.f;
         } else {
             sh.fac = Factor{0.f, 0.f, 0.f};
         }
-        sh.gap = mp > 0.f ? -(double)heat * log(fmin((double)mp, 1.)) : -1.;
+        sh.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;
     }
     cta_sync();
-    Sampler<E, HELD> s{a, sh, list, sorted, row, rank, lane, warp, 0.f, Factor{}};
+    Sampler<E, HELD> s{a, sh, list, sorted, row, rank, lane, warp, 0.f, 0.f, Factor{}, Weigh{}, 0.f};
     cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written to
     s.run(t);
     __syncwarp();
@@ -907,9 +1203,9 @@ rl_status run_sample(SampleArgs &a, int T, cudaStream_t s) {
     while (a.C < kMaxC && (pieces > a.C * 8 * kThreads || ((long long)T * a.C * 2 <= sms && pieces > a.C * kThreads))) a.C *= 2;
     const int per = (pieces + a.C - 1) / a.C;
     a.iters = (per + kThreads - 1) / kThreads;
-    a.shift = 62;
-    for (int v = 1; v < a.V; v *= 2) --a.shift;  // the sum of V weights stays below 2^62
-    if (a.shift > 45) a.shift = 45;
+    a.shift = 63;
+    for (int v = 1; v < a.V; v *= 2) --a.shift;  // the sum of V weights stays below 2^64
+    if (a.shift > 46) a.shift = 46;
     // 227 KB of shared memory per CTA: 24 pieces of 8 KB beside the lists
     if (a.iters <= 22) return launch_sample<E, true>(a, T, s);
     return launch_sample<E, false>(a, T, s);
