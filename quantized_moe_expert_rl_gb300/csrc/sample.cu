@@ -79,7 +79,7 @@ struct Factor {
 
 struct Shared {
     u64 mass[kMaxC];         // by CTA of the cluster
-    u64 wmass[kWarps];
+    u64 wmass[kWarps], wabove[kWarps];
     u64 border;              // kept: key >= border
     u64 above_mass, target;
     float wtop[kMaxC * kWarps], wjth[kMaxC * kWarps];  // by warp of the cluster
@@ -95,7 +95,11 @@ struct Shared {
     float p, u, min_p;
 };
 
-__device__ __forceinline__ void cluster_sync_all() {
+__device__ __forceinline__ void cluster_sync_all(int C) {
+    if (C == 1) {
+        cta_sync();
+        return;
+    }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncwarp();
 }
@@ -224,12 +228,13 @@ struct Row {
     uint32_t held;           // shared memory of this lane's piece 0
     __device__ __forceinline__ int at(int it) const { return first + it * 32 * EV; }
     __device__ __forceinline__ bool inner(int i0) const { return i0 >= 0 && i0 <= V - EV; }
-    __device__ __forceinline__ uint4 edge(int i0) const {
+    static __device__ __noinline__ uint4 edge_of(const E *x, int V, int i0) {
         E e[EV];
 #pragma unroll
         for (int k = 0; k < EV; ++k) e[k] = i0 + k >= 0 && i0 + k < V ? x[i0 + k] : from_float<E>(-INFINITY);
         return *reinterpret_cast<const uint4 *>(e);
     }
+    __device__ __forceinline__ uint4 edge(int i0) const { return edge_of(x, V, i0); }
     __device__ __forceinline__ void load(int iters) const {  // HELD: into shared memory
         for (int it = 0; it < iters; ++it) {
             const int i0 = at(it);
@@ -244,10 +249,11 @@ struct Row {
         cp_async_commit();
         __syncwarp();
     }
-    __device__ __forceinline__ void get(int it, float (&v)[EV]) const {
-        uint4 q;
-        if constexpr (HELD) q = lds128(held + it * 512);
-        else q = inner(at(it)) ? __ldg(reinterpret_cast<const uint4 *>(x + at(it))) : edge(at(it));
+    __device__ __forceinline__ uint4 raw(int it) const {
+        if constexpr (HELD) return lds128(held + it * 512);
+        else return inner(at(it)) ? __ldg(reinterpret_cast<const uint4 *>(x + at(it))) : edge(at(it));
+    }
+    static __device__ __forceinline__ void unpack(const uint4 &q, float (&v)[EV]) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -256,6 +262,26 @@ struct Row {
             } else {
                 const float2 f = unpack2(w[p], E());
                 v[2 * p] = f.x, v[2 * p + 1] = f.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int it, float (&v)[EV]) const { unpack(raw(it), v); }
+    // f(it, values) for this lane's pieces; from memory with four loads in flight
+    template <typename F>
+    __device__ __forceinline__ void each(int iters, F f) const {
+        constexpr int B = HELD ? 1 : 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < iters; i0 += B) {
+            uint4 q[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) q[b] = raw(i0 + b);  // (past the last: beyond the row or a neighbour's, not used)
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (i0 + b < iters) {
+                    float v[EV];
+                    unpack(q[b], v);
+                    f(i0 + b, v);
+                }
             }
         }
     }
@@ -334,39 +360,41 @@ struct Sampler {
         return t > 0ull ? t : 1ull;
     }
     __device__ __forceinline__ u64 w_of(float l) const { return weigh.one(l); }
-    // the sum of w over the values of a piece for which bit j of `in` is set
-    static __device__ __forceinline__ u64 sum_in(const Weigh &weigh, const float (&v)[EV], uint32_t in) {
+    // the sum of w over the values j of a piece with in[j]
+    static __device__ __forceinline__ u64 sum_in(const Weigh &weigh, const float (&v)[EV], const bool (&in)[EV]) {
         u64 sum = 0ull;
 #pragma unroll
         for (int j = 0; j < EV; j += 2) {
             u64 w0, w1;
             weigh.pair(v[j], v[j + 1], w0, w1);
-            if (in >> j & 1u) sum += w0;
-            if (in >> (j + 1) & 1u) sum += w1;
+            if (in[j]) sum += w0;
+            if (in[j + 1]) sum += w1;
         }
         return sum;
     }
-    static __device__ __forceinline__ uint32_t at_least(const float (&v)[EV], float lo) {
-        uint32_t in = 0u;
-#pragma unroll
-        for (int j = 0; j < EV; ++j) in |= v[j] >= lo ? 1u << j : 0u;
-        return in;
-    }
-    // bit j: value j of the piece at `i0` is kept (its logit lies above `lo`, the border's, or its key not below)
-    static __device__ __forceinline__ uint32_t kept(const float (&v)[EV], int i0, float lo, u64 border) {
-        uint32_t in = 0u, even = 0u;
+    static __device__ __forceinline__ bool at_least(const float (&v)[EV], float lo, bool (&in)[EV]) {
+        bool any = false;
 #pragma unroll
         for (int j = 0; j < EV; ++j) {
-            in |= v[j] > lo ? 1u << j : 0u;
-            even |= v[j] == lo ? 1u << j : 0u;
+            in[j] = v[j] >= lo;
+            any = any || in[j];
         }
-        const uint32_t bk = (uint32_t)(border >> 32);
-        while (even) {  // equal logits: up to the border's index (all where the border lies below)
-            const int j = __ffs(even) - 1;
-            even &= even - 1u;
-            if (make_key(order_key(lo), i0 + j) >= border || bk == 0u) in |= 1u << j;
+        return any;
+    }
+    // in[j]: value j of the piece at `i0` is kept: its logit is not below `lo`, the border's; where the border divides
+    // equal logits (its lower half is not 0), its key is not below.  True if any is.
+    static __device__ __forceinline__ bool kept(const float (&v)[EV], int i0, float lo, u64 border, bool (&in)[EV]) {
+        bool any = at_least(v, lo, in);
+        if ((uint32_t)border != 0u && any) {
+            any = false;
+#pragma unroll
+            for (int j = 0; j < EV; ++j) {
+                in[j] = in[j] && (v[j] > lo || make_key(order_key(lo), i0 + j) >= border);
+                any = any || in[j];
+            }
         }
-        return in;
+        __syncwarp();
+        return any;
     }
 
     // Tokens whose logit's key lies in [klo, khi] and that are not below `floor` into this CTA's list; sh.count
@@ -389,19 +417,18 @@ struct Sampler {
         cta_sync();
         const float lo = key_value(klo);
         u64 sum = 0ull;
-#pragma unroll 1
-        for (int it = 0; it < iters; ++it) {
-            float v[EV];
-            row.get(it, v);
+        row.each(iters, [&](int it, const float (&v)[EV]) {
             if (ALL) {
-                const uint32_t in = at_least(v, least);
-                if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
+                bool all[EV];
+                if (__any_sync(kFull, at_least(v, least, all))) sum += sum_in(weigh, v, all);
             }
-            uint32_t in = at_least(v, lo);
-            if (HIST) {
+            bool some[EV];
+            if (!__any_sync(kFull, at_least(v, lo, some))) return;
+            uint32_t in = 0u;
 #pragma unroll
-                for (int j = 0; j < EV; ++j)
-                    if (in >> j & 1u) atomicAdd(&hist[bin(v[j])], 1u);
+            for (int j = 0; j < EV; ++j) {
+                if (HIST && some[j]) atomicAdd(&hist[bin(v[j])], 1u);
+                in |= some[j] ? 1u << j : 0u;
             }
             // beyond kCap the number does not matter: the list is not used
             if (in && *reinterpret_cast<volatile int *>(&sh.mine) <= kCap) {
@@ -420,7 +447,7 @@ struct Sampler {
                 }
             }
             __syncwarp();
-        }
+        });
         if (ALL) {
             sum = warp_sum64(sum);
             if (lane == 0) sh.wmass[warp] = sum;
@@ -452,7 +479,18 @@ struct Sampler {
         const int ept = n <= kThreads ? 1 : n <= 2 * kThreads ? 2 : 4;
         for (int i = n + tid; i < ept * kThreads; i += kThreads) sorted[i] = 0ull;
         cta_sync();
-        if (ept == 1) sort_keys<1>(sorted);
+        if (n <= 128) {  // by counting the larger ones, four lanes per key
+            const int i = tid >> 2;
+            const u64 mine = sorted[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = tid & 3; j < n; j += 4) rank += sorted[j] > mine ? 1 : 0;
+            rank += __shfl_xor_sync(kFull, rank, 1);
+            rank += __shfl_xor_sync(kFull, rank, 2);
+            cta_sync();
+            if (i < n && (tid & 3) == 0) sorted[rank] = mine;
+            cta_sync();
+        } else if (ept == 1) sort_keys<1>(sorted);
         else if (ept == 2) sort_keys<2>(sorted);
         else sort_keys<4>(sorted);
         // running sums: thread t has the places ept t .. ept t + ept - 1
@@ -504,6 +542,17 @@ struct Sampler {
         __syncwarp();
     }
 
+    // the CTA's sum, of the warps', to all CTAs
+    __device__ __forceinline__ void publish_sums() {
+        cta_sync();
+        if (warp == 0) {
+            const u64 t = warp_sum64(lane < kWarps ? sh.wmass[lane] : 0ull);
+            if (lane < a.C) put64(&sh.mass[rank], lane, t);
+            __syncwarp();
+        }
+        cluster_sync_all(a.C);
+    }
+
     // The border from the counts that collect() left in the cluster (bins of [low, m]): k > 0: the bin of the k-th token;
     // else a run of bins around the place where the sum, estimated from the counts and the bins' middles, reaches
     // p times `total`.  The tokens above it are summed up exactly, those in it sorted.  False (nothing decided): the
@@ -522,12 +571,12 @@ struct Sampler {
                 for (int c = 0; c < a.C; ++c) c4[i] += get32(&cnt[rank * part + tid + i * kThreads], c);
         }
         __syncwarp();
-        cluster_sync_all();
+        cluster_sync_all(a.C);
 #pragma unroll
         for (int i = 0; i < Q; ++i)
             if (tid + i * kThreads < part) put32(&cnt[rank * part + tid + i * kThreads], 0, c4[i]);
         __syncwarp();
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         if (rank == 0) {
             // thread t has the bins Q t .. Q t + Q - 1
             const float octaves = fac.hi / bin_scale, one = (float)(1ull << a.shift);
@@ -607,7 +656,7 @@ struct Sampler {
             }
             __syncwarp();
         }
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         if (!sh.found) {
             if (!by_k) return false;
             if (tid == 0) sh.border = 0ull;  // fewer tokens than k have a weight
@@ -623,32 +672,46 @@ struct Sampler {
         u64 sum = 0ull;
         if (!by_k) {
             const float above = key_value(khi);
-#pragma unroll 1
-            for (int it = 0; it < iters; ++it) {
-                float v[EV];
-                row.get(it, v);
-                uint32_t in = 0u;
+            row.each(iters, [&](int, const float (&v)[EV]) {
+                bool in[EV], any = false;
 #pragma unroll
-                for (int j = 0; j < EV; ++j) in |= v[j] > above ? 1u << j : 0u;
-                if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
-            }
+                for (int j = 0; j < EV; ++j) {
+                    in[j] = v[j] > above;
+                    any = any || in[j];
+                }
+                if (__any_sync(kFull, any)) sum += sum_in(weigh, v, in);
+            });
             sum = warp_sum64(sum);
         }
-        if (lane == 0) sh.wmass[warp] = sum;
+        if (lane == 0) sh.wabove[warp] = sum;
         collect<false, false>(klo, khi, 0ull);
         if (warp == 0) {
-            const u64 t = warp_sum64(lane < kWarps ? sh.wmass[lane] : 0ull);
+            const u64 t = warp_sum64(lane < kWarps ? sh.wabove[lane] : 0ull);
             if (lane < a.C) put64(&sh.mass[rank], lane, t);
             __syncwarp();
         }
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         if (rank == 0) {
             u64 above_mass = 0ull;
             for (int c = 0; c < a.C; ++c) above_mass += sh.mass[c];
             border_of_list((int)inside, sh.above, above_mass, k, !by_k, total, false, false);
         }
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         return sh.found != 0;
+    }
+    // sum_kept() after border_by_counts() of top-p: the sums above the run are there, and the kept ones in it are in the lists.
+    __device__ __noinline__ void sum_listed(u64 border) {
+        for (int i = threadIdx.x; i < sh.mine; i += kThreads) {
+            const u64 key = list[i];
+            if (key >= border) {
+                const int piece = (int)(~(uint32_t)key + (uint32_t)row.skew) / EV;
+                atomicAdd(&sh.wabove[piece / (32 * a.iters) - rank * kWarps], w_of(key_value((uint32_t)(key >> 32))));
+            }
+        }
+        __syncwarp();
+        cta_sync();
+        if (lane == 0) sh.wmass[warp] = sh.wabove[warp];
+        publish_sums();
     }
 
     // The border among more keys than can be sorted: k > 0: the k-th token; else the first token at which the sum of w
@@ -697,7 +760,7 @@ struct Sampler {
                     __syncwarp();
                 }
             }
-            cluster_sync_all();
+            cluster_sync_all(a.C);
             // CTA r adds up its share of the bins over the cluster; the leader gets the sums
             const int share = kBins / a.C;
             uint32_t c4[kBins / kThreads];
@@ -715,7 +778,7 @@ struct Sampler {
                 }
             }
             __syncwarp();
-            cluster_sync_all();
+            cluster_sync_all(a.C);
 #pragma unroll
             for (int i = 0; i < kBins / kThreads; ++i) {
                 const int b = tid + i * kThreads;
@@ -724,7 +787,7 @@ struct Sampler {
                 put64(&mass[rank * share + b], 0, m4[i]);
             }
             __syncwarp();
-            cluster_sync_all();
+            cluster_sync_all(a.C);
             if (rank == 0) {
                 // thread t has the bins 4 t .. 4 t + 3; the first one at which the count or the sum gets there
                 constexpr int Q = kBins / kThreads;
@@ -790,10 +853,10 @@ struct Sampler {
                 }
                 __syncwarp();
             }
-            cluster_sync_all();
+            cluster_sync_all(a.C);
             if (!sh.found) {  // fewer tokens than k above `low`: everything that has a weight is kept
                 if (tid == 0) sh.border = 0ull;
-                cluster_sync_all();
+                cluster_sync_all(a.C);
                 return;
             }
             klo = sh.klo, khi = sh.khi, above = sh.above;
@@ -802,9 +865,9 @@ struct Sampler {
             linear = false;
             if (inside <= (uint32_t)kCap) {
                 collect<false, false>(klo, khi, floor);
-                cluster_sync_all();
+                cluster_sync_all(a.C);
                 if (rank == 0) border_of_list((int)inside, above, above_mass, k, !by_k, total, false, true);
-                cluster_sync_all();
+                cluster_sync_all(a.C);
                 return;
             }
             if (klo == khi) {
@@ -842,7 +905,7 @@ struct Sampler {
             if (lane < a.C) put32(&sh.count[rank], lane, t);
             __syncwarp();
         }
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         uint32_t before = 0u;
         for (int c = 0; c < rank; ++c) before += sh.count[c];
         for (int i = 0; i < warp; ++i) before += sh.wcount[i];
@@ -873,7 +936,7 @@ struct Sampler {
             }
         }
         __syncwarp();
-        cluster_sync_all();
+        cluster_sync_all(a.C);
     }
 
     __device__ __forceinline__ float border_logit(u64 border) const {
@@ -888,22 +951,13 @@ struct Sampler {
         const int iters = a.iters;
         const float lo = border_logit(border);
         u64 sum = 0ull;
-#pragma unroll 1
-        for (int it = 0; it < iters; ++it) {
-            float v[EV];
-            row.get(it, v);
-            const uint32_t in = kept(v, row.at(it), lo, border);
-            if (__any_sync(kFull, in != 0u)) sum += sum_in(weigh, v, in);
-        }
+        row.each(iters, [&](int it, const float (&v)[EV]) {
+            bool in[EV];
+            if (__any_sync(kFull, kept(v, row.at(it), lo, border, in))) sum += sum_in(weigh, v, in);
+        });
         sum = warp_sum64(sum);
         if (lane == 0) sh.wmass[warp] = sum;
-        cta_sync();
-        if (warp == 0) {
-            const u64 t = warp_sum64(lane < kWarps ? sh.wmass[lane] : 0ull);
-            if (lane < a.C) put64(&sh.mass[rank], lane, t);
-            __syncwarp();
-        }
-        cluster_sync_all();
+        publish_sums();
     }
 
     __device__ __forceinline__ void run(int t) {
@@ -916,13 +970,10 @@ struct Sampler {
             cp_async_wait_all_but<0>();
             __syncwarp();
         }
-#pragma unroll 1
-        for (int it = 0; it < iters; ++it) {
-            float v[EV];
-            row.get(it, v);
+        row.each(iters, [&](int, const float (&v)[EV]) {
 #pragma unroll
             for (int j = 0; j < EV; ++j) mine = max_nan(mine, v[j]);
-        }
+        });
         const int warps = a.C * kWarps, k0 = sh.k;
         // warps whose share lies in the row for certain; `full * jth` lane maxima bound the k-th logit
         const int full = max(1, min(warps, (a.V - EV) / (EV * 32 * a.iters)));
@@ -940,12 +991,14 @@ struct Sampler {
             }
             wj = key_value(__reduce_max_sync(kFull, key));
         }
+        // every CTA of the cluster runs (it arrived as it began) before its shared memory is written to
+        if (a.C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (lane < a.C) {
             put32(&sh.wtop[rank * kWarps + warp], lane, __float_as_uint(wm));
             put32(&sh.wjth[rank * kWarps + warp], lane, __float_as_uint(wj));
         }
         __syncwarp();
-        cluster_sync_all();
+        cluster_sync_all(a.C);
         float mm = -INFINITY;
         for (int i = lane; i < warps; i += 32) mm = max_nan(mm, sh.wtop[i]);
 #pragma unroll
@@ -964,6 +1017,7 @@ struct Sampler {
         least = greedy ? m : fmaxf(m - (float)a.shift / fac.hi, -3.4028234e38f);
         weigh.set(m, fac, a.shift, sh.table);
         u64 border = 0ull, total = 0ull;
+        bool summed = false;
         if (greedy) {
             border = (u64)order_key(m) << 32;
         } else if (by_k || by_p) {
@@ -1000,7 +1054,7 @@ struct Sampler {
             // the candidates; by top-p alone also the sum of all
             if (by_k) collect<false, true>(order_key(low), order_key(m), 0ull);
             else collect<true, true>(order_key(low), order_key(m), 0ull);
-            cluster_sync_all();
+            cluster_sync_all(a.C);
             uint32_t n = 0u;
             for (int c = 0; c < a.C; ++c) {
                 n += sh.count[c];
@@ -1009,12 +1063,13 @@ struct Sampler {
             // a bound of top-k has k tokens not below it (and without one everything that has a weight is a candidate)
             if (n <= (uint32_t)kCap) {
                 if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k, true);
-                cluster_sync_all();
+                cluster_sync_all(a.C);
                 border = sh.border;
             } else if (by_k != by_p && border_by_counts(by_k ? k0 : 0, total)) {
                 border = sh.border;
+                summed = by_p;
             } else {
-                cluster_sync_all();
+                cluster_sync_all(a.C);
                 u64 floor = 0ull;
                 if (by_k) {
                     border_by_ranges(k0, 0ull, low, 0ull);
@@ -1025,7 +1080,7 @@ struct Sampler {
                         sum_kept(floor);
                         total = 0ull;
                         for (int c = 0; c < a.C; ++c) total += sh.mass[c];
-                        cluster_sync_all();  // everybody has read the sums
+                        cluster_sync_all(a.C);  // everybody has read the sums
                     }
                     const float low_p = fmaxf(m + (log2f((1.f - p) / (float)a.V) - 0.05f) / fac.hi, least);
                     border_by_ranges(0, total, low_p, floor);
@@ -1050,10 +1105,12 @@ struct Sampler {
             }
             cta_sync();
             const u64 b = (u64)sh.klo << 32;
+            summed = summed && b <= border;
             border = b > border ? b : border;
         }
         cta_sync();
-        sum_kept(border);
+        if (summed) sum_listed(border);
+        else sum_kept(border);
         u64 S = 0ull, before = 0ull;
         for (int c = 0; c < a.C; ++c) {
             const u64 v = sh.mass[c];
@@ -1074,14 +1131,14 @@ struct Sampler {
             for (int it = 0; it < iters; ++it) {
                 float v[EV];
                 row.get(it, v);
-                const uint32_t in = kept(v, row.at(it), lo, border);
-                if (!__any_sync(kFull, in != 0u)) continue;
+                bool in[EV];
+                if (!__any_sync(kFull, kept(v, row.at(it), lo, border, in))) continue;
                 u64 w[EV], sum = 0ull;
 #pragma unroll
                 for (int j = 0; j < EV; j += 2) {
                     weigh.pair(v[j], v[j + 1], w[j], w[j + 1]);
-                    w[j] = in >> j & 1u ? w[j] : 0ull;
-                    w[j + 1] = in >> (j + 1) & 1u ? w[j + 1] : 0ull;
+                    w[j] = in[j] ? w[j] : 0ull;
+                    w[j + 1] = in[j + 1] ? w[j + 1] : 0ull;
                     sum += w[j] + w[j + 1];
                 }
                 const u64 incl = warp_scan64(sum);
@@ -1117,13 +1174,14 @@ struct Sampler {
 };
 
 template <typename E, bool HELD>
-__global__ void __launch_bounds__(kThreads, HELD ? 2 : 1) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int EV = 16 / sizeof(E);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x;
     const int t = blockIdx.x / a.C, rank = blockIdx.x - t * a.C;
     u64 *list = reinterpret_cast<u64 *>(smem), *sorted = list + kCap;
+    if (a.C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_wait();
     pdl_trigger();
     const E *x = static_cast<const E *>(a.x) + (size_t)t * a.V;
@@ -1135,15 +1193,21 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 1) sample_kernel(const __
     row.skew = skew;
     row.first = (((rank * kWarps + warp) * a.iters) * 32 + lane) * EV - skew;
     row.held = smem_addr(smem) + 2 * kCap * 8 + (warp * a.iters * 32 + lane) * 16;
+    float heat = 1.f, mp = 0.f, p = 1.f, u = 0.f;
+    int k = 0;
+    if (tid == 0) {
+        if (a.temperature) heat = a.temperature[t];
+        if (a.min_p) mp = a.min_p[t];
+        if (a.top_k) k = a.top_k[t];
+        if (a.top_p) p = a.top_p[t];
+        u = a.u[t];
+    }
     if (HELD) row.load(a.iters);
     if (tid < 32) sh.table[tid] = kPow2.v[tid];
     if (tid == 0) {
-        const float heat = a.temperature ? a.temperature[t] : 1.f;
-        const float mp = a.min_p ? a.min_p[t] : 0.f;
-        sh.k = a.top_k ? a.top_k[t] : 0;
-        sh.p = a.top_p ? a.top_p[t] : 1.f;
-        sh.u = a.u[t];
-        sh.p = sh.p < 1.f ? fmaxf(sh.p, 0.f) : 1.f;  // NaN: off
+        sh.k = k;
+        sh.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;  // NaN: off
+        sh.u = u;
         if (heat > 0.f) {
             // log2(e) / heat in two parts: the quotient of the significands and its remainder's
             const float h = fminf(fmaxf(heat, 8.5e-39f), 3.4028234e38f);
@@ -1161,10 +1225,9 @@ __global__ void __launch_bounds__(kThreads, HELD ? 2 : 1) sample_kernel(const __
     }
     cta_sync();
     Sampler<E, HELD> s{a, sh, list, sorted, row, rank, lane, warp, 0.f, 0.f, Factor{}, Weigh{}, 0.f};
-    cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written to
     s.run(t);
     __syncwarp();
-    cluster_sync_all();  // nobody leaves while others may still reach for its shared memory
+    cluster_sync_all(a.C);  // nobody leaves while others may still reach for its shared memory
 }
 
 template <typename E, bool HELD>
@@ -1199,15 +1262,16 @@ rl_status run_sample(SampleArgs &a, int T, cudaStream_t s) {
     const int pieces = even ? a.V / EV : (a.V + 2 * (EV - 1)) / EV;
     // CTAs per row: 64 KB of it each; with few rows as many as still leave every thread a piece
     const int sms = sm_count();
-    a.C = 1;
-    while (a.C < kMaxC && (pieces > a.C * 8 * kThreads || ((long long)T * a.C * 2 <= sms && pieces > a.C * kThreads))) a.C *= 2;
+    const bool streamed = T >= sms;
+    a.C = streamed && pieces >= 16 * kThreads ? 2 : 1;
+    while (!streamed && a.C < kMaxC && (pieces > a.C * 8 * kThreads || ((long long)T * a.C * 2 <= sms && pieces > a.C * kThreads))) a.C *= 2;
     const int per = (pieces + a.C - 1) / a.C;
     a.iters = (per + kThreads - 1) / kThreads;
     a.shift = 63;
     for (int v = 1; v < a.V; v *= 2) --a.shift;  // the sum of V weights stays below 2^64
     if (a.shift > 46) a.shift = 46;
     // 227 KB of shared memory per CTA: 24 pieces of 8 KB beside the lists
-    if (a.iters <= 22) return launch_sample<E, true>(a, T, s);
+    if (a.iters <= (streamed ? 4 : 22)) return launch_sample<E, true>(a, T, s);
     return launch_sample<E, false>(a, T, s);
 }
 
