@@ -40,7 +40,9 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxC = 8;                  // CTAs of a cluster
 constexpr int kCap = 2048;                // candidates that are sorted
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;               // of border_by_ranges()
+constexpr int kCounts = 2048;             // of border_by_counts()
+constexpr int kFixedBytes = 2 * kCap * 8 + kCounts * 4;  // shared memory beside the row
 constexpr int kMaxV = 1 << 26;
 
 struct Pow2Table {
@@ -69,7 +71,7 @@ struct SampleArgs {
     const int32_t *top_k;
     int32_t *ids;
     float *logprob;
-    int V, C, iters, shift;  // iters: pieces of 16 bytes per thread; w = multiples of 2^-shift
+    int V, C, per, iters, shift;  // pieces of 16 bytes per CTA and per thread; w = multiples of 2^-shift
 };
 
 // log2(e) / temperature as hi + lo * pre (pre: 1, or 2^-24 where lo by itself would leave f32's normal range)
@@ -288,7 +290,7 @@ struct Row {
 };
 
 // ---- the sort of the candidates ----------------------------------------------------------------
-// N = EPT * kThreads keys in buf, descending.  Element e kThreads + tid is in this thread's register e: exchanges
+// EPT * kThreads keys in buf, descending.  Element e kThreads + tid is in this thread's register e: exchanges
 // at a distance of kThreads and more stay in the thread, below 32 in the warp, the others go through buf.
 template <int EPT>
 __device__ __noinline__ void sort_keys(u64 *buf) {
@@ -344,7 +346,8 @@ struct Sampler {
     static constexpr int EV = R::EV;
     const SampleArgs &a;
     Shared &sh;
-    u64 *list, *sorted;                  // kCap keys each; together the histograms
+    u64 *list, *sorted;                  // kCap keys each; together the histograms of border_by_ranges()
+    uint32_t *counts;                    // kCounts
     R row;
     int rank, lane, warp;
     float m, least;                      // least: the smallest logit that has a weight
@@ -353,7 +356,7 @@ struct Sampler {
     float bin_scale;                     // bins per unit of the logit
 
     // bins of equal width in the logit, 0 at the maximum; monotone
-    __device__ __forceinline__ int bin(float l) const { return min((int)((m - l) * bin_scale), kBins - 1); }
+    __device__ __forceinline__ int bin(float l) const { return min((int)((m - l) * bin_scale), kCounts - 1); }
     // the sum that the tokens kept by top-p reach: a share p < 1 of `total`, at least the first token's
     __device__ __forceinline__ u64 share_of(u64 total) const {
         const u64 t = share(sh.p, total, true);
@@ -398,38 +401,39 @@ struct Sampler {
     }
 
     // Tokens whose logit's key lies in [klo, khi] and that are not below `floor` into this CTA's list; sh.count
-    // has their numbers after the next cluster barrier, also beyond kCap.  With ALL also the sums of all w
-    // (sh.mass).
-    // With HIST also the numbers of these tokens by bin() of their logit.
-    template <bool ALL, bool HIST>
+    // has their numbers after the next cluster barrier (anything beyond kCap where they are more).  With ALL also
+    // the sums of all w (sh.mass), with ABOVE the sums of the w of the tokens above khi (sh.mass, and sh.wabove by warp).
+    template <bool ALL, bool ABOVE = false>
     __device__ __noinline__ void collect(uint32_t klo, uint32_t khi, u64 floor) {
         // (the members in registers: they lie in local memory, where every use in a loop would load them again)
         const Weigh weigh = this->weigh;
         const R row = this->row;
         const int iters = a.iters;
-        const float m = this->m, least = this->least, bin_scale = this->bin_scale;
-        auto bin = [&](float l) { return min((int)((m - l) * bin_scale), kBins - 1); };
+        const float least = this->least;
         u64 *const list = this->list;
-        uint32_t *hist = reinterpret_cast<uint32_t *>(sorted);
-        if (HIST)
-            for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0u;
         if (threadIdx.x == 0) sh.mine = 0;
         cta_sync();
-        const float lo = key_value(klo);
+        const float lo = key_value(klo), hi = key_value(khi);
         u64 sum = 0ull;
         row.each(iters, [&](int it, const float (&v)[EV]) {
             if (ALL) {
                 bool all[EV];
                 if (__any_sync(kFull, at_least(v, least, all))) sum += sum_in(weigh, v, all);
             }
+            if (ABOVE) {
+                bool over[EV], any = false;
+#pragma unroll
+                for (int j = 0; j < EV; ++j) {
+                    over[j] = v[j] > hi;
+                    any = any || over[j];
+                }
+                if (__any_sync(kFull, any)) sum += sum_in(weigh, v, over);
+            }
             bool some[EV];
             if (!__any_sync(kFull, at_least(v, lo, some))) return;
             uint32_t in = 0u;
 #pragma unroll
-            for (int j = 0; j < EV; ++j) {
-                if (HIST && some[j]) atomicAdd(&hist[bin(v[j])], 1u);
-                in |= some[j] ? 1u << j : 0u;
-            }
+            for (int j = 0; j < EV; ++j) in |= some[j] ? 1u << j : 0u;
             // beyond kCap the number does not matter: the list is not used
             if (in && *reinterpret_cast<volatile int *>(&sh.mine) <= kCap) {
 #pragma unroll 1
@@ -448,17 +452,17 @@ struct Sampler {
             }
             __syncwarp();
         });
-        if (ALL) {
+        if (ALL || ABOVE) {
             sum = warp_sum64(sum);
-            if (lane == 0) sh.wmass[warp] = sum;
+            if (lane == 0) (ABOVE ? sh.wabove : sh.wmass)[warp] = sum;
         }
         cta_sync();
         if (warp == 0) {
-            u64 t = ALL && lane < kWarps ? sh.wmass[lane] : 0ull;
-            if (ALL) t = warp_sum64(t);
+            u64 t = (ALL || ABOVE) && lane < kWarps ? (ABOVE ? sh.wabove : sh.wmass)[lane] : 0ull;
+            if (ALL || ABOVE) t = warp_sum64(t);
             if (lane < a.C) {
                 put32(&sh.count[rank], lane, (uint32_t)sh.mine);
-                if (ALL) put64(&sh.mass[rank], lane, t);
+                if (ALL || ABOVE) put64(&sh.mass[rank], lane, t);
             }
             __syncwarp();
         }
@@ -476,26 +480,28 @@ struct Sampler {
             while (at >= (int)sh.count[c]) at -= (int)sh.count[c++];
             sorted[i] = get64(&list[at], c);
         }
-        const int ept = n <= kThreads ? 1 : n <= 2 * kThreads ? 2 : 4;
+        constexpr int kMost = kCap / kThreads;
+        const int ept = n <= kThreads ? 1 : n <= 2 * kThreads ? 2 : kMost;
         for (int i = n + tid; i < ept * kThreads; i += kThreads) sorted[i] = 0ull;
         cta_sync();
-        if (n <= 128) {  // by counting the larger ones, four lanes per key
-            const int i = tid >> 2;
+        if (n <= 128) {  // by counting the larger ones, several lanes per key
+            constexpr int L = kThreads / 128;
+            const int i = tid / L;
             const u64 mine = sorted[i];
             int rank = 0;
 #pragma unroll 4
-            for (int j = tid & 3; j < n; j += 4) rank += sorted[j] > mine ? 1 : 0;
-            rank += __shfl_xor_sync(kFull, rank, 1);
-            rank += __shfl_xor_sync(kFull, rank, 2);
+            for (int j = tid % L; j < n; j += L) rank += sorted[j] > mine ? 1 : 0;
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
             cta_sync();
-            if (i < n && (tid & 3) == 0) sorted[rank] = mine;
+            if (i < n && tid % L == 0) sorted[rank] = mine;
             cta_sync();
         } else if (ept == 1) sort_keys<1>(sorted);
         else if (ept == 2) sort_keys<2>(sorted);
-        else sort_keys<4>(sorted);
+        else sort_keys<kMost>(sorted);
         // running sums: thread t has the places ept t .. ept t + ept - 1
-        u64 key[4], w[4], sum = 0ull;
-        for (int e = 0; e < 4; ++e) {
+        u64 key[kMost], w[kMost], sum = 0ull;
+        for (int e = 0; e < kMost; ++e) {
             const int i = ept * tid + e;
             key[e] = e < ept && i < n ? sorted[i] : 0ull;
             w[e] = key[e] ? w_of(key_value((uint32_t)(key[e] >> 32))) : 0ull;
@@ -553,16 +559,31 @@ struct Sampler {
         cluster_sync_all(a.C);
     }
 
-    // The border from the counts that collect() left in the cluster (bins of [low, m]): k > 0: the bin of the k-th token;
+    // The border from the counts of the tokens of [sh.bound, m] by bin(): k > 0: the bin of the k-th token;
     // else a run of bins around the place where the sum, estimated from the counts and the bins' middles, reaches
     // p times `total`.  The tokens above it are summed up exactly, those in it sorted.  False (nothing decided): the
     // run is too large or, by the exact sums, does not hold the border.  Whole cluster.
     __device__ __noinline__ bool border_by_counts(int k, u64 total) {
         const int tid = threadIdx.x;
-        uint32_t *cnt = reinterpret_cast<uint32_t *>(sorted);
+        uint32_t *const cnt = counts;
+        {
+            const R row = this->row;
+            const float low = sh.bound, m = this->m, bin_scale = this->bin_scale;
+            for (int i = tid; i < kCounts; i += kThreads) cnt[i] = 0u;
+            cta_sync();
+            row.each(a.iters, [&](int, const float (&v)[EV]) {
+                bool some[EV];
+                if (!__any_sync(kFull, at_least(v, low, some))) return;
+#pragma unroll
+                for (int j = 0; j < EV; ++j)
+                    if (some[j]) atomicAdd(&cnt[min((int)((m - v[j]) * bin_scale), kCounts - 1)], 1u);
+                __syncwarp();
+            });
+            cluster_sync_all(a.C);
+        }
         const bool by_k = k > 0;
-        constexpr int Q = kBins / kThreads;
-        const int part = kBins / a.C;
+        constexpr int Q = kCounts / kThreads;
+        const int part = kCounts / a.C;
         uint32_t c4[Q];
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -616,13 +637,15 @@ struct Sampler {
             }
             cta_sync();
             if (sh.found) {
-                if (!by_k && tid == 0) {  // as many bins to both sides as half of the list takes
+                if (!by_k && tid == 0) {  // a bin or more to both sides
                     int b0 = (int)sh.klo, b1 = b0;
                     uint32_t in = sh.inside;
-                    for (int i = 0; i < 64 && in <= kCap / 2; ++i) {
+                    for (int i = 0; i < 32 && in <= 64; ++i) {
                         if (b0 > 0) --b0, in += cnt[b0], sh.above -= cnt[b0];
-                        if (b1 < kBins - 1) ++b1, in += cnt[b1];
+                        if (b1 < kCounts - 1) ++b1, in += cnt[b1];
                     }
+                    if (b0 > 0 && b0 == (int)sh.klo && in + cnt[b0 - 1] <= kCap) --b0, in += cnt[b0], sh.above -= cnt[b0];
+                    if (b1 < kCounts - 1 && b1 == (int)sh.klo && in + cnt[b1 + 1] <= kCap) ++b1, in += cnt[b1];
                     sh.klo = b1, sh.khi = b0, sh.inside = in;  // higher bins hold smaller logits
                 }
                 cta_sync();
@@ -665,31 +688,9 @@ struct Sampler {
         }
         const uint32_t klo = sh.klo, khi = sh.khi, inside = sh.inside;
         if (inside > (uint32_t)kCap) return false;
-        // sums above the run, and its tokens
-        const Weigh weigh = this->weigh;
-        const R row = this->row;
-        const int iters = a.iters;
-        u64 sum = 0ull;
-        if (!by_k) {
-            const float above = key_value(khi);
-            row.each(iters, [&](int, const float (&v)[EV]) {
-                bool in[EV], any = false;
-#pragma unroll
-                for (int j = 0; j < EV; ++j) {
-                    in[j] = v[j] > above;
-                    any = any || in[j];
-                }
-                if (__any_sync(kFull, any)) sum += sum_in(weigh, v, in);
-            });
-            sum = warp_sum64(sum);
-        }
-        if (lane == 0) sh.wabove[warp] = sum;
-        collect<false, false>(klo, khi, 0ull);
-        if (warp == 0) {
-            const u64 t = warp_sum64(lane < kWarps ? sh.wabove[lane] : 0ull);
-            if (lane < a.C) put64(&sh.mass[rank], lane, t);
-            __syncwarp();
-        }
+        // the sums above the run, and its tokens
+        if (by_k) collect<false>(klo, khi, 0ull);
+        else collect<false, true>(klo, khi, 0ull);
         cluster_sync_all(a.C);
         if (rank == 0) {
             u64 above_mass = 0ull;
@@ -699,7 +700,8 @@ struct Sampler {
         cluster_sync_all(a.C);
         return sh.found != 0;
     }
-    // sum_kept() after border_by_counts() of top-p: the sums above the run are there, and the kept ones in it are in the lists.
+    // sum_kept() from the lists, on top of the sums in sh.wabove: after border_by_counts() of top-p (those above the run), or
+    // where all kept tokens are in the lists.
     __device__ __noinline__ void sum_listed(u64 border) {
         for (int i = threadIdx.x; i < sh.mine; i += kThreads) {
             const u64 key = list[i];
@@ -731,14 +733,14 @@ struct Sampler {
         if (tid == 0) sh.target = by_k ? 0ull : share_of(total);
         cta_sync();
         const u64 target = sh.target;
-        bin_scale = fminf(kBins / fmaxf(m - low, 1e-37f), 1e37f);
+        const float scale = fminf(kBins / fmaxf(m - low, 1e-37f), 1e37f);
         bool linear = true;
 #pragma unroll 1
         for (;;) {
             const int sh_bits = max(0, 32 - __clz((khi - klo) | 1u) - 11);
             // bin 0 holds the largest logits; both maps are monotone
             auto bin_of = [&](float l, uint32_t key) {
-                return linear ? bin(l) : (int)((khi - key) >> sh_bits);
+                return linear ? min((int)((m - l) * scale), kBins - 1) : (int)((khi - key) >> sh_bits);
             };
             for (int i = tid; i < kBins; i += kThreads) cnt[i] = 0u, mass[i] = 0ull;
             cta_sync();
@@ -864,7 +866,7 @@ struct Sampler {
             const uint32_t inside = sh.inside;
             linear = false;
             if (inside <= (uint32_t)kCap) {
-                collect<false, false>(klo, khi, floor);
+                collect<false>(klo, khi, floor);
                 cluster_sync_all(a.C);
                 if (rank == 0) border_of_list((int)inside, above, above_mass, k, !by_k, total, false, true);
                 cluster_sync_all(a.C);
@@ -1017,54 +1019,65 @@ struct Sampler {
         least = greedy ? m : fmaxf(m - (float)a.shift / fac.hi, -3.4028234e38f);
         weigh.set(m, fac, a.shift, sh.table);
         u64 border = 0ull, total = 0ull;
-        bool summed = false;
+        bool summed = false, in_list = false;  // the kept tokens' sums: above a run already; all of them are in the lists
         if (greedy) {
             border = (u64)order_key(m) << 32;
         } else if (by_k || by_p) {
+            // A bound for the list: the k-th largest of the warps' maxima (for top-p alone, three quarters of their number:
+            // a few hundred tokens, which mostly hold the share p), or the smallest j-th largest lane maximum.
+            const int nth = by_k ? jth == 1 ? k0 : 0 : max(1, full * 3 / 4);
             if (tid == 0) sh.bound = -INFINITY;
             cta_sync();
-            if (by_k && jth == 1) {
-                // the k-th largest of the warps' maxima, 4 threads for each
-                const int i = tid >> 2;
-                const float own = i < warps ? sh.wjth[i] : 0.f;
+            if (nth > 0) {
+                const int i = tid >> 2;  // 4 threads for each warp
+                const float own = i < warps ? sh.wtop[i] : 0.f;
                 int above = 0;
                 if (i < warps)
-                    for (int q = tid & 3; q < warps; q += 4) above += sh.wjth[q] > own || (sh.wjth[q] == own && q < i) ? 1 : 0;
+                    for (int q = tid & 3; q < warps; q += 4) above += sh.wtop[q] > own || (sh.wtop[q] == own && q < i) ? 1 : 0;
                 above += __shfl_xor_sync(kFull, above, 1);
                 above += __shfl_xor_sync(kFull, above, 2);
-                if (i < warps && (tid & 3) == 0 && above == k0 - 1) sh.bound = own;
-            } else if (by_k && jth <= 32) {
-                if (warp == 0) {
-                    float lo = INFINITY;
-                    for (int i = lane; i < full; i += 32) lo = fminf(lo, sh.wjth[i]);
+                if (i < warps && (tid & 3) == 0 && above == nth - 1) sh.bound = own;
+            } else if (jth <= 32 && warp == 0) {
+                float lo = INFINITY;
+                for (int i = lane; i < full; i += 32) lo = fminf(lo, sh.wjth[i]);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-                    if (lane == 0) sh.bound = lo;
-                }
-            } else if (!by_k && tid == 0) {
-                sh.bound = m + (log2f((1.f - p) / (float)a.V) - 0.05f) / fac.hi;
+                for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+                if (lane == 0) sh.bound = lo;
             }
+            // Top-p: all tokens below w = (1 - p) M' / V together have less than 1 - p of the sum, M' being what the warps'
+            // maxima alone add up to.
+            float sum = 0.f;
+            for (int i = lane; i < warps; i += 32) sum += exp2f((sh.wtop[i] - m) * fac.hi);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            const float low_p = fmaxf(fminf(m + (log2f((1.f - p) * sum / (float)a.V) - 0.05f) / fac.hi, m), least);
             __syncwarp();
             cta_sync();
-            const float bound = sh.bound;
-            const float low = fmaxf(bound, least);
-            bin_scale = fminf(kBins / fmaxf(m - low, 1e-37f), 1e37f);
+            float bound = fmaxf(sh.bound, least), low = by_k ? bound : low_p;
+            if (a.V <= kCap) bound = low;
+            bound = fmaxf(bound, low);
+            bin_scale = fminf(kCounts / fmaxf(m - low, 1e-37f), 1e37f);
             cta_sync();
             if (tid == 0) sh.bound = low;
             // the candidates; by top-p alone also the sum of all
-            if (by_k) collect<false, true>(order_key(low), order_key(m), 0ull);
-            else collect<true, true>(order_key(low), order_key(m), 0ull);
+            if (by_k) collect<false>(order_key(bound), order_key(m), 0ull);
+            else collect<true>(order_key(bound), order_key(m), 0ull);
             cluster_sync_all(a.C);
             uint32_t n = 0u;
             for (int c = 0; c < a.C; ++c) {
                 n += sh.count[c];
                 total += by_k ? 0ull : sh.mass[c];
             }
-            // a bound of top-k has k tokens not below it (and without one everything that has a weight is a candidate)
+            // by top-k the list holds the k-th token (or all that have a weight); by top-p alone it may end too early
+            bool done = false;
             if (n <= (uint32_t)kCap) {
-                if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k, true);
+                if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k, by_k || bound == low);
                 cluster_sync_all(a.C);
+                done = sh.found != 0;
+            }
+            if (done) {
                 border = sh.border;
+                in_list = true;
             } else if (by_k != by_p && border_by_counts(by_k ? k0 : 0, total)) {
                 border = sh.border;
                 summed = by_p;
@@ -1082,8 +1095,7 @@ struct Sampler {
                         for (int c = 0; c < a.C; ++c) total += sh.mass[c];
                         cluster_sync_all(a.C);  // everybody has read the sums
                     }
-                    const float low_p = fmaxf(m + (log2f((1.f - p) / (float)a.V) - 0.05f) / fac.hi, least);
-                    border_by_ranges(0, total, low_p, floor);
+                    border_by_ranges(0, total, by_k ? least : low_p, floor);
                     border = sh.border > floor ? sh.border : floor;
                 }
             }
@@ -1109,7 +1121,9 @@ struct Sampler {
             border = b > border ? b : border;
         }
         cta_sync();
-        if (summed) sum_listed(border);
+        if (in_list && tid < kWarps) sh.wabove[tid] = 0ull;
+        cta_sync();
+        if (summed || in_list) sum_listed(border);
         else sum_kept(border);
         u64 S = 0ull, before = 0ull;
         for (int c = 0; c < a.C; ++c) {
@@ -1192,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     row.V = a.V;
     row.skew = skew;
     row.first = (((rank * kWarps + warp) * a.iters) * 32 + lane) * EV - skew;
-    row.held = smem_addr(smem) + 2 * kCap * 8 + (warp * a.iters * 32 + lane) * 16;
+    row.held = smem_addr(smem) + kFixedBytes + (warp * a.iters * 32 + lane) * 16;
     float heat = 1.f, mp = 0.f, p = 1.f, u = 0.f;
     int k = 0;
     if (tid == 0) {
@@ -1224,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         sh.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;
     }
     cta_sync();
-    Sampler<E, HELD> s{a, sh, list, sorted, row, rank, lane, warp, 0.f, 0.f, Factor{}, Weigh{}, 0.f};
+    Sampler<E, HELD> s{a, sh, list, sorted, reinterpret_cast<uint32_t *>(sorted + kCap), row, rank, lane, warp, 0.f, 0.f, Factor{}, Weigh{}, 0.f};
     s.run(t);
     __syncwarp();
     cluster_sync_all(a.C);  // nobody leaves while others may still reach for its shared memory
@@ -1233,7 +1247,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 template <typename E, bool HELD>
 rl_status launch_sample(SampleArgs &a, int T, cudaStream_t s) {
     auto kernel = sample_kernel<E, HELD>;
-    const size_t smem = 2 * kCap * 8 + (HELD ? (size_t)a.iters * kThreads * 16 : 0);
+    a.iters = (a.per + kThreads - 1) / kThreads;
+    const size_t smem = kFixedBytes + (HELD ? (size_t)a.iters * kThreads * 16 : 0);
     rl_status st = allow_smem((const void *)kernel, smem);
     if (st != RL_OK) return st;
     cudaLaunchConfig_t cfg = {};
@@ -1265,13 +1280,12 @@ rl_status run_sample(SampleArgs &a, int T, cudaStream_t s) {
     const bool streamed = T >= sms;
     a.C = streamed && pieces >= 16 * kThreads ? 2 : 1;
     while (!streamed && a.C < kMaxC && (pieces > a.C * 8 * kThreads || ((long long)T * a.C * 2 <= sms && pieces > a.C * kThreads))) a.C *= 2;
-    const int per = (pieces + a.C - 1) / a.C;
-    a.iters = (per + kThreads - 1) / kThreads;
+    a.per = (pieces + a.C - 1) / a.C;
     a.shift = 63;
     for (int v = 1; v < a.V; v *= 2) --a.shift;  // the sum of V weights stays below 2^64
     if (a.shift > 46) a.shift = 46;
     // 227 KB of shared memory per CTA: 24 pieces of 8 KB beside the lists
-    if (a.iters <= (streamed ? 4 : 22)) return launch_sample<E, true>(a, T, s);
+    if (a.per <= (streamed ? 4 : 22) * kThreads) return launch_sample<E, true>(a, T, s);
     return launch_sample<E, false>(a, T, s);
 }
 
