@@ -26,6 +26,83 @@ from ._lib import RL_NO_EARLY_OUT, RlShape
 EPS = 1e-6
 
 
+def pack_f8(weight: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """A float matrix [N][K] in the format of rl_f8_matmul and rl_f8_gated: (w e4m3 [N][K], scale f32
+    [ceil(N / 128)][ceil(K / 128)]), the largest magnitude of each block of 128 x 128 mapped to 448."""
+    N, K = weight.shape
+    v = torch.nn.functional.pad(weight.float(), (0, -K % 128, 0, -N % 128))
+    v = v.view(-(-N // 128), 128, -(-K // 128), 128)
+    scale = v.abs().amax((1, 3)) / 448
+    q = v / torch.where(scale > 0, scale, torch.ones_like(scale))[:, None, :, None]
+    q = q.reshape(-(-N // 128) * 128, -1)[:N, :K].clamp(-448, 448)
+    return q.to(torch.float8_e4m3fn).contiguous(), scale.contiguous()
+
+
+@dataclass
+class SharedExpert:
+    """A gated feed-forward block in 8 bits that every token of a layer goes through, beside the routed experts:
+    x += down(silu(gate RMSNorm(x)) * (up RMSNorm(x))).  Buffers for up to T tokens; a smaller step uses their first
+    rows.  The blocks of several layers may share buffers (`like`)."""
+    gate: tuple[torch.Tensor, torch.Tensor]  # e4m3 [I][H], f32 scales of blocks of 128 x 128
+    up: tuple[torch.Tensor, torch.Tensor]
+    down: tuple[torch.Tensor, torch.Tensor]  # e4m3 [H][I]
+    q: torch.Tensor                          # e4m3 [T][H], the normalised rows
+    q_scale: torch.Tensor                    # f32 [T][ceil(H / 128)]
+    h: torch.Tensor                          # e4m3 [T][I]
+    h_scale: torch.Tensor                    # f32 [T][ceil(I / 128)]
+
+    @staticmethod
+    def make(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, T: int,
+             like: "SharedExpert | None" = None) -> "SharedExpert":
+        I, H = gate.shape
+        if up.shape != gate.shape or down.shape != (H, I):
+            raise ValueError(f"gate {tuple(gate.shape)}, up {tuple(up.shape)}, down {tuple(down.shape)}: "
+                             "[inter][hidden], the same and [hidden][inter] expected")
+        if H % 128 or I % 16:
+            raise ValueError(f"hidden {H}, inter {I}: multiples of 128 and of 16 expected")
+        d = gate.device
+        f = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, device=d)  # noqa: E731
+        bufs = (like.q, like.q_scale, like.h, like.h_scale) if like is not None else (
+            f(T, H, dtype=torch.float8_e4m3fn), f(T, H // 128), f(T, I, dtype=torch.float8_e4m3fn), f(T, -(-I // 128)))
+        if bufs[0].shape != (T, H) or bufs[2].shape != (T, I):
+            raise ValueError(f"the buffers to share hold {tuple(bufs[0].shape)} and {tuple(bufs[2].shape)}")
+        return SharedExpert(pack_f8(gate), pack_f8(up), pack_f8(down), *bufs)
+
+
+def _shared(model, layer: int, T: int) -> SharedExpert | None:
+    """The layer's shared expert, or None; refuses a step of more tokens than its buffers hold."""
+    shared = getattr(model, "shared", None)
+    if shared is None:
+        return None
+    if len(shared) != model.L:
+        raise ValueError(f"{len(shared)} shared experts for {model.L} layers")
+    e = shared[layer]
+    if e.q.shape[1] != model.w.hidden or T > e.q.shape[0]:
+        raise ValueError(f"{T} tokens of {model.w.hidden}: the shared expert's buffers hold {tuple(e.q.shape)}")
+    return e
+
+
+def _routed_only(model, what: str) -> None:
+    if getattr(model, "shared", None) is not None:
+        raise ValueError(f"{what} runs the routed experts only, and this model has shared experts: "
+                         "use enqueue_tokens or the prefill chunk")
+
+
+def enqueue_shared_input(e: SharedExpert, x: torch.Tensor, T: int) -> None:
+    """The shared expert's input, RMSNorm(x) in 8 bits: before the routed experts add to x."""
+    H = x.shape[1]
+    L.rl_add_rmsnorm(x, T, H, EPS, q=e.q[:T], scale=e.q_scale[:T], group=128)
+
+
+def enqueue_shared(e: SharedExpert, layer: int, y: torch.Tensor, T: int, ctrl: torch.Tensor) -> None:
+    """y += the shared expert of the rows that enqueue_shared_input wrote; nothing where layer `layer` or an
+    earlier one stopped the chain (its routed experts did not run either)."""
+    H, I = y.shape[1], e.h.shape[1]
+    h, h_scale = e.h[:T], e.h_scale[:T]
+    L.rl_f8_gated(*e.gate, *e.up, e.q[:T], e.q_scale[:T], T, I, H, q=h, scale=h_scale, layer=layer, ctrl=ctrl)
+    L.rl_f8_matmul(*e.down, h, h_scale, y, T, H, I, res=y, layer=layer, ctrl=ctrl)
+
+
 def shape_of(w) -> RlShape:
     return RlShape.of(w.hidden, w.n_experts, w.top_k, w.inter, w.n_layers)
 
@@ -40,6 +117,7 @@ class Model:
         import synth
         self.w = w
         self.L = w.n_layers if layers is None else layers
+        self.shared: list[SharedExpert] | None = None  # one per layer, added beside the routed experts (stacked layers)
         self.shape = RlShape.of(w.hidden, w.n_experts, w.top_k, w.inter, self.L)
         self.device = torch.device(device)
         E, H, rb = w.n_experts, w.hidden, w.record_bytes
@@ -191,6 +269,7 @@ def enqueue_decode_token(model: Model, b: DecodeBuffers, x_in: torch.Tensor, y_o
     stacked=True: x = x_in; per layer x = x + MoE(RMSNorm(x)) (the router and the experts
     normalise x on the fly); y_out = x.
     x_hist[l] (optional) receives layer l's input for per-layer checks."""
+    _routed_only(model, "enqueue_decode_token")
     shp = model.shape
     if not stacked:
         for l in range(model.L):
@@ -233,6 +312,7 @@ def enqueue_decode_token_fused(model: Model, b: DecodeBuffers, x_in: torch.Tenso
     last bits.  x_hist[l] (optional) receives layer l's input.
     pregate > 0 prefetches into L2 the next layer's predicted experts (never changes results);
     pregate_hits[l] (optional) receives how many of layer l's experts were predicted."""
+    _routed_only(model, "enqueue_decode_token_fused")
     y_out.copy_(x_in)
     L.moe_decode_stack(model.shape, layer0, model.L - layer0, y_out, EPS, model.routers, model.bias, model.table,
                        model.codebook, b.ids, b.weights, b.slots, b.miss, b.ctrl, b.logits if keep_logits else None,
@@ -280,12 +360,18 @@ def enqueue_tokens_layer(model: Model, b: TokensBuffers, layer: int, x: torch.Te
                          stacked: bool, routed: bool = True, logits: torch.Tensor | None = None) -> None:
     """One layer for the tokens x [T][H], router and experts in ONE launch:
     stacked: y = x + MoE(RMSNorm(x)) in place (y is x), else y = MoE(x).  routed=False runs the
-    experts with the ids and weights b holds (after a fill and rl_resolve_slots)."""
+    experts with the ids and weights b holds (after a fill and rl_resolve_slots).  A stacked layer of a model with
+    shared experts adds the layer's too: y = x + MoE(RMSNorm(x)) + shared(RMSNorm(x))."""
     T = _step_tokens(model, b, x, y)
+    shared = _shared(model, layer, T) if stacked else None
+    if shared is not None:
+        enqueue_shared_input(shared, x, T)
     L.moe_decode_tokens(model.shape, layer, T, x, EPS if stacked else -1.0, model.routers[layer] if routed else None,
                         None if model.bias is None else model.bias[layer], model.table, model.codebook,
                         b.ids[layer, :T], b.weights[layer, :T], b.slots[layer, :T], b.miss, b.ctrl, logits, y,
                         int(stacked), b.ws, b.ws.numel())
+    if shared is not None:
+        enqueue_shared(shared, layer, y, T, b.ctrl)
 
 
 def enqueue_tokens(model: Model, b: TokensBuffers, x_in: torch.Tensor, y_out: torch.Tensor, layer0: int = 0) -> None:
@@ -313,10 +399,10 @@ def pack_q4(weight: torch.Tensor, group: int = 128) -> tuple[torch.Tensor, torch
 
 @dataclass
 class Head:
-    """The end of a verification step: final RMSNorm with gain into 8 bits, an output head in 4
-    bits, log probabilities.  Buffers for up to T tokens; a smaller step uses their first rows."""
-    w: torch.Tensor            # uint8 [V][H / 2]
-    scale: torch.Tensor        # half [V][H / group]
+    """The end of a verification step: final RMSNorm with gain into 8 bits, an output head in 4 bits (or 8), log
+    probabilities.  Buffers for up to T tokens; a smaller step uses their first rows."""
+    w: torch.Tensor            # uint8 [V][H / 2]; in 8 bits e4m3 [V][H]
+    scale: torch.Tensor        # half [V][H / group]; in 8 bits f32 [ceil(V / 128)][H / 128]
     gain: torch.Tensor | None  # f32 [H]
     group: int
     q: torch.Tensor            # e4m3 [T][H]
@@ -327,18 +413,46 @@ class Head:
     top_ids: torch.Tensor | None
     top_logprob: torch.Tensor | None
     ws: torch.Tensor           # zero-filled: completion counters of rl_logprobs
+    bits: int = 4
 
     @staticmethod
-    def make(weight: torch.Tensor, T: int, gain: torch.Tensor | None = None, group: int = 128, top_n: int = 0) -> "Head":
+    def make(weight: torch.Tensor, T: int, gain: torch.Tensor | None = None, group: int = 128, top_n: int = 0,
+             bits: int = 4) -> "Head":
         V, H = weight.shape
         d = weight.device
-        w, scale = pack_q4(weight, group)
+        if bits not in (4, 8) or (bits == 8 and (group != 128 or H % 128)):
+            raise ValueError(f"a head of {bits} bits with groups of {group} and {H} columns: 4 bits, or 8 with "
+                             "groups of 128 and a multiple of 128 columns")
+        w, scale = pack_q4(weight, group) if bits == 4 else pack_f8(weight)
         f = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, device=d)  # noqa: E731
         return Head(w=w, scale=scale, gain=gain, group=group, q=f(T, H, dtype=torch.float8_e4m3fn),
                     q_scale=f(T, H // group), logits=f(T, V), logprob=f(T), entropy=f(T),
                     top_ids=f(T, top_n, dtype=torch.int32) if top_n else None,
                     top_logprob=f(T, top_n) if top_n else None,
-                    ws=f(L.rl_logprobs_workspace_bytes(T, V, top_n), dtype=torch.uint8))
+                    ws=f(L.rl_logprobs_workspace_bytes(T, V, top_n), dtype=torch.uint8), bits=bits)
+
+
+def _head_rows(model: Model, head: Head, T: int) -> None:
+    if T > head.q.shape[0] or head.q.shape[1] != model.w.hidden:
+        raise ValueError(f"a step of {T} tokens of {model.w.hidden}: the head holds {tuple(head.q.shape)}")
+
+
+def enqueue_logits(head: Head, y: torch.Tensor, T: int) -> torch.Tensor:
+    """head.logits[:T] = head(RMSNorm(y)), y [T][H]."""
+    H, V = head.q.shape[1], head.logits.shape[1]
+    q, q_scale, logits = head.q[:T], head.q_scale[:T], head.logits[:T]
+    L.rl_add_rmsnorm(y, T, H, EPS, gain=head.gain, q=q, scale=q_scale, group=head.group)
+    if head.bits == 8:
+        L.rl_f8_matmul(head.w, head.scale, q, q_scale, logits, T, V, H)
+    else:
+        L.rl_q4_matvec(head.w, head.scale, q, logits, T, V, H, head.group, x_scale=q_scale)
+    return logits
+
+
+def _enqueue_logprobs(head: Head, logits: torch.Tensor, T: int, targets: torch.Tensor) -> None:
+    V = logits.shape[1]
+    top = (0, None, None) if head.top_ids is None else (head.top_ids.shape[1], head.top_ids[:T], head.top_logprob[:T])
+    L.rl_logprobs(logits, T, V, targets, head.logprob[:T], head.entropy[:T], *top, head.ws, head.ws.numel())
 
 
 def enqueue_verify(model: Model, b: TokensBuffers, head: Head, x_in: torch.Tensor, y_out: torch.Tensor,
@@ -347,18 +461,61 @@ def enqueue_verify(model: Model, b: TokensBuffers, head: Head, x_in: torch.Tenso
     head.logits = head(RMSNorm(y_out)) and the log probabilities of `targets` (int32 [T]), the
     entropies and the most probable tokens, in the head's first T rows, T being x_in's rows.  Valid when
     b.ctrl still reads (RL_NO_EARLY_OUT, 0)."""
-    T, H = _step_tokens(model, b, x_in, y_out), model.w.hidden
-    V = head.logits.shape[1]
-    if T > head.q.shape[0] or head.q.shape[1] != H:
-        raise ValueError(f"a step of {T} tokens of {H}: the head holds {tuple(head.q.shape)}")
+    T = _step_tokens(model, b, x_in, y_out)
+    _head_rows(model, head, T)
     if targets.dtype != torch.int32 or targets.numel() != T:
         raise ValueError(f"targets: {T} int32 values expected, got {targets.dtype} {tuple(targets.shape)}")
     enqueue_tokens(model, b, x_in, y_out)
-    q, q_scale, logits = head.q[:T], head.q_scale[:T], head.logits[:T]
-    L.rl_add_rmsnorm(y_out, T, H, EPS, gain=head.gain, q=q, scale=q_scale, group=head.group)
-    L.rl_q4_matvec(head.w, head.scale, q, logits, T, V, H, head.group, x_scale=q_scale)
-    top = (0, None, None) if head.top_ids is None else (head.top_ids.shape[1], head.top_ids[:T], head.top_logprob[:T])
-    L.rl_logprobs(logits, T, V, targets, head.logprob[:T], head.entropy[:T], *top, head.ws, head.ws.numel())
+    _enqueue_logprobs(head, enqueue_logits(head, y_out, T), T, targets)
+
+
+@dataclass
+class Sampler:
+    """How the next tokens are drawn: a setting per row and, for every step, a random number per row in
+    `uniform`.  Buffers for up to T tokens; a smaller step uses their first rows."""
+    uniform: torch.Tensor              # f32 [T], [0, 1): the caller fills it before each step
+    temperature: torch.Tensor          # f32 [T], 0: the most probable token
+    top_k: torch.Tensor | None         # int32 [T], 0: off
+    top_p: torch.Tensor | None         # f32 [T], 1: off
+    min_p: torch.Tensor | None         # f32 [T], 0: off
+    ids: torch.Tensor                  # int32 [T]: the tokens, -1 where a row has no distribution
+    logprob: torch.Tensor              # f32 [T]: their log probability among the tokens kept
+
+    @staticmethod
+    def make(T: int, device="cuda", temperature: float = 1.0, top_k: int | None = None, top_p: float | None = None,
+             min_p: float | None = None) -> "Sampler":
+        f = lambda v, dt=torch.float32: None if v is None else torch.full((T,), v, dtype=dt, device=device)  # noqa: E731
+        return Sampler(uniform=f(0.0), temperature=f(temperature), top_k=f(top_k, torch.int32), top_p=f(top_p),
+                       min_p=f(min_p), ids=f(0, torch.int32), logprob=f(0.0))
+
+
+def enqueue_sample(sampler: Sampler, logits: torch.Tensor) -> torch.Tensor:
+    """Draws the next token of each row of logits [T][V] into the sampler's first T rows; returns those of ids."""
+    T, V = logits.shape
+    if T > sampler.ids.shape[0]:
+        raise ValueError(f"{T} rows of logits: the sampler holds {sampler.ids.shape[0]}")
+    first = lambda t: None if t is None else t[:T]  # noqa: E731
+    ids = sampler.ids[:T]
+    L.rl_sample(logits, T, V, sampler.uniform[:T], ids, temperature=sampler.temperature[:T], top_k=first(sampler.top_k),
+                top_p=first(sampler.top_p), min_p=first(sampler.min_p), logprob=sampler.logprob[:T])
+    return ids
+
+
+def enqueue_generate(model: Model, b: TokensBuffers, head: Head, sampler: Sampler, x_in: torch.Tensor,
+                     y_out: torch.Tensor) -> torch.Tensor:
+    """A step of sequences decoded side by side: y_out as enqueue_tokens, head.logits = head(RMSNorm(y_out)), a token of each row
+    drawn by the sampler, and the model's own log probabilities of these tokens, entropies and most probable tokens in
+    the head's first T rows, as enqueue_verify writes them.  Returns the tokens (the sampler's first T ids).  Valid when b.ctrl
+    still reads (RL_NO_EARLY_OUT, 0)."""
+    T = _step_tokens(model, b, x_in, y_out)
+    _head_rows(model, head, T)
+    if T > sampler.ids.shape[0]:
+        raise ValueError(f"a step of {T} tokens: the sampler holds {sampler.ids.shape[0]}")
+    enqueue_tokens(model, b, x_in, y_out)
+    logits = enqueue_logits(head, y_out, T)
+    ids = enqueue_sample(sampler, logits)
+    _enqueue_logprobs(head, logits, T, ids)
+    return ids
 
 
 @dataclass
@@ -387,6 +544,7 @@ def run_bounded_decode_token(model: Model, b: DecodeBuffers, x_in: torch.Tensor,
     the next layer's router on this layer's input), and fill the absent experts of both, so
     that the restarted stack stops less often.  Results are unchanged; miss[l] then counts the
     misses the stack met after those fills."""
+    _routed_only(model, "run_bounded_decode_token")
     shp, K = model.shape, model.w.top_k
     b.ctrl.copy_(torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32))
     y_out.copy_(x_in)
@@ -488,6 +646,7 @@ def run_bounded_decode_token_device(model: Model, b: DecodeBuffers, x_in: torch.
     [1], accumulated) the experts filled.  Same results as run_bounded_decode_token.  The caller
     zeroes b.miss; b.ctrl is reset here; call model.sync_residency_from_device() before using
     the host mirror of the table."""
+    _routed_only(model, "run_bounded_decode_token_device")
     src, dst = model.device_fill_tables()
     b.ctrl.copy_(torch.tensor([RL_NO_EARLY_OUT, 0], dtype=torch.int32))
     y_out.copy_(x_in)
@@ -554,9 +713,14 @@ def enqueue_prefill_experts(model: Model, b: PrefillBuffers, layer: int, x: torc
                             stacked: bool, path: str = "tc") -> None:
     T, shp = x.shape[0], model.shape
     src = b.xn if stacked else x
+    shared = _shared(model, layer, T) if stacked else None
+    if shared is not None:
+        enqueue_shared_input(shared, x, T)
     L.rl_build_pairs(shp, layer, T, b.ids, b.offs, b.pair_tok, b.pair_k, b.ctrl)
     _experts_fn(path)(shp, layer, T, src, b.offs, b.pair_tok, b.pair_k, b.slots, b.weights, model.codebook, y,
                       1 if stacked else 0, b.ctrl, b.ws, b.ws.numel())
+    if shared is not None:
+        enqueue_shared(shared, layer, y, T, b.ctrl)
 
 
 @dataclass

@@ -126,3 +126,117 @@ def test_f8_gated(L, T, I, K):
     back = full(q, scale)
     assert torch.all((back - h2.double()).abs() <= h2.double().abs() * (2.0 ** -4 + 8 * U)
                      + 2.0 ** -10 * 1.001 * scale.double().repeat_interleave(128, 1)[:, :I])
+
+
+@pytest.mark.parametrize("T", [1, 20, 100, 300])
+def test_f8_broken_values_stay_in_their_row(L, T):
+    """NaN and infinite scales and an e4m3 NaN reach their own token's outputs only; the other rows keep their bits."""
+    N, K = 640, 400
+    g = torch.Generator().manual_seed(T)
+    x, xs = rows(T, K, g)
+    (w, ws), (wu, su) = matrix(N, K, g), matrix(N, K, g)
+    good, q, s = torch.empty(T, N, device="cuda"), torch.zeros(T, N, dtype=F8, device="cuda"), torch.zeros(T, 5, device="cuda")
+    L.rl_f8_matmul(w, ws, x, xs, good, T, N, K)
+    L.rl_f8_gated(w, ws, wu, su, x, xs, T, N, K, q=q, scale=s)
+    bad = torch.tensor(sorted({0, T // 2, T - 1}))
+    x2, xs2 = x.clone(), xs.clone()
+    xs2[bad[0], 1] = float("nan")
+    x2.view(torch.uint8)[bad[-1], 7] = 0x7F
+    if len(bad) > 2:
+        xs2[bad[1], 3] = float("inf")
+    y, q2, s2 = torch.empty_like(good), torch.ones_like(q), torch.ones_like(s)
+    L.rl_f8_matmul(w, ws, x2, xs2, y, T, N, K)
+    L.rl_f8_gated(w, ws, wu, su, x2, xs2, T, N, K, q=q2, scale=s2)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[bad] = False
+    assert torch.equal(y[rest], good[rest]) and torch.equal(s2[rest], s[rest])
+    assert torch.equal(q2.view(torch.uint8)[rest], q.view(torch.uint8)[rest])
+    assert not torch.isfinite(y[bad]).any()
+    assert torch.isnan(s2[bad]).all() and (q2.float()[bad] == 0).all()  # a group with a NaN or an infinity is marked
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_f8_zeros_and_extremes(L, T):
+    """Zero rows, zero scales and zero weights give zeros (scale 0, q 0); the type's largest values everywhere."""
+    N, K = 300, 256
+    z8 = lambda *s: torch.zeros(*s, device="cuda").to(F8)  # noqa: E731
+    one, big = torch.ones(T, 2, device="cuda"), torch.full((T, K), 448.0, device="cuda").to(F8)
+    w1, wbig = torch.ones(3, 2, device="cuda"), torch.full((N, K), 448.0, device="cuda").to(F8)
+    y = torch.full((T, N), 7.0, device="cuda")
+    q, s = torch.ones(T, N, dtype=F8, device="cuda"), torch.full((T, 3), 7.0, device="cuda")
+    for x, xs, w, ws in ((z8(T, K), one, wbig, w1), (big, 0 * one, wbig, w1), (big, one, z8(N, K), w1), (big, one, wbig, 0 * w1)):
+        L.rl_f8_matmul(w, ws, x, xs, y, T, N, K)
+        L.rl_f8_gated(w, ws, w, ws, x, xs, T, N, K, q=q, scale=s)
+        assert not y.any() and not s.any() and not q.float().any()
+    L.rl_f8_matmul(wbig, w1, big, one, y, T, N, K)
+    assert torch.equal(y, torch.full_like(y, 448.0 * 448.0 * K))  # exact in f32
+    # silu(v) v with v = 448^2 K up to f32's largest: finite, at the top of the type
+    L.rl_f8_gated(wbig, w1, wbig, w1, big, one, T, N, K, q=q, scale=s)
+    assert (q.float() == 448).all() and torch.isfinite(s).all()
+    # values near the smallest subnormal: 448 / max leaves f32's range
+    L.rl_f8_gated(wbig, w1, wbig, w1 * 1e-33, big, one * 1e-6, T, N, K, q=q, scale=s)
+    assert torch.isfinite(q.float()).all() and torch.isfinite(s).all() and (s > 0).all()
+    assert (q.float() > 400).all()
+
+
+def test_f8_rows_apart_from_16_bytes(L):
+    """Outputs and residuals at any element, sizes that no vector divides."""
+    g = torch.Generator().manual_seed(3)
+    for T, N, K in ((5, 129, 144), (200, 515, 144), (150, 513, 272)):
+        x, xs = rows(T, K, g)
+        w, ws = matrix(N, K, g)
+        ref, err = reference(x, xs, w, ws)
+        for dt in TYPES.values():
+            y = torch.zeros(T * N + 3, dtype=dt, device="cuda")[3:].view(T, N)
+            res = torch.randn(T * N + 1, generator=g).to(dt).cuda()[1:].view(T, N)
+            L.rl_f8_matmul(w, ws, x, xs, y, T, N, K, res=res)
+            close(y, ref + res.double(), err + (ref + res.double()).abs() * U, dt)
+
+
+@pytest.mark.parametrize("T", [2, 60, 140])
+def test_f8_skips_a_stopped_layer(L, T):
+    """ctrl[0] <= layer: nothing is written; above it the call runs.  No error bits either way."""
+    g = torch.Generator().manual_seed(T)
+    x, xs = rows(T, 256, g)
+    w, ws = matrix(300, 256, g)
+    ctrl = torch.tensor([5, 0], dtype=torch.int32, device="cuda")
+    y = torch.full((T, 300), 7.0, device="cuda")
+    q, s = torch.ones(T, 300, dtype=F8, device="cuda"), torch.full((T, 3), 7.0, device="cuda")
+    for layer in (5, 6):
+        L.rl_f8_matmul(w, ws, x, xs, y, T, 300, 256, layer=layer, ctrl=ctrl)
+        L.rl_f8_gated(w, ws, w, ws, x, xs, T, 300, 256, q=q, scale=s, layer=layer, ctrl=ctrl)
+    assert (y == 7).all() and (s == 7).all() and (q.float() == 1).all()
+    L.rl_f8_matmul(w, ws, x, xs, y, T, 300, 256, layer=4, ctrl=ctrl)
+    L.rl_f8_gated(w, ws, w, ws, x, xs, T, 300, 256, q=q, scale=s, layer=4, ctrl=ctrl)
+    ref, err = reference(x, xs, w, ws)
+    close(y, ref, err, torch.float32)
+    assert (s != 7).all() and ctrl.tolist() == [5, 0]
+
+
+@pytest.mark.parametrize("T", [1, 30, 300])
+def test_f8_graph_stream_and_neighbours(L, T):
+    """Captured and replayed on new rows; another stream; two calls side by side; the bytes behind the outputs."""
+    N, K = 1030, 512
+    g = torch.Generator().manual_seed(T)
+    w, ws = matrix(N, K, g)
+    x, xs = rows(T, K, g)
+    buf = torch.full((T * N + 64,), 7.0, device="cuda")
+    y = buf[:T * N].view(T, N)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ys = [torch.empty(T, N, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, out in zip((s1, s2), ys):
+        for _ in range(5):
+            L.rl_f8_matmul(w, ws, x, xs, out, T, N, K, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.rl_f8_matmul(w, ws, x, xs, y, T, N, K)
+    for k in range(3):
+        x2, xs2 = rows(T, K, g)
+        x.copy_(x2), xs.copy_(xs2)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, err = reference(x, xs, w, ws)
+        close(y, ref, err, torch.float32)
+    assert (buf[T * N:] == 7).all() and torch.equal(ys[0], ys[1])
