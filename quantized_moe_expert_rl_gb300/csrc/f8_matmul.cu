@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kG = 128;                       // values per scale
 constexpr int kTileBytes = 128 * kG;          // 128 rows of one block
-constexpr int kThreads = 320, kLoadW = 8, kMmaW = 9;
+constexpr int kThreads = 352, kLoadW = 8, kMmaW = 9, kPollW = 10;
 constexpr int kMaxCluster = 8;
 
 struct F8Args {
@@ -81,28 +81,30 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_peer(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
+}
+// The sum over the cluster's S CTAs, in rank order, of the four values at this shared-memory address in each; all loads are
+// on their way before the first is used (one after the other they cost 700 cycles each).
+__device__ __forceinline__ float4 sum_peers(uint32_t at, int S) {
+    float4 v[kMaxCluster];
+#pragma unroll
+    for (int p = 0; p < kMaxCluster; ++p) v[p] = p < S ? ld_peer4(peer_addr(at, p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 1; p < kMaxCluster; ++p)
+        if (p < S) v[0].x += v[p].x, v[0].y += v[p].y, v[0].z += v[p].z, v[0].w += v[p].w;
+    return v[0];
 }
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
 }
-// Barrier of the 256 promoting threads; true for all where any of them brought `pred`, so that they leave
-// together after a wait that ran out.
-__device__ __forceinline__ bool epi_sync(bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)pred)
-        : "memory");
+__device__ __forceinline__ void epi_sync() {  // the 256 promoting threads
+    asm volatile("bar.sync 1, 256;" ::: "memory");
     __syncwarp();
-    return r != 0u;
 }
 
 // The outputs of the gated form for 128 values of one row, lane L holding values 4 L .. 4 L + 3 of group g:
@@ -148,16 +150,24 @@ template <int TT, bool GATED>
 struct Rows {
     static constexpr int NA = GATED ? 2 : 1;
     static constexpr int kStage = NA * kTileBytes + TT * kG;
-    static constexpr int kStages = TT >= 128 || (GATED && TT >= 64) ? 4 : GATED ? 3 : 5;
+    static constexpr int kStages = GATED ? 3 : TT >= 128 ? 4 : 5;
     static constexpr int kBufs = NA * TT >= 128 ? 2 : 4;              // accumulators in tensor memory
     static constexpr int kCols = kBufs * NA * TT < 32 ? 32 : kBufs * NA * TT;
-    static constexpr int kScales = (TT + 4) * 4;                       // bytes per stage: xs of the tokens, ws
+    static constexpr int kScales = TT + 4;                             // floats per block: xs of the tokens, ws
+    // A slot's last block was released when the MMAs of the block kStages before are done and they followed the release
+    // of the one kBufs before those.
+    static constexpr int kSlots = 16;
+    static_assert(kSlots >= kStages + kBufs, "scales are not overwritten before their block is released");
     static constexpr int o_sc = 1024;
-    static constexpr int o_ring = (o_sc + kStages * kScales + 1023) / 1024 * 1024;
+    static constexpr int o_ring = (o_sc + kSlots * kScales * 4 + 1023) / 1024 * 1024;
     static constexpr int o_part = o_ring + kStages * kStage;           // f32 [NA][TT][128] (see below)
+    // A tile's sums go through shared memory, and a short loop makes the outputs: straight code that a CTA runs once costs
+    // 17 cycles an instruction (64 outputs, or 32 activations, per thread unrolled: 5 to 9 us).
+    static constexpr bool kStaged = GATED || TT >= 64;
     static constexpr size_t bytes(bool split) {
-        return o_part + (split ? NA * TT * 512 : GATED ? TT * 512 : 0);
+        return o_part + (split || kStaged ? NA * TT * 512 : 0);
     }
+    static_assert(o_part + NA * TT * 512 <= 232448, "shared memory of one CTA");
 };
 
 // Tiles of 128 weight rows (of each matrix) x TT tokens.  With a cluster of S > 1 CTAs every CTA takes a
@@ -168,10 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     using R = Rows<TT, GATED>;
     constexpr int NA = R::NA, CW = TT / 2;  // columns per promoting warp
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *sc_full = full + 16, *sc_empty = full + 24;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + 8, *sc_full = full + 16;
     uint64_t *d_full = full + 32, *d_empty = full + 36, *fin = full + 40;
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
-    int *abort_s = reinterpret_cast<int *>(smem + 516);
+    int *abort_s = reinterpret_cast<int *>(smem + 516), *leave_s = reinterpret_cast<int *>(smem + 520);
     float *sc = reinterpret_cast<float *>(smem + R::o_sc);
     float *part = reinterpret_cast<float *>(smem + R::o_part);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -181,14 +191,13 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
             mbar_init(&sc_full[i], 32);
-            mbar_init(&sc_empty[i], 8);
         }
         for (int i = 0; i < R::kBufs; ++i) {
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], 8);
         }
         mbar_init(fin, 1);
-        *abort_s = 0;
+        *abort_s = *leave_s = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -205,13 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     const int rank = S > 1 ? (int)cluster_rank() : 0;
     const int first = S > 1 ? blockIdx.x / S : blockIdx.x, step = gridDim.x / S;
     const int kb0 = (int)((long long)a.KB * rank / S), kb1 = (int)((long long)a.KB * (rank + 1) / S);
+    const uint32_t blocks = first < a.tiles ? (uint32_t)((a.tiles - 1 - first) / step + 1) * (uint32_t)(kb1 - kb0) : 0u;
     bool failed = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_spin_warp(bar, parity)) {
-            if (lane == 0) atomicExch(abort_s, 1);
-            failed = true;
-        }
-        return !failed;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {  // of one thread
+        for (uint32_t i = 0; i < kSpinPolls; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        atomicExch(abort_s, 1);
+        failed = true;
+        return false;
     };
 
     if (skip) {
@@ -222,11 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
             const int tn = tile % a.tiles_n, t0 = tile / a.tiles_n * TT;
             for (int kb = kb0; kb < kb1; ++kb, ++n) {
                 const int s = n % R::kStages;
-                if (n >= (uint32_t)R::kStages) {
-                    const uint32_t par = (n / R::kStages - 1) & 1;
-                    if (!wait(&empty[s], par) || !wait(&sc_empty[s], par)) break;
-                }
-                if (lane == 0) {
+                if (lane == 0 && (n < (uint32_t)R::kStages || wait(&empty[s], (n / R::kStages - 1) & 1))) {
                     uint8_t *st = smem + R::o_ring + s * R::kStage;
                     mbar_arrive_expect_tx(&full[s], R::kStage);
 #pragma unroll
@@ -234,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                     tma_load_2d(st + NA * kTileBytes, &a.xmap, kb * kG, t0, &full[s]);
                 }
                 __syncwarp();
-                const uint32_t dst = smem_addr(sc + s * (TT + 4));
+                failed = __any_sync(kFull, failed);
+                if (failed) break;
+                const uint32_t dst = smem_addr(sc + (n % R::kSlots) * R::kScales);
 #pragma unroll
                 for (int i = 0; i < (TT + 31) / 32; ++i) {
                     const int t = 32 * i + lane;
@@ -254,29 +262,42 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
             for (uint32_t j = n >= (uint32_t)R::kStages ? n - R::kStages : 0; j < n; ++j)
                 mbar_wait_warp(&full[j % R::kStages], (j / R::kStages) & 1);
     } else if (warp == kMmaW) {
-        const uint32_t idesc = tc::instr_desc(0u, 128, TT);
-        uint32_t n = 0;
-        for (int tile = first; tile < a.tiles && !failed; tile += step) {
-            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        if (lane == 0) {
+            const uint32_t idesc = tc::instr_desc(0u, 128, TT), ring = smem_addr(smem + R::o_ring);
+            for (uint32_t n = 0; n < blocks; ++n) {
                 const int s = n % R::kStages, b = n % R::kBufs;
-                if (n >= (uint32_t)R::kBufs && !wait(&d_empty[b], (n / R::kBufs - 1) & 1)) break;
                 if (!wait(&full[s], (n / R::kStages) & 1)) break;
+                if (n >= (uint32_t)R::kBufs && !wait(&d_empty[b], (n / R::kBufs - 1) & 1)) break;
                 tc::fence_after();
-                if (lane == 0) {
-                    const uint32_t st = smem_addr(smem + R::o_ring + s * R::kStage);
+                const uint32_t st = ring + s * R::kStage;
+                const uint64_t bd = tc::smem_desc_sw128(st + NA * kTileBytes, 1024);
 #pragma unroll
-                    for (int m = 0; m < NA; ++m) {
-                        const uint64_t ad = tc::smem_desc_sw128(st + m * kTileBytes, 1024);
-                        const uint64_t bd = tc::smem_desc_sw128(st + NA * kTileBytes, 1024);
+                for (int m = 0; m < NA; ++m) {
+                    const uint64_t ad = tc::smem_desc_sw128(st + m * kTileBytes, 1024);
 #pragma unroll
-                        for (int k = 0; k < kG / 32; ++k)
-                            tc::mma_f8(tmem + (b * NA + m) * TT, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-                    }
-                    tc::commit(&empty[s]);
-                    tc::commit(&d_full[b]);
+                    for (int k = 0; k < kG / 32; ++k)
+                        tc::mma_f8(tmem + (b * NA + m) * TT, ad + 2 * k, bd + 2 * k, idesc, k > 0);
                 }
-                __syncwarp();
+                tc::commit(&d_full[b]);
+                tc::commit(&empty[s]);
             }
+        }
+        __syncwarp();
+    } else if (warp == kPollW) {
+        // waits for each block's scales and product and lets the promoting warps pass the barrier of its buffer
+        // (id 2 + buffer); the next arrival there comes after they have released the buffer
+        for (uint32_t n = 0; n < blocks; ++n) {
+            const int s = n % R::kStages, b = n % R::kBufs;
+            bool ok = true;
+            if (lane == 0 && (!wait(&sc_full[s], (n / R::kStages) & 1) || !wait(&d_full[b], (n / R::kBufs) & 1))) {
+                ok = false;
+                *reinterpret_cast<volatile int *>(leave_s) = 1;
+                __threadfence_block();
+            }
+            __syncwarp();
+            ok = __all_sync(kFull, ok);
+            asm volatile("bar.arrive %0, 288;" ::"r"(2 + b) : "memory");
+            if (!ok) break;
         }
     } else if (warp < 8) {
         const int qd = warp & 3, c0 = (warp >> 2) * CW;  // lane quadrant, first column
@@ -292,10 +313,16 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
 #pragma unroll
                 for (int j = 0; j < CW / 2; ++j) acc[m][j] = 0ull;
             for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                const int s = n % R::kStages, b = n % R::kBufs;
-                if (!wait(&sc_full[s], (n / R::kStages) & 1) || !wait(&d_full[b], (n / R::kBufs) & 1)) break;
+                const int b = n % R::kBufs;
+                asm volatile("bar.sync %0, 288;" ::"r"(2 + b) : "memory");
+                __syncwarp();
+                if (*reinterpret_cast<volatile int *>(leave_s)) {  // the same for all eight warps: set before the arrival
+                    failed = true;
+                    break;
+                }
                 tc::fence_after();
-                const uint32_t xa = smem_addr(sc + s * (TT + 4) + c0);
+                const float *ss = sc + (n % R::kSlots) * R::kScales;
+                const uint32_t xa = smem_addr(ss + c0);
                 constexpr int C = CW < 16 ? CW : 16;
 #pragma unroll
                 for (int c = 0; c < CW; c += C) {
@@ -314,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                     }
 #pragma unroll
                     for (int m = 0; m < NA; ++m) {
-                        const unsigned long long w2 = dup2(sc[s * (TT + 4) + TT + m]);
+                        const unsigned long long w2 = dup2(ss[TT + m]);
                         tc::ld_wait(d[m]);
 #pragma unroll
                         for (int j = 0; j < C; j += 2)
@@ -323,21 +350,41 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                 }
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&d_empty[b]);
-                    mbar_arrive(&sc_empty[s]);
-                }
+                if (lane == 0) mbar_arrive(&d_empty[b]);
                 __syncwarp();  // rejoin the warp (see cta_sync)
             }
-            if (GATED && S == 1) failed = epi_sync(failed);
             if (failed) break;
-            if (S > 1) {
+            if (S > 1 || R::kStaged) {
 #pragma unroll
                 for (int m = 0; m < NA; ++m)
 #pragma unroll
                     for (int j = 0; j < CW; ++j)
                         if (c0 + j < nt)
                             part[(m * TT + c0 + j) * 128 + row] = j & 1 ? hi2(acc[m][j / 2]) : lo2(acc[m][j / 2]);
+                if (S == 1) {
+                    epi_sync();
+                    if constexpr (!GATED) {
+                        const int col = tn * 128 + (tid & 127);
+                        if (col < a.N) {
+#pragma unroll 4
+                            for (int t = tid >> 7; t < nt; t += 2) {
+                                const size_t at = (size_t)(t0 + t) * a.N + col;
+                                float v = part[t * 128 + (tid & 127)];
+                                if (a.res) v += load1(a.res, at, a.dtype);
+                                store1(a.y, at, v, a.dtype);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int t = warp; t < nt; t += 8) {
+                            const float4 g = lds_f4(smem_addr(part + t * 128 + 4 * lane));
+                            const float4 u = lds_f4(smem_addr(part + (TT + t) * 128 + 4 * lane));
+                            float h[4] = {silu(g.x) * u.x, silu(g.y) * u.y, silu(g.z) * u.z, silu(g.w) * u.w};
+                            gated_store(a, t0 + t, tn, h);
+                        }
+                    }
+                    epi_sync();  // the sums are read before the next tile's are written
+                }
             } else if constexpr (!GATED) {
                 const int col = tn * 128 + row;
                 if (col < a.N) {
@@ -350,19 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                             store1(a.y, at, v, a.dtype);
                         }
                     }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < CW; ++j) {
-                    const float g = j & 1 ? hi2(acc[0][j / 2]) : lo2(acc[0][j / 2]);
-                    const float u = j & 1 ? hi2(acc[NA - 1][j / 2]) : lo2(acc[NA - 1][j / 2]);
-                    if (c0 + j < nt) part[(c0 + j) * 128 + row] = silu(g) * u;
-                }
-                epi_sync(false);
-                for (int t = warp; t < nt; t += 8) {
-                    const float4 v = lds_f4(smem_addr(part + t * 128 + 4 * lane));
-                    float h[4] = {v.x, v.y, v.z, v.w};
-                    gated_store(a, t0 + t, tn, h);
                 }
             }
         }
@@ -377,31 +411,25 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
             const int nt = a.T - t0 < TT ? a.T - t0 : TT;
             const uint32_t base = smem_addr(part);
             if constexpr (!GATED) {
-                for (int e = rank * kThreads + tid; e < nt * 128; e += S * kThreads) {
-                    const int t = e >> 7, col = tn * 128 + (e & 127);
-                    float v = 0.f;
-                    for (int p = 0; p < S; ++p) v += ld_peer(peer_addr(base + 4 * e, p));
-                    if (col < a.N) {
-                        const size_t at = (size_t)(t0 + t) * a.N + col;
-                        if (a.res) v += load1(a.res, at, a.dtype);
-                        store1(a.y, at, v, a.dtype);
+#pragma unroll 1
+                for (int e = rank * kThreads + tid; e < nt * 32; e += S * kThreads) {
+                    const int t = e >> 5, col = tn * 128 + 4 * (e & 31);
+                    const float4 f = sum_peers(base + 16 * e, S);
+                    const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (col + j < a.N) {
+                            const size_t at = (size_t)(t0 + t) * a.N + col + j;
+                            store1(a.y, at, a.res ? v[j] + load1(a.res, at, a.dtype) : v[j], a.dtype);
+                        }
                     }
                 }
             } else {
+#pragma unroll 1
                 for (int t = rank + S * warp; t < nt; t += S * (kThreads / 32)) {
-                    float h[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float g = 0.f, u = 0.f;
-                        const uint32_t at = base + 4 * (t * 128 + 4 * lane + j);
-                        for (int p = 0; p < S; ++p) {
-                            const uint32_t pa = peer_addr(at, p);
-                            g += ld_peer(pa);
-                            u += ld_peer(pa + 4 * TT * 128);
-                        }
-                        h[j] = silu(g) * u;
-                    }
-                    __syncwarp();
+                    const uint32_t at = base + 4 * (t * 128 + 4 * lane);
+                    const float4 g = sum_peers(at, S), u = sum_peers(at + 4 * TT * 128, S);
+                    float h[4] = {silu(g.x) * u.x, silu(g.y) * u.y, silu(g.z) * u.z, silu(g.w) * u.w};
                     gated_store(a, t0 + t, tn, h);
                 }
             }
