@@ -429,11 +429,10 @@ struct Sampler {
                 }
                 if (__any_sync(kFull, any)) sum += sum_in(weigh, v, over);
             }
-            bool some[EV];
-            if (!__any_sync(kFull, at_least(v, lo, some))) return;
             uint32_t in = 0u;
 #pragma unroll
-            for (int j = 0; j < EV; ++j) in |= some[j] ? 1u << j : 0u;
+            for (int j = 0; j < EV; ++j) in |= v[j] >= lo && v[j] <= hi ? 1u << j : 0u;
+            if (!__any_sync(kFull, in != 0u)) return;
             // beyond kCap the number does not matter: the list is not used
             if (in && *reinterpret_cast<volatile int *>(&sh.mine) <= kCap) {
 #pragma unroll 1
@@ -640,7 +639,7 @@ struct Sampler {
                 if (!by_k && tid == 0) {  // a bin or more to both sides
                     int b0 = (int)sh.klo, b1 = b0;
                     uint32_t in = sh.inside;
-                    for (int i = 0; i < 32 && in <= 64; ++i) {
+                    for (int i = 0; i < 8 && in <= 64; ++i) {
                         if (b0 > 0) --b0, in += cnt[b0], sh.above -= cnt[b0];
                         if (b1 < kCounts - 1) ++b1, in += cnt[b1];
                     }
@@ -649,24 +648,25 @@ struct Sampler {
                     sh.klo = b1, sh.khi = b0, sh.inside = in;  // higher bins hold smaller logits
                 }
                 cta_sync();
-                const uint32_t b = tid == 0 ? sh.klo : sh.khi, bottom = order_key(sh.bound), top = order_key(m);
+                const uint32_t b = warp == 0 ? sh.klo : sh.khi, bottom = order_key(sh.bound), top = order_key(m);
                 cta_sync();
-                if (tid == 0 || tid == 32) {
-                    // the smallest key whose bin is not beyond klo's, the largest whose bin is not before khi's
-                    uint32_t x0 = bottom, x1 = top;
+                if (warp < 2) {
+                    // warp 0: the smallest key whose bin is not beyond klo's; warp 1: the smallest whose bin is before khi's,
+                    // less one.  32 places of the range at a time.
+                    uint32_t x0 = bottom, x1 = warp == 0 ? top : top + 1u;
+                    const int limit = (int)__shfl_sync(kFull, b, 0) - warp;  // the first key with a bin of at most this
                     while (x0 < x1) {
-                        const uint32_t d = x1 - x0, mid = tid == 0 ? x0 + d / 2 : x1 - d / 2;
-                        const uint32_t bm = (uint32_t)bin(key_value(mid));
-                        if (tid == 0) {
-                            if (bm <= b) x1 = mid;
-                            else x0 = mid + 1;
-                        } else {
-                            if (bm >= b) x0 = mid;
-                            else x1 = mid - 1;
-                        }
+                        const uint32_t x = x0 + (uint32_t)((u64)(x1 - x0) * (uint32_t)lane >> 5);
+                        const unsigned in = __ballot_sync(kFull, bin(key_value(x)) <= limit);
+                        const int at = in ? __ffs(in) - 1 : 32;
+                        const uint32_t below = __shfl_sync(kFull, x, at > 0 ? at - 1 : 0), above = __shfl_sync(kFull, x, at & 31);
+                        if (at < 32) x1 = above;
+                        if (at > 0) x0 = below + 1u;
                     }
-                    if (tid == 0) sh.klo = x0;
-                    else sh.khi = x0;
+                    if (lane == 0) {
+                        if (warp == 0) sh.klo = x0;
+                        else sh.khi = x0 - 1u;
+                    }
                 }
                 __syncwarp();
                 cta_sync();
@@ -1069,8 +1069,9 @@ struct Sampler {
                 total += by_k ? 0ull : sh.mass[c];
             }
             // by top-k the list holds the k-th token (or all that have a weight); by top-p alone it may end too early
+            // (it does for certain where its tokens, at a weight of one each, do not add up to p of the sum)
             bool done = false;
-            if (n <= (uint32_t)kCap) {
+            if (n <= (uint32_t)kCap && (by_k || bound == low || (float)n >= p * (float)(total >> a.shift) * 0.999f)) {
                 if (rank == 0) border_of_list((int)n, 0u, 0ull, by_k ? k0 : 0, by_p, total, by_k, by_k || bound == low);
                 cluster_sync_all(a.C);
                 done = sh.found != 0;
