@@ -154,8 +154,9 @@ struct Rows {
     static constexpr int kBufs = NA * TT >= 128 ? 2 : 4;              // accumulators in tensor memory
     static constexpr int kCols = kBufs * NA * TT < 32 ? 32 : kBufs * NA * TT;
     static constexpr int kScales = TT + 4;                             // floats per block: xs of the tokens, ws
-    // A slot's last block was released when the MMAs of the block kStages before are done and they followed the release
-    // of the one kBufs before those.
+    // A slot's (and its barrier's) last block was released when the MMAs of the block kStages before are done, for they
+    // followed the release of the one kBufs before those.  A barrier per stage would not do: MMAs do not wait for
+    // scales, so a lane's arrival for the stage's next block could count for a block whose copies are still on their way.
     static constexpr int kSlots = 16;
     static_assert(kSlots >= kStages + kBufs, "scales are not overwritten before their block is released");
     static constexpr int o_sc = 1024;
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
         for (int i = 0; i < R::kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-            mbar_init(&sc_full[i], 32);
         }
+        for (int i = 0; i < R::kSlots; ++i) mbar_init(&sc_full[i], 32);
         for (int i = 0; i < R::kBufs; ++i) {
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], 8);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                                        t0 + t < a.T ? 4 : 0);
                 }
                 if (lane < NA) cp_async_ca<4>(dst + 4 * (TT + lane), a.ws[lane] + (size_t)tn * a.KB + kb, 4);
-                cp_async_arrive(&sc_full[s]);
+                cp_async_arrive(&sc_full[n % R::kSlots]);
                 __syncwarp();
             }
         }
@@ -287,9 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
         // waits for each block's scales and product and lets the promoting warps pass the barrier of its buffer
         // (id 2 + buffer); the next arrival there comes after they have released the buffer
         for (uint32_t n = 0; n < blocks; ++n) {
-            const int s = n % R::kStages, b = n % R::kBufs;
+            const int b = n % R::kBufs;
             bool ok = true;
-            if (lane == 0 && (!wait(&sc_full[s], (n / R::kStages) & 1) || !wait(&d_full[b], (n / R::kBufs) & 1))) {
+            if (lane == 0 && (!wait(&sc_full[n % R::kSlots], (n / R::kSlots) & 1) || !wait(&d_full[b], (n / R::kBufs) & 1))) {
                 ok = false;
                 *reinterpret_cast<volatile int *>(leave_s) = 1;
                 __threadfence_block();

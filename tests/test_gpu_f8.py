@@ -240,3 +240,22 @@ def test_f8_graph_stream_and_neighbours(L, T):
         ref, err = reference(x, xs, w, ws)
         close(y, ref, err, torch.float32)
     assert (buf[T * N:] == 7).all() and torch.equal(ys[0], ys[1])
+
+
+@pytest.mark.parametrize("T,N,K,calls", [(8, 60000, 2048, 400), (1, 2048, 512, 2000), (40, 20000, 1040, 300), (77, 10007, 1040, 300),
+                                         (200, 4096, 1024, 300)])
+def test_f8_repeats(L, T, N, K, calls):
+    """Many calls back to back, several tiles per CTA: the same bits every time, no error bits."""
+    g = torch.Generator().manual_seed(N)
+    x, xs = rows(T, K, g)
+    w, ws = matrix(N, K, g)
+    ctrl = torch.tensor([0x7FFFFFFF, 0], dtype=torch.int32, device="cuda")
+    first, y, odd = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    L.rl_f8_matmul(w, ws, x, xs, first, T, N, K, ctrl=ctrl)
+    for _ in range(calls):
+        y.fill_(7)
+        L.rl_f8_matmul(w, ws, x, xs, y, T, N, K, ctrl=ctrl)
+        odd += (y != first).sum()
+    ref, err = reference(x, xs, w, ws)
+    close(first, ref, err, torch.float32)
+    assert int(odd) == 0 and ctrl.tolist() == [0x7FFFFFFF, 0]
