@@ -459,11 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
 // each.  Two threads issue the MMAs of every other block: one needs about 1200 cycles for a block's two waits, four MMAs
 // and two commits beside the promoting warps, the tensor cores 512.
 constexpr int kWThreads = 640, kWEpi = 16, kWLoadW = 16, kWMmaW = 17 /* and 18 */, kWPollW = 19;
-constexpr int kWStages = 6, kWStage = 2 * kTileBytes;
+constexpr int kWStages = 4, kWStage = 2 * kTileBytes;
 constexpr int kWScales = 132, kWSlots = 16;                              // a block's scales: 128 tokens, the two halves' weights
 constexpr int kWoRing = 1024;
-constexpr int kWoOut = kWoRing + kWStages * kWStage;                    // per warp 32 x 9 floats
-constexpr int kWOutFloats = 32 * 9;
+constexpr int kWoOut = kWoRing + kWStages * kWStage;                    // per warp 32 x 33 floats
+constexpr int kWOutFloats = 32 * 33;
 constexpr int kWoTop = kWoOut + kWEpi * kWOutFloats * 4;                // gated: maxima of [4][128] row quarters
 constexpr int kWoSc = kWoTop + 4 * 128 * 4;
 constexpr size_t kWBytes = kWoSc + kWSlots * kWScales * 4;
@@ -487,47 +487,54 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// 32 values of each lane's row from column n on, the lanes' rows starting at t.  Through shared memory, so that a warp
+// stores 32 neighbouring values at a time, wherever rows start: pieces of 16 bytes straight from the lanes, 32 rows
+// apart, took 1.5 times as long (32768 f32 outputs of 4096 rows from K = 32: 288 us).
 template <typename E>
-__device__ __forceinline__ void put8_as(const F8Args &a, size_t at, float (&v)[8]) {
-    if (a.res) {
-        float e[8];
-        load8(static_cast<const E *>(a.res) + at, e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += e[i];
-    }
-    store8(static_cast<E *>(a.y) + at, v);
+__device__ __forceinline__ void put32_as(void *to, const float *stage, int N, int rows, size_t at) {
+    E *y = static_cast<E *>(to) + at;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, y += N) *y = from_float<E>(stage[r * 33]);
 }
-// 8 values of this lane's row t from column n on
-__device__ __forceinline__ void put8(const F8Args &a, float *stage, int t, int n, float (&v)[8], bool vec) {
-    if (vec && n + 8 <= a.N) {  // rows and pieces start at 16-byte boundaries
-        if (t < a.T) {
-            const size_t at = (size_t)t * a.N + n;
-            if (a.dtype == RL_F32) put8_as<float>(a, at, v);
-            else if (a.dtype == RL_F16) put8_as<__half>(a, at, v);
-            else put8_as<__nv_bfloat16>(a, at, v);
-        }
-        __syncwarp();
-        return;
-    }
-    // through shared memory, so that neighbouring lanes store neighbouring values
-    const int lane = threadIdx.x & 31, tb = t - lane, c = n + (lane & 7);
+// the same with a residual
+template <typename E>
+__device__ __forceinline__ void put32_res(void *to, const void *res, const float *stage, int N, int rows, size_t at) {
+    E *y = static_cast<E *>(to) + at;
+    const E *e = static_cast<const E *>(res) + at;
+    for (int r0 = 0; r0 < rows; r0 += 16) {  // the reads first: res may be y, so they would wait for the stores
+        float q[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) stage[lane * 9 + j] = v[j];
+        for (int r = 0; r < 16; ++r) q[r] = r0 + r < rows ? to_float(e[(size_t)(r0 + r) * N]) : 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (r0 + r < rows) y[(size_t)(r0 + r) * N] = from_float<E>(stage[(r0 + r) * 33] + q[r]);
+    }
+}
+template <bool RES>
+__device__ __forceinline__ void put32(const F8Args &a, float *stage, int t, int n, const unsigned long long (&v)[16]) {
+    const int lane = threadIdx.x & 31, rows = a.T - t < 32 ? a.T - t : 32;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 33 + 2 * j] = lo2(v[j]), stage[lane * 33 + 2 * j + 1] = hi2(v[j]);
     __syncwarp();
-#pragma unroll 2
-    for (int r = lane >> 3; r < 32; r += 4) {
-        if (tb + r < a.T && c < a.N) {
-            const size_t at = (size_t)(tb + r) * a.N + c;
-            float w = stage[r * 9 + (lane & 7)];
-            if (a.res) w += load1(a.res, at, a.dtype);
-            store1(a.y, at, w, a.dtype);
+    if (n + lane < a.N && rows > 0) {
+        const size_t at = (size_t)t * a.N + n + lane;
+        const float *mine = stage + lane;
+        if constexpr (RES) {
+            if (a.dtype == RL_F32) put32_res<float>(a.y, a.res, mine, a.N, rows, at);
+            else if (a.dtype == RL_F16) put32_res<__half>(a.y, a.res, mine, a.N, rows, at);
+            else put32_res<__nv_bfloat16>(a.y, a.res, mine, a.N, rows, at);
+        } else {
+            if (a.dtype == RL_F32) put32_as<float>(a.y, mine, a.N, rows, at);
+            else if (a.dtype == RL_F16) put32_as<__half>(a.y, mine, a.N, rows, at);
+            else put32_as<__nv_bfloat16>(a.y, mine, a.N, rows, at);
         }
     }
     __syncwarp();
 }
 
-// GATED: the 256 weight rows are 128 rows of the gate's matrix and the same 128 of the up matrix.
-template <bool GATED>
+// GATED: the 256 weight rows are 128 rows of the gate's matrix and the same 128 of the up matrix.  RES: a residual is added (a
+// variant of its own, because the registers of its loads slow the promotion down by 5% even where there is none).
+template <bool GATED, bool RES>
 __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     // full and d_empty: of the even CTA, for both; the others: of each CTA
@@ -609,7 +616,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
                     }
                     if (++s == kWStages) s = 0, par ^= 1;
                     if ((n & 7) == 0) {
-                        // the MMAs of block n - 6 are done, so block n - 8 and the ones before it were released
+                        // the MMAs of block n - 4 are done, so block n - 6 and the ones before it were released
                         while (mkb >= a.KB) mkb -= a.KB, mtile += step;
                         if (m < blocks) {
                             const int mt = mtile % tiles_t * 256 + 128 * rank, mj = mtile / tiles_t;
@@ -681,8 +688,6 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
         const uint32_t release = peer_addr(smem_addr(d_empty), 0);
         float *stage = reinterpret_cast<float *>(smem + kWoOut) + warp * kWOutFloats;
         float *top = reinterpret_cast<float *>(smem + kWoTop);
-        const int es = a.dtype == RL_F32 ? 4 : 2;
-        const bool vec = ((size_t)a.N * es) % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.res)) & 15) == 0;
         uint32_t n = 0;
         for (int tile = skip ? a.tiles : first; tile < a.tiles && !failed; tile += step) {
             const int t = tile % tiles_t * 256 + 128 * rank + row, j = tile / tiles_t;
@@ -722,12 +727,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
             if (failed) break;
             if constexpr (!GATED) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[2 * i] = lo2(acc[c >> 2][4 * (c & 3) + i]), v[2 * i + 1] = hi2(acc[c >> 2][4 * (c & 3) + i]);
-                    put8(a, stage, t, j * 256 + 64 * part + 8 * c, v, vec);
-                }
+                for (int r = 0; r < 2; ++r) put32<RES>(a, stage, t - lane, j * 256 + 64 * part + 32 * r, acc[r]);
             } else {
                 const int i0 = j * 128 + 32 * part;
                 float m = 0.f;
@@ -738,15 +738,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
                     if (i0 + 2 * i + 1 < a.N) m = max_abs_nan(m, h1);
                     acc[0][i] = pack2(__float_as_uint(h0), __float_as_uint(h1));
                 }
-                if (a.y) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[2 * i] = lo2(acc[0][4 * c + i]), v[2 * i + 1] = hi2(acc[0][4 * c + i]);
-                        put8(a, stage, t, i0 + 8 * c, v, vec);
-                    }
-                }
+                if (a.y) put32<false>(a, stage, t - lane, i0, acc[0]);
                 if (a.q) {
                     wide_sync();  // every warp has read the last tile's maxima
                     top[128 * part + row] = m;
@@ -856,7 +848,8 @@ rl_status run_wide(F8Args &a, const void *x, cudaStream_t s, const char *what) {
     const int per = GATED ? 128 : 256;
     a.tiles = (a.T + 255) / 256 * ((a.N + per - 1) / per);
     const int pairs = a.tiles < sm_count() / 2 ? a.tiles : sm_count() / 2;
-    return launch_cluster(f8_wide_kernel<GATED>, 2 * pairs, kWThreads, 2, kWBytes, s, what, a);
+    if (!GATED && a.res) return launch_cluster(f8_wide_kernel<false, true>, 2 * pairs, kWThreads, 2, kWBytes, s, what, a);
+    return launch_cluster(f8_wide_kernel<GATED, false>, 2 * pairs, kWThreads, 2, kWBytes, s, what, a);
 }
 
 // shared checks; 0 rows: nothing to do
