@@ -478,8 +478,8 @@ rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, int32_t V, c
  * their own token's outputs only.
  * ctrl (NULL: always runs): does nothing when ctrl[0] <= layer, as the other calls for a layer.  A bounded wait
  * that ran out sets RL_DEVERR_WAIT_TIMEOUT there.
- * w, x 16-byte aligned; scales 4-byte; y, res to their element (16-byte where N times their size is a
- * multiple of 16 is faster); y must not overlap w, x or the scales.  It may be captured in a CUDA graph.
+ * w, x 16-byte aligned; scales and ctrl 4-byte; y, res to their element; y must not overlap w, x or the scales.  It may
+ * be captured in a CUDA graph.
  */
 rl_status rl_f8_matmul(const uint8_t *w, const float *w_scale, int32_t N, int32_t K, const uint8_t *x,
                        const float *x_scale, int32_t T, const void *res, void *y, int32_t y_dtype, int32_t layer,
@@ -515,8 +515,9 @@ rl_status rl_f8_gated(const uint8_t *w_gate, const float *gate_scale, const uint
  * A temperature of 0 (or below, or NaN), and top_k = 1, take the first token of the order (logprob 0).  A row that holds
  * a NaN or +infinity, or nothing but -infinities, has no distribution: ids -1, logprob NaN.  Tokens at -infinity are
  * never drawn.
- * The sums are integer, in multiples of 2^-45 of the largest e (2^-(62 - ceil(log2 V)) beyond 2^17 tokens), so they depend
- * on no order; each e is good to 2^-30 of itself, then rounded to such a multiple (below one it is none).
+ * The sums are integer, in multiples of 2^-46 of the largest e (2^-(63 - ceil(log2 V)) beyond 2^17 tokens), so they depend
+ * on no order; each e is good to 2^-30 of itself, then off by at most one such multiple (below one it is none).  A token
+ * nearer to a border than that may fall on either side of it.
  * Temperatures below 8.5e-39 count as that, an infinite one as the largest f32.
  * logits [T][V] of `dtype` (RL_F32, RL_F16, RL_BF16), aligned to their element; uniform f32 [T]; temperature f32
  * [T] or NULL (1); top_k int32 [T], top_p f32 [T], min_p f32 [T], each or NULL (off); ids int32 [T]; logprob

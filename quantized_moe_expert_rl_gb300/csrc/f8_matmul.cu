@@ -13,6 +13,16 @@
 //   wide  many rows.  A operand: 256 activation rows over a pair of CTAs, B operand: 256 weight rows.  Lane =
 //         token, so that a lane's scale is one number per block.
 //
+// Up to 128 rows (64 in the gated form) take the first kernel.  Small matrices are split over clusters of up to 8 CTAs along the
+// shared dimension, so that one row of 512 x 2048 does not run through four CTAs alone.
+//
+// Measured back to back in a graph (us; the copy rate allows, where bytes bound): 1 row of 2048 x 512 4.6; 8 rows of 131072 x
+// 2048 48 (41: 85% of the copy rate); 77 rows of 10007 x 1040 9.5 (1.8; the latency of nine blocks, start and stores); 4096 rows
+// of 8192 x 8192 253, 2.17 PFLOP/s, 1.13 times what the cuBLAS bf16 product reaches; gated 512 x 2048: 1 row 5.2, 2048 rows
+// 14.5; gated 8192 x 4096, 4096 rows 278, 1.97 PFLOP/s.  The large products are bound by the way of a block from the end of its
+// MMAs over the waiting warp, the reads of tensor memory and the other CTA's arrival back to the issuing thread: two
+// accumulators of 256 columns fill tensor memory, so only one other block hides it (the tensor pipe is 44% busy).
+//
 // Both: the first 8 or 16 warps promote (warp w reads the lanes of quadrant w % 4, a share of the columns
 // each), one warp loads (tensor copies with the 128-byte swizzle, 4-byte asynchronous copies for the
 // scales), one thread of another issues the MMAs.

@@ -4,9 +4,9 @@
 // Order: logits descending, equal ones by index.  A token's place in it is the 64-bit key (order-preserving
 // logit above ~index), so that a border is one key and a token is kept when its key is not below.
 //
-//   w(l) = 2^((l - max) log2(e) / temperature), as an integer multiple of 2^-s (s = 45 for 2^17 tokens)
+//   w(l) = 2^((l - max) log2(e) / temperature), as an integer multiple of 2^-s (s = 46 for up to 2^17 tokens)
 //   top-k border: the k-th key;  top-p border: the first key at which the sum of w reaches p times that of
-//   all (of the k);  min-p border: logit max + temperature ln(min_p);  the highest of them counts
+//   all (of the k);  min-p border: the smallest logit whose w is min_p of the largest;  the highest of them counts
 //   the token: the first one in index order at which the sum of the kept w passes u times their total
 //
 // Why integers: whether a token next to a border is in, and which one u meets, must depend neither on the order
@@ -14,17 +14,27 @@
 // token about once).  w is good to 2^-30 of itself: the exponent is a pair of f32, its fraction's first five bits go
 // through a table of 2^(j / 32) (one entry per bank, so lookups never conflict), the rest through the series of e^x.
 //
-// A row is held by a cluster of up to 8 CTAs in shared memory and read from HBM once (rows beyond what
-// fits are read again in each pass).  Passes over it: the maximum; the sum of all w (top-p without top-k)
-// and the candidates above a bound that the border cannot lie below; the sums of the kept w per warp (a
-// warp holds neighbouring tokens); and the warp that holds the token goes through its share once more.
-//   bound for top-k: the k-th largest of the warps' largest logits (or, for larger k, the smallest of the
-//   warps' j-th largest lane maxima, j = k / warps);  for top-p: (1 - p) / V of the largest w, because all
-//   tokens below it together have less than 1 - p of the sum.
-// Up to 2048 candidates are sorted by one CTA (bitonic, in registers and through shared memory), which finds
-// the border on their running sum.  With more of them (flat rows, large k) the range of keys that holds the border is
-// narrowed by histograms of counts and sums, 2048 bins of equal width in the logit first and of equal width in the key
-// after that, until 2048 keys are left or a single logit, whose tokens have equal w and are counted off by index.
+// Few rows: a row is held by a cluster of up to 8 CTAs in shared memory and read from HBM once.  From as many rows as SMs
+// on, and for rows that do not fit, a pair of CTAs (one for short rows) streams a row in every pass; all but the first come
+// from L2 (512 rows of 131072: 294 us held, 192 streamed, since a cluster's barriers leave its SMs idle).  Passes: the
+// maximum; then, where nothing is filtered, the sums of w per warp (a warp holds neighbouring tokens), and the warp that
+// holds the token goes through its share once more.  With top-k or top-p:
+//   1. The candidates above a bound go into a list: for top-k the k-th largest of the warps' largest logits (for larger k the
+//      smallest of the warps' j-th largest lane maxima, j = k / warps), so that the k-th token is in it; for top-p alone the
+//      bound at three quarters of the warps, which a peaked row's share p lies above.  One CTA sorts up to 2048 of them (by
+//      counting the larger ones up to 128, else bitonic) and finds the border on their running sum; all kept tokens are in
+//      the list, whose w give the warps' sums.
+//   2. Where that does not hold the border (flat rows, large k): counts of the tokens in 2048 bins of the logit, of those above
+//      (1 - p) M' / V (all below together have less than 1 - p of the sum; M' is the sum of w of the warps' maxima).  For
+//      top-k the counts name the bin; for top-p an estimate from the bins' middles names a few bins, whose tokens are sorted
+//      while those above are summed up exactly, which also tells whether the estimate was right.
+//   3. Else (top-k and top-p with more than 2048 candidates; thousands of equal logits at the border; an estimate that missed): the
+//      range of keys is narrowed by histograms of counts and of 64-bit sums until 2048 keys are left or a single logit, whose
+//      tokens have equal w and are counted off by index.
+//
+// Measured back to back in a graph: 1 x 131072 f32 9.8 us greedy, 13 unfiltered, 20 with k = 50 and p = 0.9, 52 for a flat
+// row with p = 0.95; 512 x 131072 f32 181 unfiltered (the copy rate allows 40; a w takes some 25 instructions, and issue slots are
+// 39% used), 424 with p = 0.95 and a quarter of the rows flat (L2 passes, and one CTA sorting while the others wait).
 #include <math.h>
 
 #include "qdot.cuh"

@@ -1,7 +1,7 @@
 """rl_sample on the GPU against the definition in 64 bits.
 
-Bounds.  A kernel's weight e is good to 2^-30 of itself and is kept in multiples of 2^-45 of the largest, so a sum of
-weights is off by at most 2^-30 of itself + V 2^-45.  Where a border of the definition (a running sum against its
+Bounds.  A kernel's weight e is good to 2^-30 of itself and is kept in multiples of 2^-46 of the largest, so a sum of
+weights is off by at most 2^-30 of itself + V 2^-46 (V up to 2^17).  Where a border of the definition (a running sum against its
 target) is nearer than 2^-28 of the total, either side may be right, and the row is not compared; otherwise the token has
 to be the definition's.  A distance of exactly 0 is that of equal logits (weights of 1, sums and targets that are exact on both
 sides), and is compared.  The log probability is a sum of two f32 results: four half steps of each part."""
