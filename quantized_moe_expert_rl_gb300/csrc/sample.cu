@@ -1286,7 +1286,8 @@ rl_status run_sample(SampleArgs &a, int T, cudaStream_t s) {
     // pieces of 16 bytes of a row, one more where rows do not start on 16-byte boundaries
     const bool even = (size_t)a.V * sizeof(E) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
     const int pieces = even ? a.V / EV : (a.V + 2 * (EV - 1)) / EV;
-    // CTAs per row: 64 KB of it each; with few rows as many as still leave every thread a piece
+    // CTAs per row: held, 64 KB of it each, and with few rows as many as still leave every thread a piece; streamed (from as
+    // many rows as SMs on) two, whose waves are finer than one's (512 x 131072: 198 against 220 us, four 218)
     const int sms = sm_count();
     const bool streamed = T >= sms;
     a.C = streamed && pieces >= 16 * kThreads ? 2 : 1;
@@ -1295,7 +1296,7 @@ rl_status run_sample(SampleArgs &a, int T, cudaStream_t s) {
     a.shift = 63;
     for (int v = 1; v < a.V; v *= 2) --a.shift;  // the sum of V weights stays below 2^64
     if (a.shift > 46) a.shift = 46;
-    // 227 KB of shared memory per CTA: 24 pieces of 8 KB beside the lists
+    // 227 KB of shared memory per CTA: 22 times 8 KB of a row beside the lists (streamed rows of up to 32 KB are held too)
     if (a.per <= (streamed ? 4 : 22) * kThreads) return launch_sample<E, true>(a, T, s);
     return launch_sample<E, false>(a, T, s);
 }
