@@ -484,6 +484,9 @@ struct Sampler {
     // sh.found 0.
     __device__ __noinline__ void border_of_list(int n, uint32_t above, u64 above_mass, int k, bool by_p, u64 total, bool total_of_k, bool whole) {
         const int tid = threadIdx.x;
+        int have = 0;  // never more than the lists hold, whatever the caller counted
+        for (int c = 0; c < a.C; ++c) have += (int)sh.count[c];
+        n = min(n, have);
         for (int i = tid; i < n; i += kThreads) {
             int c = 0, at = i;
             while (at >= (int)sh.count[c]) at -= (int)sh.count[c++];
