@@ -178,7 +178,7 @@ __device__ __forceinline__ u64 share(float p, u64 total, bool up) {
 }
 
 // The steps of w(l) for two logits (packed f32 pairs); one logit is the same with both halves alike.  Valid for
-// t = (l - m) log2(e) / temperature in [-shift, 0], anything below (the callers leave that out).
+// t = (l - m) log2(e) / temperature in [-shift, 0]; anything else gives any value (the callers leave out what is below `least`).
 //   d + e = l - m exactly (two-sum);  k / 32 = t rounded (the magic sum leaves k in the low bits);  r = t - k / 32
 //   P = 2^32 (e^(r ln 2) - 1), |r| <= 1 / 64: the fifth term of the series is below 2^-39
 //   w = 2^(k / 32 + shift) (1 + P / 2^32), truncated and made odd, which is off by at most a unit to either side and not
@@ -1029,7 +1029,9 @@ struct Sampler {
         }
         const float p = sh.p;
         const bool greedy = !(fac.hi > 0.f) || k0 == 1, by_k = jth > 0, by_p = p < 1.f;
-        least = greedy ? m : fmaxf(m - (float)a.shift / fac.hi, -3.4028234e38f);
+        // rounded up (towards m): below it the integer weight's shift would pass 63 and wrap, and the logit next below the exact
+        // border may be several temperatures away from it
+        least = greedy ? m : fmaxf(__fsub_ru(m, __fdiv_rd((float)a.shift, fac.hi)), -3.4028234e38f);
         weigh.set(m, fac, a.shift, sh.table);
         u64 border = 0ull, total = 0ull;
         bool summed = false, in_list = false;  // the kept tokens' sums: above a run already; all of them are in the lists

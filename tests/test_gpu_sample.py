@@ -231,3 +231,24 @@ def test_sample_follows_the_distribution(L):
     got = torch.bincount(ids.long(), minlength=V).double()
     chi = float(((got - want) ** 2 / want).sum())
     assert chi < (V - 1) + 6 * math.sqrt(2 * (V - 1))
+
+
+def near_ties(m, T, V, seed):
+    """Rows of m and the 64 f32 values below it, in any order, m at least once."""
+    steps = [torch.tensor(m)]
+    for _ in range(64):
+        steps.append(torch.nextafter(steps[-1], torch.tensor(-math.inf)))
+    g = torch.Generator().manual_seed(seed)
+    x = torch.stack(steps)[torch.randint(0, 65, (T, V), generator=g)]
+    x[:, V // 3] = m
+    return x.cuda(), torch.rand(T, generator=g)
+
+
+@pytest.mark.parametrize("m", [1.0, 5.0, 20.0, 1000.0, 1e8, 1e-20, -20.0, 3e38])
+def test_sample_near_ties(L, m):
+    """Logits a few f32 steps apart and temperatures beside those steps: from all weights alike to the largest's alone, with the last
+    logit that has a weight anywhere between."""
+    heat = torch.cat([torch.logspace(-8, 0, 33), (abs(m) * torch.logspace(-9, -4, 61, dtype=torch.float64)).float()])
+    for i, kw in enumerate(({}, {"p": 0.9}, {"m": 0.01}, {"k": 400}, {"k": 300, "p": 0.8}, {"p": 0.99, "m": 1e-6})):
+        x, u = near_ties(m, len(heat), 1000, 31 * i + 7)
+        check(L, x, u, heat=heat, **kw)
