@@ -84,9 +84,11 @@ struct SampleArgs {
     int V, C, per, iters, shift;  // pieces of 16 bytes per CTA and per thread; w = multiples of 2^-shift
 };
 
-// log2(e) / temperature as hi + lo * pre (pre: 1, or 2^-24 where lo by itself would leave f32's normal range)
+// log2(e) / temperature as (hi + lo * pre) * s (pre: 1, or 2^-24 where lo by itself would leave f32's normal range).  s: 1, or 1 / 2
+// at temperatures that see no differences but those of logits near the largest f32, whose difference as such may be twice that:
+// there logits are halved before they are subtracted.
 struct Factor {
-    float hi, lo, pre;
+    float hi, lo, pre, s;
 };
 
 struct Shared {
@@ -154,6 +156,7 @@ __device__ __forceinline__ u64 make_key(uint32_t k, int idx) { return ((u64)k <<
 
 // log2(w) of a logit as a pair, for l <= m
 __device__ __forceinline__ void exponent(float l, float m, Factor c, float &t, float &t_lo) {
+    l *= c.s, m *= c.s;
     const float d = l - m, b = d + m, e = (l - b) + ((b - d) - m);  // d + e = l - m exactly (two-sum)
     t = d * c.hi;
     t_lo = fmaf(e, c.hi, fmaf(d * c.pre, c.lo, fmaf(d, c.hi, -t)));
@@ -179,12 +182,12 @@ __device__ __forceinline__ u64 share(float p, u64 total, bool up) {
 
 // The steps of w(l) for two logits (packed f32 pairs); one logit is the same with both halves alike.  Valid for
 // t = (l - m) log2(e) / temperature in [-shift, 0]; anything else gives any value (the callers leave out what is below `least`).
-//   d + e = l - m exactly (two-sum);  k / 32 = t rounded (the magic sum leaves k in the low bits);  r = t - k / 32
+//   d + e = s l - s m exactly (two-sum, -b in place of b);  k / 32 = t rounded (the magic sum leaves k in the low bits);  r = t - k / 32
 //   P = 2^32 (e^(r ln 2) - 1), |r| <= 1 / 64: the fifth term of the series is below 2^-39
 //   w = 2^(k / 32 + shift) (1 + P / 2^32), truncated and made odd, which is off by at most a unit to either side and not
 //   on the average (131072 truncations would sum up to 2^-30 of the largest w)
 struct Weigh {
-    u64 m, nm, hi, lo, pre;
+    u64 s, nm, hi, lo, pre;
     int sh;
     uint32_t table;
     static constexpr float kMagic = 393216.f;  // 1.5 * 2^18: sums with it are rounded to multiples of 1 / 32
@@ -200,7 +203,7 @@ struct Weigh {
         return d;
     }
     __device__ __forceinline__ void set(float max, Factor c, int shift, const int32_t *tab) {
-        m = both(max), nm = both(-max), hi = both(c.hi), lo = both(c.lo), pre = both(c.pre);
+        s = both(c.s), nm = both(-max * c.s), hi = both(c.hi), lo = both(c.lo), pre = both(c.pre);
         sh = 62 - shift + (__float_as_int(kMagic) >> 5);
         table = smem_addr(tab);
     }
@@ -213,7 +216,7 @@ struct Weigh {
     }
     __device__ __forceinline__ void pair(float l0, float l1, u64 &w0, u64 &w1) const {
         const u64 l = pack2(__float_as_uint(l0), __float_as_uint(l1)), neg = both(-1.f), magic = both(kMagic);
-        const u64 d = add2(l, nm), b = add2(d, m), e = add2(ffma2(b, neg, l), add2(ffma2(d, neg, b), nm));
+        const u64 d = ffma2(l, s, nm), nb = ffma2(d, neg, nm), e = add2(ffma2(l, s, nb), ffma2(add2(nb, d), neg, nm));
         const u64 kf = ffma2(d, hi, magic);
         u64 r = ffma2(d, hi, ffma2(kf, neg, magic));
         r = ffma2(mul2(d, pre), lo, ffma2(e, hi, r));
@@ -612,7 +615,7 @@ struct Sampler {
         cluster_sync_all(a.C);
         if (rank == 0) {
             // thread t has the bins Q t .. Q t + Q - 1
-            const float octaves = fac.hi / bin_scale, one = (float)(1ull << a.shift);
+            const float octaves = fac.hi * fac.s / bin_scale, one = (float)(1ull << a.shift);
             uint32_t n[Q], csum = 0u;
             float e[Q], esum = 0.f;
             for (int i = 0; i < Q; ++i) {
@@ -1031,7 +1034,8 @@ struct Sampler {
         const bool greedy = !(fac.hi > 0.f) || k0 == 1, by_k = jth > 0, by_p = p < 1.f;
         // rounded up (towards m): below it the integer weight's shift would pass 63 and wrap, and the logit next below the exact
         // border may be several temperatures away from it
-        least = greedy ? m : fmaxf(__fsub_ru(m, __fdiv_rd((float)a.shift, fac.hi)), -3.4028234e38f);
+        least = __fsub_ru(m * fac.s, __fdiv_rd((float)a.shift, fac.hi));
+        least = greedy ? m : fmaxf(fac.s < 1.f ? least + least : least, -3.4028234e38f);
         weigh.set(m, fac, a.shift, sh.table);
         u64 border = 0ull, total = 0ull;
         bool summed = false, in_list = false;  // the kept tokens' sums: above a run already; all of them are in the lists
@@ -1062,10 +1066,10 @@ struct Sampler {
             // Top-p: all tokens below w = (1 - p) M' / V together have less than 1 - p of the sum, M' being what the warps'
             // maxima alone add up to.
             float sum = 0.f;
-            for (int i = lane; i < warps; i += 32) sum += exp2f((sh.wtop[i] - m) * fac.hi);
+            for (int i = lane; i < warps; i += 32) sum += exp2f((sh.wtop[i] * fac.s - m * fac.s) * fac.hi);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            const float low_p = fmaxf(fminf(m + (log2f((1.f - p) * sum / (float)a.V) - 0.05f) / fac.hi, m), least);
+            const float low_p = fmaxf(fminf(m + (log2f((1.f - p) * sum / (float)a.V) - 0.05f) / (fac.hi * fac.s), m), least);
             __syncwarp();
             cta_sync();
             float bound = fmaxf(sh.bound, least), low = by_k ? bound : low_p;
@@ -1245,11 +1249,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             const float f = 2.f * frexpf(h, &ex), q = 1.44269504f / f;
             const float rest = (fmaf(-q, f, 1.44269504f) + 1.9259630e-8f) / f;
             const bool tiny = ex > 60;
+            sh.fac.s = ex > 100 ? 0.5f : 1.f;
+            if (ex > 100) --ex;
             sh.fac.hi = ldexpf(q, 1 - ex);
             sh.fac.lo = ldexpf(rest, 1 - ex + (tiny ? 24 : 0)) + (tiny ? ldexpf(ldexpf(q, 25 - ex) - ldexpf(sh.fac.hi, 24), 0) : 0.f);
             sh.fac.pre = tiny ? 5.9604644775390625e-8f : 1.f;
         } else {
-            sh.fac = Factor{0.f, 0.f, 0.f};
+            sh.fac = Factor{0.f, 0.f, 0.f, 1.f};
         }
         sh.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;
     }

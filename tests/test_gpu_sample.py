@@ -252,3 +252,26 @@ def test_sample_near_ties(L, m):
     for i, kw in enumerate(({}, {"p": 0.9}, {"m": 0.01}, {"k": 400}, {"k": 300, "p": 0.8}, {"p": 0.99, "m": 1e-6})):
         x, u = near_ties(m, len(heat), 1000, 31 * i + 7)
         check(L, x, u, heat=heat, **kw)
+
+
+def test_sample_huge_temperatures(L):
+    """Logits of both signs up to the largest f32, whose differences leave the type, at temperatures that keep them all."""
+    top = torch.finfo(torch.float32).max
+    g = torch.Generator().manual_seed(12)
+    heat = torch.tensor([1e35, 5e36, 1.07e37, 3e37, 1e38, top, math.inf, 2e38])
+    T, V = len(heat), 3000
+    u = torch.rand(T, generator=g)
+    x = (2 * torch.rand(T, V, generator=g) - 1) * top
+    x[:, 17], x[:, 2900] = top, -top
+    big = x.bfloat16()
+    big[torch.isinf(big)] = 1e38
+    for kw in ({}, {"p": 0.9}, {"p": 0.3}, {"k": 100}, {"k": 2500, "p": 0.7}, {"k": 2500}, {"m": 0.2}, {"p": 0.95, "m": 0.05}):
+        for rows in (x.cuda(), big.cuda()):
+            ids = check(L, rows, u, heat=heat.clamp(max=top), **kw)  # (an infinite temperature counts as the largest f32)
+            out = torch.full((T,), -7, dtype=torch.int32, device="cuda")
+            k, p, m = (None if n not in kw else torch.full((T,), kw[n], dtype=dt, device="cuda")
+                       for n, dt in (("k", torch.int32), ("p", torch.float32), ("m", torch.float32)))
+            L.rl_sample(rows, T, V, u.cuda(), out, temperature=heat.cuda(), top_k=k, top_p=p, min_p=m)
+            assert torch.equal(out, ids)
+    x, u = logits("broad", T, 5000, 3)  # differences that such temperatures do not see
+    check(L, x, u, heat=heat, p=0.6)
