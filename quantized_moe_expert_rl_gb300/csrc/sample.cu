@@ -244,7 +244,7 @@ struct Row {
     __device__ __forceinline__ int at(int it) const { return first + it * 32 * EV; }
     __device__ __forceinline__ bool inner(int i0) const { return i0 >= 0 && i0 <= V - EV; }
     static __device__ __noinline__ uint4 edge_of(const E *x, int V, int i0) {
-        E e[EV];
+        alignas(16) E e[EV];
 #pragma unroll
         for (int k = 0; k < EV; ++k) e[k] = i0 + k >= 0 && i0 + k < V ? x[i0 + k] : from_float<E>(-INFINITY);
         return *reinterpret_cast<const uint4 *>(e);
