@@ -202,7 +202,7 @@ struct LpTile {
         return l - (int)((reinterpret_cast<uintptr_t>(p + l) & 15) / sizeof(E));
     }
     static __device__ __forceinline__ uint4 edge(const E *p, int l, int h, int i0) {
-        E e[EV];
+        alignas(16) E e[EV];
 #pragma unroll
         for (int k = 0; k < EV; ++k) e[k] = i0 + k >= l && i0 + k < h ? p[i0 + k] : from_float<E>(-INFINITY);
         return *reinterpret_cast<const uint4 *>(e);

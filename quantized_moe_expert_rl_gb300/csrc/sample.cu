@@ -481,11 +481,10 @@ struct Sampler {
     }
 
     // Sorts the candidates of all lists (n <= kCap, all that they hold: every caller counts the keys that collect() takes) and
-    // finds the border: the k-th token of the order (k > 0)
-    // and the first at which the sum reaches p times `total` (of the k tokens' sum with k > 0), counted from
-    // `above` tokens and a sum of `above_mass` that lie before the candidates.  Leader CTA; the border goes to
-    // all CTAs.  whole: nothing that has a weight lies behind the candidates; else a sum that does not get there leaves
-    // sh.found 0.
+    // finds the border: the k-th token of the order (k > 0) and the first at which the sum reaches p times `total` (of the k
+    // tokens' sum with k > 0), counted from `above` tokens and a sum of `above_mass` that lie before the candidates.
+    // Leader CTA; the border goes to all CTAs.  whole: nothing that has a weight lies behind the candidates; else a sum that
+    // does not get there leaves sh.found 0.
     __device__ __noinline__ void border_of_list(int n, uint32_t above, u64 above_mass, int k, bool by_p, u64 total, bool total_of_k, bool whole) {
         const int tid = threadIdx.x;
         for (int i = tid; i < n; i += kThreads) {
