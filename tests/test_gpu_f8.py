@@ -259,3 +259,45 @@ def test_f8_repeats(L, T, N, K, calls):
     ref, err = reference(x, xs, w, ws)
     close(first, ref, err, torch.float32)
     assert int(odd) == 0 and ctrl.tolist() == [0x7FFFFFFF, 0]
+
+
+@pytest.mark.parametrize("T,N,K", [(1100, 20000, 272), (1100, 20000, 640), (600, 30001, 1040), (70, 45000, 400)])
+def test_f8_matmul_tiles_after_tiles(L, T, N, K):
+    """Three tiles and more for every CTA or pair, odd numbers of blocks: what is kept between blocks goes on across tiles."""
+    g = torch.Generator().manual_seed(N + K)
+    x, xs = rows(T, K, g)
+    w, ws = matrix(N, K, g)
+    ref, err = reference(x, xs, w, ws)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    L.rl_f8_matmul(w, ws, x, xs, y, T, N, K)
+    close(y, ref, err, torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,I,K,calls", [(600, 13000, 272, 60), (600, 13000, 640, 60), (300, 20001, 1040, 60), (2048, 512, 2048, 500),
+                                         (40, 22000, 400, 100), (1, 512, 2048, 1000)])
+def test_f8_gated_tiles_after_tiles(L, T, I, K, calls):
+    """The gated form over several tiles per CTA or pair, and called many times: right, and the same bits every time."""
+    g = torch.Generator().manual_seed(I + K)
+    x, xs = rows(T, K, g, spread=1.0)
+    (wg, sg), (wu, su) = matrix(I, K, g), matrix(I, K, g)
+    sg *= 4 / (xs.mean() * 60 * 1e-3 * K ** 0.5 * 3)  # gates of a few units
+    a, da = reference(x, xs, wg, sg)
+    b, db = reference(x, xs, wu, su)
+    ref = a * torch.sigmoid(a) * b
+    err = 1.1 * da * b.abs() + (a * torch.sigmoid(a)).abs() * db + 1.1 * da * db + 8 * U * ref.abs()  # as in test_f8_gated
+    h = torch.full((T, I), 7.0, device="cuda")
+    q, scale = torch.zeros(T, I, dtype=F8, device="cuda"), torch.full((T, blocks(I)), 7.0, device="cuda")
+    ctrl = torch.tensor([0x7FFFFFFF, 0], dtype=torch.int32, device="cuda")
+    L.rl_f8_gated(wg, sg, wu, su, x, xs, T, I, K, h=h, q=q, scale=scale, ctrl=ctrl)
+    close(h, ref, err, torch.float32)
+    top = torch.nn.functional.pad(h.double(), (0, -I % 128)).view(T, -1, 128).abs().amax(2)
+    assert torch.all((scale.double() - top / 448).abs() <= 2 * U * top / 448)
+    assert torch.all((full(q, scale) - h.double()).abs() <= h.double().abs() * (2.0 ** -4 + 8 * U)
+                     + 2.0 ** -10 * 1.001 * scale.double().repeat_interleave(128, 1)[:, :I])
+    odd = torch.zeros(1, dtype=torch.int64, device="cuda")
+    q1, s1 = torch.empty_like(q), torch.empty_like(scale)
+    for _ in range(calls):
+        q1.view(torch.uint8).fill_(1), s1.fill_(7)
+        L.rl_f8_gated(wg, sg, wu, su, x, xs, T, I, K, q=q1, scale=s1, ctrl=ctrl)
+        odd += (q1.view(torch.uint8) != q.view(torch.uint8)).sum() + (s1 != scale).sum()
+    assert int(odd) == 0 and ctrl.tolist() == [0x7FFFFFFF, 0]

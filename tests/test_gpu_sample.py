@@ -275,3 +275,17 @@ def test_sample_huge_temperatures(L):
             assert torch.equal(out, ids)
     x, u = logits("broad", T, 5000, 3)  # differences that such temperatures do not see
     check(L, x, u, heat=heat, p=0.6)
+
+
+@pytest.mark.parametrize("T,V,dt", [(200, 40001, "f32"), (170, 70001, "bf16")])
+def test_sample_many_long_rows(L, T, V, dt):
+    """More rows than SMs, each streamed by two CTAs: settings of their own, flat rows with top-p, many kept tokens."""
+    g = torch.Generator().manual_seed(V)
+    pick = lambda v: torch.tensor(v)[torch.randint(0, len(v), (T,), generator=g)]  # noqa: E731
+    for kind in ("peaked", "broad", "steps"):
+        x, u = logits(kind, T, V, T + V, TYPES[dt])
+        check(L, x, u, pick([0.0, 0.5, 1.0, 1.5]), pick([0, 1, 40, 5000, V // 2]).int(), pick([1.0, 0.4, 0.95]), pick([0.0, 0.05]))
+    x, u = logits("flat", T, V, 5, TYPES[dt])
+    check(L, x, u, p=0.95)
+    x, u = logits("broad", T, V, 6, TYPES[dt])
+    check(L, x, u, p=0.95)
