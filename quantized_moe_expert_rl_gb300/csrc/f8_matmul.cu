@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
         const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16) + c0;
         const int row = 32 * qd + lane;
         uint32_t n = 0;
-        for (int tile = first; tile < a.tiles; tile += step) {
+        for (int tile = first; tile < a.tiles && !failed; tile += step) {
             const int tn = tile % a.tiles_n, t0 = tile / a.tiles_n * TT;
             const int nt = a.T - t0 < TT ? a.T - t0 : TT;
             unsigned long long acc[NA][CW / 2];
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
             for (int m = 0; m < NA; ++m)
 #pragma unroll
                 for (int j = 0; j < CW / 2; ++j) acc[m][j] = 0ull;
-            for (int kb = kb0; kb < kb1 && !failed; ++kb, ++n) {
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
                 const int b = n % R::kBufs;
                 asm volatile("bar.sync %0, 288;" ::"r"(2 + b) : "memory");
                 __syncwarp();
@@ -364,12 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                 if (lane == 0) mbar_arrive(&d_empty[b]);
                 __syncwarp();  // rejoin the warp (see cta_sync)
             }
-            if (failed) {  // a wait ran out: this tile's outputs and the ones after it are NaN, also where there is no ctrl to tell
-#pragma unroll
-                for (int m = 0; m < NA; ++m)
-#pragma unroll
-                    for (int j = 0; j < CW / 2; ++j) acc[m][j] = dup2(__int_as_float(0x7fffffff));
-            }
+            if (failed) break;
             if (S > 1 || R::kStaged) {
 #pragma unroll
                 for (int m = 0; m < NA; ++m)
@@ -422,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     const bool bad = *reinterpret_cast<volatile int *>(abort_s) != 0;
     if (S > 1) {
         cluster_sync();
-        if (!skip) {  // (a CTA whose wait ran out left NaN as its sums)
+        if (!skip && !bad) {
             const int tn = first % a.tiles_n, t0 = first / a.tiles_n * TT;
             const int nt = a.T - t0 < TT ? a.T - t0 : TT;
             const uint32_t base = smem_addr(part);
@@ -543,25 +538,6 @@ __device__ __forceinline__ void put32(const F8Args &a, float *stage, int t, int 
             else if (a.dtype == RL_F16) put32_as<__half>(a.y, mine, a.N, rows, at);
             else put32_as<__nv_bfloat16>(a.y, mine, a.N, rows, at);
         }
-    }
-    __syncwarp();
-}
-
-// After a wait that ran out, as in f8_rows_kernel: NaN in the outputs of one row (of 256) and a quarter of the columns, in `tile` and the
-// CTA's tiles after it.
-template <bool GATED>
-__device__ __noinline__ void spoil_wide(const F8Args &a, int tile, int step, int row, int part) {
-    const int tiles_t = (a.T + 255) / 256, per = GATED ? 32 : 64;
-    for (; tile < a.tiles; tile += step) {
-        const int t = tile % tiles_t * 256 + row, j = tile / tiles_t;
-        if (t >= a.T) continue;
-        for (int i = 0; i < per; ++i) {
-            const int n = (j * 4 + part) * per + i;
-            const size_t at = (size_t)t * a.N + n;
-            if (n < a.N && a.y) store1(a.y, at, __int_as_float(0x7fffffff), a.dtype);
-            if (n < a.N && GATED && a.q) a.q[at] = 0;
-        }
-        if (GATED && a.q && part == 0) a.scale[(size_t)t * a.tiles_n + j] = __int_as_float(0x7fffffff);
     }
     __syncwarp();
 }
@@ -723,8 +699,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
         float *stage = reinterpret_cast<float *>(smem + kWoOut) + warp * kWOutFloats;
         float *top = reinterpret_cast<float *>(smem + kWoTop);
         uint32_t n = 0;
-        int tile = skip ? a.tiles : first;
-        for (; tile < a.tiles; tile += step) {
+        for (int tile = skip ? a.tiles : first; tile < a.tiles && !failed; tile += step) {
             const int t = tile % tiles_t * 256 + 128 * rank + row, j = tile / tiles_t;
             unsigned long long acc[2][16];
 #pragma unroll
@@ -808,7 +783,6 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
                 }
             }
         }
-        if (failed) spoil_wide<GATED>(a, tile, step, 128 * rank + row, part);
     }
     __syncwarp();
     __syncthreads();
