@@ -483,10 +483,13 @@ __device__ __forceinline__ void wide_sync() {  // the sixteen promoting warps
     asm volatile("bar.sync 1, 512;" ::: "memory");
     __syncwarp();
 }
-// Arrive on an mbarrier of the cluster, by its address there.  Release: the warp's reads of the block's scales come before
-// whatever follows from the arrival, such as the copies that overwrite their slot (a relaxed one was no faster).
+// Arrive on an mbarrier of the cluster, by its address there.  Relaxed: what it tells of are reads of tensor memory that
+// have returned their values, and it publishes no memory (as a release, 8192 x 8192 x 4096 takes 485 us in place of 253).
+// The reads of a block's scales are not ordered by it: they have returned before the warp's multiply-adds of that block
+// were issued, those before the next block's values were loaded into the same registers, and a slot of scales is written
+// again only after the release of the block three after its own.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // tma_load_2d into this CTA's shared memory, completing on the mbarrier `bar` of either CTA of the pair
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
