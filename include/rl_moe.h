@@ -477,7 +477,8 @@ rl_status rl_logprobs(const void *logits, int32_t dtype, int32_t T, int32_t V, c
  * shorter); any T >= 0; T <= 2^22, N <= 2^26, K <= 2^20.  An infinite or NaN scale and an e4m3 NaN in x reach
  * their own token's outputs only.
  * ctrl (NULL: always runs): does nothing when ctrl[0] <= layer, as the other calls for a layer.  A bounded wait
- * that ran out sets RL_DEVERR_WAIT_TIMEOUT there.
+ * that ran out sets RL_DEVERR_WAIT_TIMEOUT there; the outputs that it kept from being computed are NaN, so that a call
+ * without ctrl tells of it too.
  * w, x 16-byte aligned; scales and ctrl 4-byte; y, res to their element; y must not overlap w, x or the scales.  It may
  * be captured in a CUDA graph.
  */
@@ -494,7 +495,8 @@ rl_status rl_f8_matmul(const uint8_t *w, const float *w_scale, int32_t N, int32_
  *   them: scale NaN, q = 0).
  * w_gate, w_up e4m3 bytes [I][K]; their scales f32 [ceil(I / 128)][ceil(K / 128)]; x, x_scale, ctrl and the limits
  * as for rl_f8_matmul (I for N).  h [T][I] of h_dtype (RL_F32, RL_F16, RL_BF16) or NULL; q e4m3 bytes [T][I]
- * with scale f32 [T][ceil(I / 128)], or both NULL; one of the two is given.  The down projection reads (q, scale)
+ * with scale f32 [T][ceil(I / 128)], or both NULL; one of the two is given.  Outputs that a wait which ran out kept from
+ * being computed: h and scale NaN, q 0.  The down projection reads (q, scale)
  * through rl_f8_matmul where I is a multiple of 16.  q and scale 4-byte aligned, h to its element.
  */
 rl_status rl_f8_gated(const uint8_t *w_gate, const float *gate_scale, const uint8_t *w_up, const float *up_scale,

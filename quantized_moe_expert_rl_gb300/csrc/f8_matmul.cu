@@ -155,6 +155,23 @@ __device__ __forceinline__ void gated_store(const F8Args &a, int t, int g, float
     }
 }
 
+// After a wait that ran out: NaN as the outputs of rows t0 .. t0 + rows - 1 and columns n0 .. n0 + cols - 1 (gated: a group; its scale
+// NaN and q 0).  By the first `threads` threads.
+template <bool GATED>
+__device__ __noinline__ void spoil(const F8Args &a, int threads, int t0, int rows, int n0, int cols) {
+    for (int e = threadIdx.x; e < rows * cols && threadIdx.x < threads; e += threads) {
+        const int t = t0 + e / cols, n = n0 + e % cols;
+        if (t >= a.T || n >= a.N) continue;
+        const size_t at = (size_t)t * a.N + n;
+        if (a.y) store1(a.y, at, __int_as_float(0x7fffffff), a.dtype);
+        if (GATED && a.q) {
+            a.q[at] = 0;
+            if (n == n0) a.scale[(size_t)t * a.tiles_n + n0 / kG] = __int_as_float(0x7fffffff);
+        }
+    }
+    __syncwarp();
+}
+
 // ---- rows: 128 weight rows x TT tokens per tile -----------------------------------------------
 template <int TT, bool GATED>
 struct Rows {
@@ -193,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     uint64_t *d_full = full + 32, *d_empty = full + 36, *fin = full + 40;
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
     int *abort_s = reinterpret_cast<int *>(smem + 516), *leave_s = reinterpret_cast<int *>(smem + 520);
+    int *left_s = reinterpret_cast<int *>(smem + 524);  // the first tile without sums
     float *sc = reinterpret_cast<float *>(smem + R::o_sc);
     float *part = reinterpret_cast<float *>(smem + R::o_part);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -209,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
         }
         mbar_init(fin, 1);
         *abort_s = *leave_s = 0;
+        *left_s = 0x7fffffff;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -364,7 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
                 if (lane == 0) mbar_arrive(&d_empty[b]);
                 __syncwarp();  // rejoin the warp (see cta_sync)
             }
-            if (failed) break;
+            if (failed) {
+                *left_s = tile;  // the same of all eight warps
+                break;
+            }
             if (S > 1 || R::kStaged) {
 #pragma unroll
                 for (int m = 0; m < NA; ++m)
@@ -415,9 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1) f8_rows_kernel(const __grid_const
     __syncwarp();
     __syncthreads();
     const bool bad = *reinterpret_cast<volatile int *>(abort_s) != 0;
+    if (bad) {  // outputs that could not be computed are NaN, so that a call without ctrl tells of it too
+        int tile = *reinterpret_cast<volatile int *>(left_s);
+        if (S > 1 && tile < a.tiles) {
+            for (int e = tid; e < NA * TT * 128; e += kThreads) part[e] = __int_as_float(0x7fffffff);
+            __syncwarp();
+        }
+        if (S == 1)
+            for (; tile < a.tiles; tile += step) spoil<GATED>(a, kThreads, tile / a.tiles_n * TT, TT, tile % a.tiles_n * 128, 128);
+    }
     if (S > 1) {
         cluster_sync();
-        if (!skip && !bad) {
+        if (!skip) {
             const int tn = first % a.tiles_n, t0 = first / a.tiles_n * TT;
             const int nt = a.T - t0 < TT ? a.T - t0 : TT;
             const uint32_t base = smem_addr(part);
@@ -555,6 +586,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
     uint64_t *fin = full + 20, *sc_full = full + 21;
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + 512);
     int *abort_s = reinterpret_cast<int *>(smem + 516), *leave_s = reinterpret_cast<int *>(smem + 520);
+    int *left_s = reinterpret_cast<int *>(smem + 524);  // the first tile without sums
     float *sc = reinterpret_cast<float *>(smem + kWoSc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
@@ -571,6 +603,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
         for (int i = 0; i < 2; ++i) mbar_init(&sc_full[i], 32);
         mbar_init(fin, 2);
         *abort_s = *leave_s = 0;
+        *left_s = 0x7fffffff;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -737,7 +770,10 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
                     for (int i = 0; i < 8; ++i) acc[c >> 1][8 * (c & 1) + i] = ffma2(pack2(d[2 * i], d[2 * i + 1]), f, acc[c >> 1][8 * (c & 1) + i]);
                 }
             }
-            if (failed) break;
+            if (failed) {
+                *left_s = tile;  // the same of all sixteen warps
+                break;
+            }
             if constexpr (!GATED) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) put32<RES>(a, stage, t - lane, j * 256 + 64 * part + 32 * r, acc[r]);
@@ -790,6 +826,8 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
     __syncwarp();
     __syncthreads();
     if (*reinterpret_cast<volatile int *>(abort_s) != 0) {
+        for (int tile = *reinterpret_cast<volatile int *>(left_s); tile < a.tiles; tile += step)  // as in f8_rows_kernel
+            spoil<GATED>(a, 32 * kWEpi, tile % tiles_t * 256 + 128 * rank, 128, tile / tiles_t * (GATED ? 128 : 256), GATED ? 128 : 256);
         if (tid == 0 && a.ctrl) dev_error(a.ctrl, RL_DEVERR_WAIT_TIMEOUT);
         if (rank == 0 && lane == 0 && (warp == kWMmaW || warp == kWMmaW + 1)) {
             tc::commit_pair(fin);  // MMAs in flight end before tensor memory is given back

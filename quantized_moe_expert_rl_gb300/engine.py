@@ -438,7 +438,8 @@ def _head_rows(model: Model, head: Head, T: int) -> None:
 
 
 def enqueue_logits(head: Head, y: torch.Tensor, T: int) -> torch.Tensor:
-    """head.logits[:T] = head(RMSNorm(y)), y [T][H]."""
+    """head.logits[:T] = head(RMSNorm(y)), y [T][H].  The head does not depend on a layer, so it takes no control block: logits of an
+    8-bit head that a wait which ran out kept from being computed are NaN, for which rl_sample gives -1 and rl_logprobs NaN."""
     H, V = head.q.shape[1], head.logits.shape[1]
     q, q_scale, logits = head.q[:T], head.q_scale[:T], head.logits[:T]
     L.rl_add_rmsnorm(y, T, H, EPS, gain=head.gain, q=q, scale=q_scale, group=head.group)
