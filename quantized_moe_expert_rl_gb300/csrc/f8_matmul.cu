@@ -13,19 +13,26 @@
 //   wide  many rows.  A operand: 256 activation rows over a pair of CTAs, B operand: 256 weight rows.  Lane =
 //         token, so that a lane's scale is one number per block.
 //
-// Up to 128 rows (64 in the gated form) take the first kernel.  Small matrices are split over clusters of up to 8 CTAs along the
+// Up to 128 rows (64 in the gated form) take the first kernel.  Both sides of that, rows / wide, in us:
+//   8192 x 8192: 128 rows 23 / 42, 129 37 / 41, 384 72 / 42      10007 x 1040: 65 rows 9.5 / 10.1, 128 11.1 / 11.1, 129 14.7 / 11.0
+//   32768 x 2048: 64 rows 24 / 25, 128 29 / 26, 129 45 / 27      2048 x 512: 128 rows 6.8 / 8.0, 256 7.2 / 8.1, 384 8.4 / 8.1
+//   gated 8192 x 4096: 64 rows 19 / 30, 128 26 / 30, 129 47 / 31        gated 512 x 2048: 64 rows 7.7 / 18, 128 8.0 / 18, 256 15 / 15
+// A pass over the rows in the first kernel reads all weights, so the limit is where a second pass would begin; matrices with
+// fewer tiles than SMs would bear two or three (512 x 2048 and 65 gated rows: 18 where 8 would do).
+// Small matrices are split over clusters of up to 8 CTAs along the
 // shared dimension, so that one row of 512 x 2048 does not run through four CTAs alone.
 //
 // Measured back to back in a graph (us; the copy rate allows, where bytes bound): 1 row of 2048 x 512 4.6; 8 rows of 131072 x
-// 2048 48 (41: 85% of the copy rate); 77 rows of 10007 x 1040 9.5 (1.8; the latency of nine blocks, start and stores); 4096 rows
-// of 8192 x 8192 253, 2.17 PFLOP/s, 1.13 times what the cuBLAS bf16 product reaches; gated 512 x 2048: 1 row 5.2, 2048 rows
-// 14.5; gated 8192 x 4096, 4096 rows 278, 1.97 PFLOP/s.  The large products are bound by the way of a block from the end of its
+// 2048 47 to 50 (41: 82 to 87% of the copy rate); 77 rows of 10007 x 1040 9.5 to 10 (1.8; the latency of nine blocks, start and
+// stores); 4096 rows of 8192 x 8192 253, 2.17 PFLOP/s, 1.13 times what the cuBLAS bf16 product reaches; gated 512 x 2048: 1 row
+// 5.3, 2048 rows 14.6; gated 8192 x 4096, 4096 rows 281, 1.96 PFLOP/s.  The large products are bound by the way of a block from the end of its
 // MMAs over the waiting warp, the reads of tensor memory and the other CTA's arrival back to the issuing thread: two
-// accumulators of 256 columns fill tensor memory, so only one other block hides it (the tensor pipe is 44% busy).
+// accumulators of 256 columns fill tensor memory, so only one other block hides it (the tensor pipe is 45% busy).
 //
 // Both: the first 8 or 16 warps promote (warp w reads the lanes of quadrant w % 4, a share of the columns
 // each), one warp loads (tensor copies with the 128-byte swizzle, 4-byte asynchronous copies for the
-// scales), one thread of another issues the MMAs.
+// scales), one thread of another issues the MMAs (wide: a thread each of two others, every other block), one warp waits for the
+// promoting ones.
 #include "qdot.cuh"
 #include "row_types.cuh"
 #include "tc_desc.cuh"
@@ -532,8 +539,8 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
 }
 
 // 32 values of each lane's row from column n on, the lanes' rows starting at t.  Through shared memory, so that a warp
-// stores 32 neighbouring values at a time, wherever rows start: pieces of 16 bytes straight from the lanes, 32 rows
-// apart, took 1.5 times as long (32768 f32 outputs of 4096 rows from K = 32: 288 us).
+// stores 32 neighbouring values at a time, wherever rows start: 32768 f32 outputs of 4096 rows from K = 32 take 93 us, with
+// pieces of 16 bytes straight from the lanes, 32 rows apart, 288.
 template <typename E>
 __device__ __forceinline__ void put32_as(void *to, const float *stage, int N, int rows, size_t at) {
     E *y = static_cast<E *>(to) + at;

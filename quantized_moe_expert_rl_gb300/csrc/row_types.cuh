@@ -1,4 +1,4 @@
-// row_types.cuh - element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_logprobs):
+// row_types.cuh - element types of the row operators (rl_add_rmsnorm, rl_q4_matvec, rl_f8_matmul, rl_f8_gated, rl_logprobs, rl_sample):
 // 16-byte loads and stores of 8 values as f32, whatever the type in memory.
 #pragma once
 #include <cuda_fp8.h>

@@ -14,9 +14,10 @@
 // token about once).  w is good to 2^-30 of itself: the exponent is a pair of f32, its fraction's first five bits go
 // through a table of 2^(j / 32) (one entry per bank, so lookups never conflict), the rest through the series of e^x.
 //
-// Few rows: a row is held by a cluster of up to 8 CTAs in shared memory and read from HBM once.  From as many rows as SMs
-// on, and for rows that do not fit, a pair of CTAs (one for short rows) streams a row in every pass; all but the first come
-// from L2 (512 rows of 131072: 294 us held, 192 streamed, since a cluster's barriers leave its SMs idle).  Passes: the
+// Fewer rows than SMs: a row is held by a cluster of up to 8 CTAs in shared memory and read from HBM once; rows that do not fit
+// are streamed by the cluster in every pass.  From as many rows as SMs on, two CTAs (one for rows below 128 KB) stream a row in
+// every pass, all but the first from L2 (512 rows of 131072: 294 us held, 192 streamed, since a cluster's barriers leave its SMs
+// idle); rows of up to 32 KB are held there too.  Passes: the
 // maximum; then, where nothing is filtered, the sums of w per warp (a warp holds neighbouring tokens), and the warp that
 // holds the token goes through its share once more.  With top-k or top-p:
 //   1. The candidates above a bound go into a list: for top-k the k-th largest of the warps' largest logits (for larger k the
@@ -32,9 +33,11 @@
 //      range of keys is narrowed by histograms of counts and of 64-bit sums until 2048 keys are left or a single logit, whose
 //      tokens have equal w and are counted off by index.
 //
-// Measured back to back in a graph: 1 x 131072 f32 9.8 us greedy, 13 unfiltered, 20 with k = 50 and p = 0.9, 52 for a flat
-// row with p = 0.95; 512 x 131072 f32 181 unfiltered (the copy rate allows 40; a w takes some 25 instructions, and issue slots are
-// 39% used), 424 with p = 0.95 and a quarter of the rows flat (L2 passes, and one CTA sorting while the others wait).
+// Measured back to back in a graph: 1 x 131072 f32 9.7 us greedy, 12 unfiltered, 21 with k = 50 and p = 0.9; with p = 0.95 30 for
+// a peaked row and 50 for normally distributed logits; k = 5000 and p = 0.9 77 and 92; 76 to 190 where all logits are equal; 512 x
+// 131072 f32 182 unfiltered (the copy rate allows 40; the row's maximum parts the pass that loads from the one that weighs, so
+// neither HBM, 25%, nor the issue slots, 41%, are full), 428 with p = 0.95 and a quarter of the rows nearly flat (L2 passes, and one
+// CTA sorting while the others wait).  A batch takes as long as its slowest row.
 #include <math.h>
 
 #include "qdot.cuh"
