@@ -19,8 +19,8 @@
 //   gated 8192 x 4096: 64 rows 19 / 30, 128 26 / 30, 129 47 / 31        gated 512 x 2048: 64 rows 7.7 / 18, 128 8.0 / 18, 256 15 / 15
 // A pass over the rows in the first kernel reads all weights, so the limit is where a second pass would begin; matrices with
 // fewer tiles than SMs would bear two or three (512 x 2048 and 65 gated rows: 18 where 8 would do).
-// Small matrices are split over clusters of up to 8 CTAs along the
-// shared dimension, so that one row of 512 x 2048 does not run through four CTAs alone.
+// Small matrices are split over clusters of up to 8 CTAs along the shared dimension, so that one row of 512 x 2048 does not run
+// through four CTAs alone.
 //
 // Measured back to back in a graph (us; the copy rate allows, where bytes bound): 1 row of 2048 x 512 4.6; 8 rows of 131072 x
 // 2048 47 to 50 (41: 82 to 87% of the copy rate); 77 rows of 10007 x 1040 9.5 to 10 (1.8; the latency of nine blocks, start and

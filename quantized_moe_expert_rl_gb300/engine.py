@@ -41,8 +41,8 @@ def pack_f8(weight: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
 @dataclass
 class SharedExpert:
     """A gated feed-forward block in 8 bits that every token of a layer goes through, beside the routed experts:
-    x += down(silu(gate RMSNorm(x)) * (up RMSNorm(x))), with a weight of 1 for every token.  Buffers for up to T tokens; a smaller step uses their first
-    rows.  The blocks of several layers may share buffers (`like`)."""
+    x += down(silu(gate RMSNorm(x)) * (up RMSNorm(x))), with a weight of 1 for every token.  Buffers for up to T
+    tokens; a smaller step uses their first rows.  The blocks of several layers may share buffers (`like`)."""
     gate: tuple[torch.Tensor, torch.Tensor]  # e4m3 [I][H], f32 scales of blocks of 128 x 128
     up: tuple[torch.Tensor, torch.Tensor]
     down: tuple[torch.Tensor, torch.Tensor]  # e4m3 [H][I]
